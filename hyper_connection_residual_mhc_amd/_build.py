@@ -6,6 +6,8 @@ the measurement library the tests and the benchmark use:
 
 * libmhc_h_aggregate.so  (csrc/mhc_h_aggregate.hip, include/mhc_h_aggregate.h)
 * libmhc_coeff_bwd.so    (csrc/mhc_coeff_bwd.hip,   include/mhc_coeff_bwd.h)
+* libmhc_rms_norm.so     (csrc/mhc_rms_norm.hip,    include/mhc_rms_norm.h)
+* libmhc_post.so         (csrc/mhc_post.hip,        include/mhc_post.h)
 * libmhc_probes.so       (csrc/mhc_probes.hip,      csrc/mhc_probes.h;
                           not part of the operation)
 
@@ -49,28 +51,36 @@ import os
 import shutil
 import subprocess
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG_DIR = Path(__file__).resolve().parent
 REPO_DIR = PKG_DIR.parent
 SRC = PKG_DIR / "csrc" / "mhc_h_aggregate.hip"
 COEFF_SRC = PKG_DIR / "csrc" / "mhc_coeff_bwd.hip"
+NORM_SRC = PKG_DIR / "csrc" / "mhc_rms_norm.hip"
+POST_SRC = PKG_DIR / "csrc" / "mhc_post.hip"
 PROBE_SRC = PKG_DIR / "csrc" / "mhc_probes.hip"
 INCLUDE_DIR = REPO_DIR / "include"
 HEADER = INCLUDE_DIR / "mhc_h_aggregate.h"
 COEFF_HEADER = INCLUDE_DIR / "mhc_coeff_bwd.h"
+NORM_HEADER = INCLUDE_DIR / "mhc_rms_norm.h"
+POST_HEADER = INCLUDE_DIR / "mhc_post.h"
 LIB_DIR = PKG_DIR / "lib"
 LIB_PATH = LIB_DIR / "libmhc_h_aggregate.so"
 COEFF_LIB_PATH = LIB_DIR / "libmhc_coeff_bwd.so"
+NORM_LIB_PATH = LIB_DIR / "libmhc_rms_norm.so"
+POST_LIB_PATH = LIB_DIR / "libmhc_post.so"
 PROBE_LIB_PATH = LIB_DIR / "libmhc_probes.so"
 BUILD_DIR = REPO_DIR / "_build"
 
 # source -> library, header
 LIBRARIES = {SRC: (LIB_PATH, HEADER), COEFF_SRC: (COEFF_LIB_PATH, COEFF_HEADER),
+             NORM_SRC: (NORM_LIB_PATH, NORM_HEADER), POST_SRC: (POST_LIB_PATH, POST_HEADER),
              PROBE_SRC: (PROBE_LIB_PATH, PKG_DIR / "csrc" / "mhc_probes.h")}
 # source -> its own flags (see the module docstring)
 SOURCE_FLAGS = {SRC: ["-mllvm", "-amdgpu-kernarg-preload-count=16"], COEFF_SRC: [],
-                PROBE_SRC: []}
+                NORM_SRC: [], POST_SRC: [], PROBE_SRC: []}
 
 ARCH = "gfx950"
 
@@ -154,8 +164,11 @@ def _build_one(src: Path, lib: Path, extra_flags: list[str] | None) -> Path:
 def build_library(extra_flags: list[str] | None = None) -> Path:
     """Compile every shared library (always recompiles); returns the
     h_aggregate library's path."""
-    for src, (lib, _) in LIBRARIES.items():
-        _build_one(src, lib, extra_flags)
+    with ThreadPoolExecutor(max_workers=min(8, len(LIBRARIES))) as pool:
+        jobs = [pool.submit(_build_one, src, lib, extra_flags)
+                for src, (lib, _) in LIBRARIES.items()]
+        for job in jobs:
+            job.result()
     return LIB_PATH
 
 

@@ -1,6 +1,6 @@
-"""ctypes view of the C ABIs in include/mhc_h_aggregate.h and
-include/mhc_coeff_bwd.h, and of the measurement library (csrc/mhc_probes.h)
-that the tests and the benchmark use.
+"""ctypes view of the C ABIs in include/ (mhc_h_aggregate.h, mhc_coeff_bwd.h,
+mhc_rms_norm.h, mhc_post.h), and of the measurement library
+(csrc/mhc_probes.h) that the tests and the benchmark use.
 
 Loading fails loudly (ImportError) when a shared library has not been built,
 or was built from other sources than the ones in the tree (the digest
@@ -14,7 +14,8 @@ import ctypes
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_uint32, c_void_p
 
 from . import _build
-from ._build import COEFF_LIB_PATH, COEFF_SRC, LIB_PATH, PROBE_LIB_PATH, PROBE_SRC, SRC
+from ._build import (COEFF_LIB_PATH, COEFF_SRC, LIB_PATH, NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH,
+                     POST_SRC, PROBE_LIB_PATH, PROBE_SRC, SRC)
 
 MHC_SUCCESS = 0
 MHC_ERROR_INVALID_VALUE = 1
@@ -115,6 +116,39 @@ COEFF_SIGNATURES = {
 MHC_COEFF_F32, MHC_COEFF_BF16, MHC_COEFF_F16 = 0, 1, 2
 MHC_COEFF_SCRATCH_BYTES = 2 << 20
 
+MHC_NORM_ABI_VERSION = 1
+MHC_NORM_F32, MHC_NORM_BF16, MHC_NORM_F16 = 0, 1, 2
+MHC_NORM_SAME, MHC_NORM_E4M3_ROW, MHC_NORM_E4M3_MX = 0, 1, 2
+
+# Every symbol include/mhc_rms_norm.h declares.
+_NORM_FWD = [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_float, c_void_p, c_void_p,
+             c_void_p, c_void_p, c_int64, c_int64, c_int32, c_int32]
+_NORM_BWD = [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+             c_void_p, c_int64, c_int64, c_int64, c_int32]
+NORM_SIGNATURES = {
+    "mhc_rms_norm_abi_version": (c_int, []),
+    "mhc_rms_norm_last_error_message": (c_char_p, []),
+    "mhc_rms_norm_bwd_workspace_bytes": (c_int64, [c_int64, c_int64]),
+    "mhc_rms_norm_fwd": (c_int, _NORM_FWD + [c_void_p] * 3),
+    "mhc_rms_norm_bwd": (c_int, _NORM_BWD + [c_void_p] * 3),
+    "mhc_rms_norm_validate_fwd": (c_int, _NORM_FWD),
+    "mhc_rms_norm_validate_bwd": (c_int, _NORM_BWD),
+}
+
+MHC_POST_ABI_VERSION = 1
+
+# Every symbol include/mhc_post.h declares.
+_POST_FWD = [c_void_p] * 5 + [c_int64, c_int32, c_int64]
+_POST_BWD = [c_void_p] * 9 + [c_int64, c_int32, c_int64]
+POST_SIGNATURES = {
+    "mhc_post_abi_version": (c_int, []),
+    "mhc_post_last_error_message": (c_char_p, []),
+    "mhc_post_fwd": (c_int, _POST_FWD + [c_void_p] * 3),
+    "mhc_post_bwd": (c_int, _POST_BWD + [c_void_p] * 3),
+    "mhc_post_validate_fwd": (c_int, _POST_FWD),
+    "mhc_post_validate_bwd": (c_int, _POST_BWD),
+}
+
 MHC_PROBE_ABI_VERSION = 2
 
 # Every symbol csrc/mhc_probes.h declares.
@@ -173,6 +207,18 @@ def coeff_lib() -> ctypes.CDLL:
                 MHC_COEFF_ABI_VERSION)
 
 
+def norm_lib() -> ctypes.CDLL:
+    """The norm library (loaded once). ImportError if missing or stale."""
+    return _get("norm", NORM_LIB_PATH, NORM_SRC, NORM_SIGNATURES, "mhc_rms_norm_abi_version",
+                MHC_NORM_ABI_VERSION)
+
+
+def post_lib() -> ctypes.CDLL:
+    """The write-back library (loaded once). ImportError if missing or stale."""
+    return _get("post", POST_LIB_PATH, POST_SRC, POST_SIGNATURES, "mhc_post_abi_version",
+                MHC_POST_ABI_VERSION)
+
+
 def probe_lib() -> ctypes.CDLL:
     """The measurement library (loaded once). ImportError if missing or stale."""
     return _get("probes", PROBE_LIB_PATH, PROBE_SRC, PROBE_SIGNATURES, "mhc_probe_abi_version",
@@ -196,6 +242,16 @@ def check(status: int) -> None:
 def check_coeff(status: int) -> None:
     if status != MHC_SUCCESS:
         raise MhcError(status, coeff_lib().mhc_coeff_last_error_message().decode())
+
+
+def check_norm(status: int) -> None:
+    if status != MHC_SUCCESS:
+        raise MhcError(status, norm_lib().mhc_rms_norm_last_error_message().decode())
+
+
+def check_post(status: int) -> None:
+    if status != MHC_SUCCESS:
+        raise MhcError(status, post_lib().mhc_post_last_error_message().decode())
 
 
 def check_probe(status: int) -> None:
