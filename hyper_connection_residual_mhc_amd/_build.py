@@ -7,6 +7,7 @@ the measurement library the tests and the benchmark use:
 * libmhc_h_aggregate.so  (csrc/mhc_h_aggregate.hip, include/mhc_h_aggregate.h)
 * libmhc_coeff_bwd.so    (csrc/mhc_coeff_bwd.hip,   include/mhc_coeff_bwd.h)
 * libmhc_rms_norm.so     (csrc/mhc_rms_norm.hip,    include/mhc_rms_norm.h)
+* libmhc_linear.so       (csrc/mhc_linear.hip,      include/mhc_linear.h)
 * libmhc_post.so         (csrc/mhc_post.hip,        include/mhc_post.h)
 * libmhc_probes.so       (csrc/mhc_probes.hip,      csrc/mhc_probes.h;
                           not part of the operation)
@@ -59,28 +60,32 @@ REPO_DIR = PKG_DIR.parent
 SRC = PKG_DIR / "csrc" / "mhc_h_aggregate.hip"
 COEFF_SRC = PKG_DIR / "csrc" / "mhc_coeff_bwd.hip"
 NORM_SRC = PKG_DIR / "csrc" / "mhc_rms_norm.hip"
+LINEAR_SRC = PKG_DIR / "csrc" / "mhc_linear.hip"
 POST_SRC = PKG_DIR / "csrc" / "mhc_post.hip"
 PROBE_SRC = PKG_DIR / "csrc" / "mhc_probes.hip"
 INCLUDE_DIR = REPO_DIR / "include"
 HEADER = INCLUDE_DIR / "mhc_h_aggregate.h"
 COEFF_HEADER = INCLUDE_DIR / "mhc_coeff_bwd.h"
 NORM_HEADER = INCLUDE_DIR / "mhc_rms_norm.h"
+LINEAR_HEADER = INCLUDE_DIR / "mhc_linear.h"
 POST_HEADER = INCLUDE_DIR / "mhc_post.h"
 LIB_DIR = PKG_DIR / "lib"
 LIB_PATH = LIB_DIR / "libmhc_h_aggregate.so"
 COEFF_LIB_PATH = LIB_DIR / "libmhc_coeff_bwd.so"
 NORM_LIB_PATH = LIB_DIR / "libmhc_rms_norm.so"
+LINEAR_LIB_PATH = LIB_DIR / "libmhc_linear.so"
 POST_LIB_PATH = LIB_DIR / "libmhc_post.so"
 PROBE_LIB_PATH = LIB_DIR / "libmhc_probes.so"
 BUILD_DIR = REPO_DIR / "_build"
 
 # source -> library, header
 LIBRARIES = {SRC: (LIB_PATH, HEADER), COEFF_SRC: (COEFF_LIB_PATH, COEFF_HEADER),
-             NORM_SRC: (NORM_LIB_PATH, NORM_HEADER), POST_SRC: (POST_LIB_PATH, POST_HEADER),
+             NORM_SRC: (NORM_LIB_PATH, NORM_HEADER),
+             LINEAR_SRC: (LINEAR_LIB_PATH, LINEAR_HEADER), POST_SRC: (POST_LIB_PATH, POST_HEADER),
              PROBE_SRC: (PROBE_LIB_PATH, PKG_DIR / "csrc" / "mhc_probes.h")}
 # source -> its own flags (see the module docstring)
 SOURCE_FLAGS = {SRC: ["-mllvm", "-amdgpu-kernarg-preload-count=16"], COEFF_SRC: [],
-                NORM_SRC: [], POST_SRC: [], PROBE_SRC: []}
+                NORM_SRC: [], LINEAR_SRC: [], POST_SRC: [], PROBE_SRC: []}
 
 ARCH = "gfx950"
 

@@ -1,5 +1,5 @@
 """ctypes view of the C ABIs in include/ (mhc_h_aggregate.h, mhc_coeff_bwd.h,
-mhc_rms_norm.h, mhc_post.h), and of the measurement library
+mhc_rms_norm.h, mhc_linear.h, mhc_post.h), and of the measurement library
 (csrc/mhc_probes.h) that the tests and the benchmark use.
 
 Loading fails loudly (ImportError) when a shared library has not been built,
@@ -14,8 +14,9 @@ import ctypes
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_uint32, c_void_p
 
 from . import _build
-from ._build import (COEFF_LIB_PATH, COEFF_SRC, LIB_PATH, NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH,
-                     POST_SRC, PROBE_LIB_PATH, PROBE_SRC, SRC)
+from ._build import (COEFF_LIB_PATH, COEFF_SRC, LIB_PATH, LINEAR_LIB_PATH, LINEAR_SRC,
+                     NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH, POST_SRC, PROBE_LIB_PATH, PROBE_SRC,
+                     SRC)
 
 MHC_SUCCESS = 0
 MHC_ERROR_INVALID_VALUE = 1
@@ -135,6 +136,41 @@ NORM_SIGNATURES = {
     "mhc_rms_norm_validate_bwd": (c_int, _NORM_BWD),
 }
 
+MHC_LINEAR_ABI_VERSION = 1
+MHC_LINEAR_BF16, MHC_LINEAR_F16, MHC_LINEAR_E4M3_ROW, MHC_LINEAR_E4M3_MX = 1, 2, 3, 4
+MHC_ACT_NONE, MHC_ACT_RELU, MHC_ACT_SILU, MHC_ACT_GELU = 0, 1, 2, 3
+MHC_LINEAR_MAX_K = 1 << 21
+MHC_LINEAR_ROWS, MHC_LINEAR_NARROW, MHC_LINEAR_SMALL, MHC_LINEAR_MEDIUM, MHC_LINEAR_LARGE = \
+    1, 2, 3, 4, 5
+
+
+class mhc_linear_launch(ctypes.Structure):
+    """Launch shape of the product (see the header): 0 in a field means
+    "policy chooses"."""
+    _fields_ = [("kernel", c_int32), ("splits", c_int32)]
+
+    def as_dict(self) -> dict:
+        return {name: int(getattr(self, name)) for name, _ in self._fields_}
+
+
+# Every symbol include/mhc_linear.h declares.
+_LINEAR_FWD = [c_void_p] * 9 + [c_int64] * 4 + [c_int32, c_int32]
+_LINEAR_BWD = [c_void_p] * 8 + [c_int64] * 4 + [c_int32, c_int32]
+LINEAR_SIGNATURES = {
+    "mhc_linear_abi_version": (c_int, []),
+    "mhc_linear_last_error_message": (c_char_p, []),
+    "mhc_linear_plan": (c_int, [c_int64, c_int64, c_int64, c_int32, POINTER(mhc_linear_launch),
+                                POINTER(mhc_linear_launch)]),
+    "mhc_linear_fwd_workspace_bytes": (c_int64, [c_int64, c_int64, c_int64, c_int32,
+                                                 POINTER(mhc_linear_launch)]),
+    "mhc_linear_bwd_workspace_bytes": (c_int64, [c_int64, c_int64, c_int64, c_int32]),
+    "mhc_linear_fwd": (c_int, _LINEAR_FWD + [c_void_p, POINTER(mhc_linear_launch), c_void_p,
+                                             c_void_p]),
+    "mhc_linear_bwd": (c_int, _LINEAR_BWD + [c_void_p] * 3),
+    "mhc_linear_validate_fwd": (c_int, _LINEAR_FWD + [POINTER(mhc_linear_launch)]),
+    "mhc_linear_validate_bwd": (c_int, _LINEAR_BWD),
+}
+
 MHC_POST_ABI_VERSION = 1
 
 # Every symbol include/mhc_post.h declares.
@@ -213,6 +249,13 @@ def norm_lib() -> ctypes.CDLL:
                 MHC_NORM_ABI_VERSION)
 
 
+def linear_lib() -> ctypes.CDLL:
+    """The matrix-product library (loaded once). ImportError if missing or
+    stale."""
+    return _get("linear", LINEAR_LIB_PATH, LINEAR_SRC, LINEAR_SIGNATURES,
+                "mhc_linear_abi_version", MHC_LINEAR_ABI_VERSION)
+
+
 def post_lib() -> ctypes.CDLL:
     """The write-back library (loaded once). ImportError if missing or stale."""
     return _get("post", POST_LIB_PATH, POST_SRC, POST_SIGNATURES, "mhc_post_abi_version",
@@ -247,6 +290,11 @@ def check_coeff(status: int) -> None:
 def check_norm(status: int) -> None:
     if status != MHC_SUCCESS:
         raise MhcError(status, norm_lib().mhc_rms_norm_last_error_message().decode())
+
+
+def check_linear(status: int) -> None:
+    if status != MHC_SUCCESS:
+        raise MhcError(status, linear_lib().mhc_linear_last_error_message().decode())
 
 
 def check_post(status: int) -> None:

@@ -1,0 +1,1277 @@
+// mhc_linear.hip - matrix product with bias, activation and residual in its
+// epilogue, and its backward, for gfx950 (see include/mhc_linear.h for the
+// operation).
+
+#include "mhc_linear.h"
+
+#include <math.h>
+
+#include <type_traits>
+
+#include "mhc_host.h"
+#include "mhc_launch.h"
+#include "mhc_rows.h"
+
+#ifdef __FAST_MATH__
+#error "this source must not be built with fast-math"
+#endif
+
+#pragma clang fp contract(off)
+
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// What the operands of a product are. kE4M3 has its scales applied in the
+// epilogue, kMX in the matrix instruction.
+constexpr int kOpBF16 = MHC_LINEAR_BF16;
+constexpr int kOpF16 = MHC_LINEAR_F16;
+constexpr int kOpE4M3 = MHC_LINEAR_E4M3_ROW;
+constexpr int kOpMX = MHC_LINEAR_E4M3_MX;
+
+constexpr bool is8(int op) { return op == kOpE4M3 || op == kOpMX; }
+// Storage format of bias, residual, out and z.
+constexpr int out_format(int op) { return op == kOpF16 ? kF16 : kBF16; }
+
+// ---------------------------------------------------------------------------
+// Epilogue
+// ---------------------------------------------------------------------------
+
+// erfc(x) exp(x^2) for x >= 0 as a polynomial in t = 1 / (1 + 0.44 x) without
+// constant term, fitted for least relative error (7e-6 over [0, 14], far below
+// the 2^-9 of a bf16 and the 2^-12 of an fp16 result). `half_erfc_sqrt2` gives
+// erfc(a / sqrt 2) / 2 = the normal distribution's tail past a.
+__device__ __forceinline__ float half_erfc_sqrt2(float a) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.44f * 0.70710678f, a, 1.0f));
+  float q = -0.14439557f;
+  q = fmaf(q, t, 0.34594810f);
+  q = fmaf(q, t, 0.045597363f);
+  q = fmaf(q, t, 0.26124406f);
+  q = fmaf(q, t, 0.24308856f);
+  q = fmaf(q, t, 0.24851908f);
+  return 0.5f * q * t * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if constexpr (ACT == MHC_ACT_RELU) return v < 0.0f ? 0.0f : v;
+  if constexpr (ACT == MHC_ACT_SILU)
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+  if constexpr (ACT == MHC_ACT_GELU) {
+    // max(v, 0) - |v| tail(|v|); the tail is 0 from 30 on, where an infinite |v| would make 0 * inf
+    const float a = fminf(fabsf(v), 30.0f);
+    return (v < 0.0f ? 0.0f : v) - a * half_erfc_sqrt2(a);
+  }
+  return v;
+}
+
+// act'(v), for the backward.
+template <int ACT>
+__device__ __forceinline__ float slope(float v) {
+  if constexpr (ACT == MHC_ACT_RELU) return v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v);
+  if constexpr (ACT == MHC_ACT_SILU) {
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
+    return s * fmaf(v, 1.0f - s, 1.0f);
+  }
+  if constexpr (ACT == MHC_ACT_GELU) {
+    const float a = fminf(fabsf(v), 30.0f);
+    const float tail = half_erfc_sqrt2(a);
+    const float density = 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
+    return (v < 0.0f ? tail : 1.0f - tail) + (v < 0.0f ? -a : a) * density + (v - v) * 0.0f;
+  }
+  return 1.0f;
+}
+
+struct Epilogue {
+  const void* bias;
+  const void* residual;
+  void* out;
+  void* z;
+  const float* x_scales;       // kE4M3 only
+  const float* weight_scales;  // kE4M3 only
+  int64_t N;                   // row stride of residual, out and z
+  int32_t act;
+};
+
+// Columns [n, n + count) of row m, count <= 8, from the sums over k.
+template <int OP, int ACT>
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int64_t n, int count,
+                                       float (&v)[8]) {
+  constexpr int F = out_format(OP);
+  typedef typename Store<F>::type S;
+  float b[8];
+  if constexpr (OP == kOpE4M3) {
+    const float xs = e.x_scales[m];
+    widen_chunk<kF32>(load_chunk<kF32>(e.weight_scales + n, count), b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * (xs * b[i]);
+  }
+  if (e.bias != nullptr) {
+    widen_chunk<F>(load_chunk<F>(static_cast<const S*>(e.bias) + n, count), b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
+  }
+  Chunk<F> c;
+  if (e.z != nullptr) {
+    narrow_chunk<F>(v, c);
+    store_chunk<F>(static_cast<S*>(e.z) + m * e.N + n, count, c);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
+  if (e.residual != nullptr) {
+    widen_chunk<F>(load_chunk<F>(static_cast<const S*>(e.residual) + m * e.N + n, count), b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
+  }
+  narrow_chunk<F>(v, c);
+  store_chunk<F>(static_cast<S*>(e.out) + m * e.N + n, count, c);
+}
+
+// f with the activation as a constant.
+template <typename Fn>
+__device__ __forceinline__ void with_act(int32_t act, const Fn& f) {
+  switch (act) {
+    case MHC_ACT_RELU: f(std::integral_constant<int, MHC_ACT_RELU>()); break;
+    case MHC_ACT_SILU: f(std::integral_constant<int, MHC_ACT_SILU>()); break;
+    case MHC_ACT_GELU: f(std::integral_constant<int, MHC_ACT_GELU>()); break;
+    default: f(std::integral_constant<int, MHC_ACT_NONE>()); break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Matrix instructions
+// ---------------------------------------------------------------------------
+
+// Bytes of one row that one pass over the tiles in LDS covers: 64 values of 16
+// bits or 128 of 8.
+constexpr int kTileK = 128;
+
+// One operand's values of one matrix instruction, row l % 16 in lane l. 16
+// bits: 8 values from k = 8 (l / 16) on. 8 bits: 16 values from k = 16 (l / 16)
+// on and 16 from 64 + 16 (l / 16) on; the lane's scale byte is that of the 32
+// values from k = 32 (l / 16) on.
+template <int OP>
+struct Frag {
+  i32x4 w[is8(OP) ? 2 : 1];
+};
+
+// acc[i] of lane l: row 4 (l / 16) + i of `a` against row l % 16 of `b`. sa, sb:
+// the lane's e8m0 bytes (kMX).
+template <int OP>
+__device__ __forceinline__ f32x4 mma(const Frag<OP>& a, const Frag<OP>& b, f32x4 acc, int sa,
+                                     int sb) {
+  const i32x4 a0 = a.w[0], b0 = b.w[0];
+  if constexpr (OP == kOpBF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+        __builtin_bit_cast(bf16x8, a0), __builtin_bit_cast(bf16x8, b0), acc, 0, 0, 0);
+  } else if constexpr (OP == kOpF16) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(
+        __builtin_bit_cast(f16x8, a0), __builtin_bit_cast(f16x8, b0), acc, 0, 0, 0);
+  } else {
+    const i32x8 x = __builtin_shufflevector(a0, a.w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 y = __builtin_shufflevector(b0, b.w[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    // 0x7F is the scale 1
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0,
+                                                            OP == kOpMX ? sa : 0x7F, 0,
+                                                            OP == kOpMX ? sb : 0x7F);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tile kernel
+//
+// A block computes BM x BN outputs from tiles of x and W rows in LDS, kTileK
+// bytes of each row at a time, in two buffers: while one is multiplied the
+// next is loaded, straight into LDS where rows are 16-byte aligned (no
+// registers, no waits but one before the barrier), through registers where
+// they are not. A row's eight 16-byte pieces are stored at places that are
+// exchanged by its number (piece ^ swap(row)), so that the matrix
+// instructions' reads, 16 rows at the same k, spread over all banks.
+//
+// W's rows are the first operand of the matrix instruction and x's the second,
+// so a lane's four results are consecutive columns of one row; which W row
+// stands at which place is chosen (column()) so that over four tiles they are
+// 16 consecutive columns, which the epilogue moves in 16-byte accesses.
+// ---------------------------------------------------------------------------
+
+struct TileArgs {
+  const void* x;
+  const void* w;
+  const uint8_t* xs;  // kMX
+  const uint8_t* ws;  // kMX
+  int64_t M, N;
+  int64_t ldx, ldw;   // bytes from row to row
+  uint32_t kbytes;    // bytes of a row that count
+  uint32_t tiles_m, tiles_n;
+  uint32_t splits, per_split;  // parts of the sum, and tiles of kTileK in each
+  float* partial;              // [splits][M][N] where splits > 1
+  Epilogue e;
+};
+
+// Offset that lies past every buffer: such a lane loads zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+
+template <int V>
+constexpr int log2_of() {
+  return V <= 1 ? 0 : 1 + log2_of<V / 2>();
+}
+
+// How many consecutive tiles of 16 columns a lane's results run through.
+constexpr int group_of(int tj) { return tj < 4 ? tj : 4; }
+
+// The XOR of a row's pieces. SH = 3 is row % 8; the W rows that one
+// instruction reads are 4 consecutive ones out of every 2^SH.
+template <int SH>
+__device__ __forceinline__ uint32_t swap_of(uint32_t row) {
+  return (row & 3) | (((row >> SH) & 1) << 2);
+}
+
+// Loads ROWS rows x kTileK bytes into LDS.
+template <int ROWS, int THREADS, int SH, bool DMA, int ELEM>
+struct Loader {
+  static constexpr int Q = ROWS * 8 / THREADS;
+  static_assert(ROWS * 8 % THREADS == 0, "whole pieces for every thread");
+  const uint8_t* base;
+  i32x4 rsrc;
+  uint32_t offset[Q];  // row * ld + piece * 16, or kOutside
+  uint32_t piece[Q];   // the piece's place in the row, in bytes
+  i32x4 held[DMA ? 1 : Q];
+
+  __device__ __forceinline__ void init(const void* p, int64_t row0, int64_t rows, int64_t ld) {
+    const int64_t left = rows - row0;
+    const uint32_t here = static_cast<uint32_t>(left < ROWS ? left : ROWS);
+    base = static_cast<const uint8_t*>(p) + row0 * ld;
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    rsrc = i32x4{static_cast<int32_t>(b), static_cast<int32_t>(b >> 32),
+                 static_cast<int32_t>(here * static_cast<uint32_t>(ld)), kRsrcFormat};
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t id = q * THREADS + threadIdx.x;
+      const uint32_t row = id / 8;
+      piece[q] = ((id % 8) ^ swap_of<SH>(row)) * 16;
+      offset[q] = row < here ? row * static_cast<uint32_t>(ld) + piece[q] : kOutside;
+    }
+  }
+
+  // Starts the loads of the tile at byte k of every row into `to`.
+  __device__ __forceinline__ void start(uint32_t k, uint32_t kbytes, uint32_t to) {
+    if constexpr (DMA) {
+      const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const uint32_t at = k + piece[q] < kbytes ? offset[q] : kOutside;
+        const uint32_t dst = to + (q * THREADS + wave * 64) * 16;
+        // No register is written; the tile is waited for by wait_tiles().
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(dst), "v"(at), "s"(rsrc), "s"(k)
+                     : "memory");
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        held[q] = i32x4{0, 0, 0, 0};
+        if (offset[q] != kOutside && k + piece[q] < kbytes) {
+          const uint8_t* p = base + offset[q] + k;
+          const uint32_t left = kbytes - (k + piece[q]);
+          if constexpr (ELEM == 2) {
+            const Chunk<kBF16> c = load_chunk<kBF16>(reinterpret_cast<const uint16_t*>(p), left / 2 < 8 ? left / 2 : 8);
+            const u32x4 v = c.w[0];
+            held[q] = __builtin_bit_cast(i32x4, v);
+          } else if (left >= 16) {
+            typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
+            held[q] = *reinterpret_cast<const i32x4_at1*>(p);
+          } else {
+            uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (uint32_t i = 0; i < 16; ++i)
+              if (i < left) u[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+            held[q] = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
+                            static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
+          }
+        }
+      }
+    }
+  }
+
+  // Through registers: writes the loaded tile.
+  __device__ __forceinline__ void put(uint8_t* to) {
+    if constexpr (!DMA) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        *reinterpret_cast<i32x4*>(to + (q * THREADS + threadIdx.x) * 16) = held[q];
+    }
+  }
+};
+
+// Every load into LDS that this wave has started has arrived; then every
+// wave's has, and every wave is done with the other buffer.
+__device__ __forceinline__ void wait_tiles() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// e8m0 bytes of TILES rows of 16, for the tile at kTileK: one byte a lane.
+template <int TILES>
+struct Scales {
+  uint32_t offset[TILES];
+  uint32_t now[TILES], next[TILES];
+};
+
+template <int OP, int BM, int BN, int WM, int WN, bool DMA>
+__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
+  constexpr int kThreads = 64 * WM * WN;
+  constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
+  constexpr int G = group_of(TJ);
+  constexpr int SH = log2_of<4 * G>();
+  constexpr int ELEM = is8(OP) ? 1 : 2;
+  constexpr int kSteps = is8(OP) ? 1 : 2;
+  __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kTileK];
+
+  // Which tile: blocks go round the 8 XCDs, so consecutive tiles are given to
+  // every eighth block, and tiles run down 4 rows of tiles before the next
+  // column: the blocks of one XCD share rows of x and W in its L2.
+  const uint32_t tiles = a.tiles_m * a.tiles_n;
+  uint32_t id = blockIdx.x;
+  const uint32_t part = id / tiles;
+  id -= part * tiles;
+  {
+    const uint32_t each = tiles / 8, more = tiles % 8, xcd = id % 8, k = id / 8;
+    id = xcd * each + (xcd < more ? xcd : more) + k;
+  }
+  const uint32_t band = id / (4 * a.tiles_n);
+  const uint32_t high = min(4u, a.tiles_m - 4 * band);
+  id -= band * 4 * a.tiles_n;
+  const int64_t m0 = static_cast<int64_t>(4 * band + id % high) * BM;
+  const int64_t n0 = static_cast<int64_t>(id / high) * BN;
+
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const uint32_t wm = wave / WN, wn = wave % WN;
+
+  Loader<BM, kThreads, 2, DMA, ELEM> lx;
+  Loader<BN, kThreads, SH, DMA, ELEM> lw;
+  lx.init(a.x, m0, a.M, a.ldx);
+  lw.init(a.w, n0, a.N, a.ldw);
+
+  // Place of this lane's reads: x rows 16 apart, W rows 4 apart in a group.
+  const uint32_t xrow = wm * (TI * 16) + low;
+  const uint32_t wrow = wn * (TJ * 16) + (low / 4) * (4 * G) + low % 4;
+
+  Scales<OP == kOpMX ? TI : 1> sx;
+  Scales<OP == kOpMX ? TJ : 1> sw;
+  const uint32_t kblocks = (a.kbytes + 31) / 32;
+  if constexpr (OP == kOpMX) {
+    // rows past the end read the last row's scales: their values are zeros
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+      sx.offset[i] = static_cast<uint32_t>(min(m0 + xrow + 16 * i, a.M - 1) - m0) * kblocks + g;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      sw.offset[j] = static_cast<uint32_t>(
+          min(n0 + wrow + (j / G) * (16 * G) + (j % G) * 4, a.N - 1) - n0) * kblocks + g;
+  }
+  const uint8_t* xs = OP == kOpMX ? a.xs + m0 * kblocks : nullptr;
+  const uint8_t* ws = OP == kOpMX ? a.ws + n0 * kblocks : nullptr;
+  const auto start_scales = [&](uint32_t kt) {
+    if constexpr (OP == kOpMX) {
+      // past the last block of a row the values are zeros; any finite scale does
+      const uint32_t at = kt * 4 + g < kblocks ? kt * 4 : 0;
+      const bool in = kt * 4 + g < kblocks;
+#pragma unroll
+      for (int i = 0; i < TI; ++i) sx.next[i] = in ? xs[sx.offset[i] + at] : 0;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) sw.next[j] = in ? ws[sw.offset[j] + at] : 0;
+    }
+  };
+  // The scales are settled before the next tile's loads are started, so that
+  // waiting for them never waits for those.
+  const auto take_scales = [&]() {
+    if constexpr (OP == kOpMX) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        asm volatile("" : "+v"(sx.next[i]));
+        sx.now[i] = sx.next[i];
+      }
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        asm volatile("" : "+v"(sw.next[j]));
+        sw.now[j] = sw.next[j];
+      }
+    }
+  };
+
+  f32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  const auto multiply = [&](const uint8_t* tile) {
+    const uint8_t* tx = tile + xrow * kTileK;
+    const uint8_t* tw = tile + BM * kTileK + wrow * kTileK;
+    const uint32_t fx = swap_of<2>(low) * 16;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      Frag<OP> fw[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const uint32_t row = (j / G) * (16 * G) + (j % G) * 4;
+        const uint32_t f = swap_of<SH>(wrow + row) * 16;
+        const uint8_t* p = tw + row * kTileK;
+        if constexpr (is8(OP)) {
+          fw[j].w[0] = *reinterpret_cast<const i32x4*>(p + ((g * 16) ^ f));
+          fw[j].w[1] = *reinterpret_cast<const i32x4*>(p + ((64 + g * 16) ^ f));
+        } else {
+          fw[j].w[0] = *reinterpret_cast<const i32x4*>(p + ((s * 64 + g * 16) ^ f));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        Frag<OP> f;
+        const uint8_t* p = tx + i * 16 * kTileK;
+        if constexpr (is8(OP)) {
+          f.w[0] = *reinterpret_cast<const i32x4*>(p + ((g * 16) ^ fx));
+          f.w[1] = *reinterpret_cast<const i32x4*>(p + ((64 + g * 16) ^ fx));
+        } else {
+          f.w[0] = *reinterpret_cast<const i32x4*>(p + ((s * 64 + g * 16) ^ fx));
+        }
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+          acc[i][j] = mma<OP>(fw[j], f, acc[i][j], static_cast<int>(sw.now[OP == kOpMX ? j : 0]),
+                              static_cast<int>(sx.now[OP == kOpMX ? i : 0]));
+      }
+    }
+  };
+
+  const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
+  const uint32_t first = part * a.per_split;
+  const uint32_t last = min(all, first + a.per_split);
+  const uint32_t at0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)&lds[0][0]));
+  constexpr uint32_t kBuffer = (BM + BN) * kTileK;
+  sx.now[0] = sw.now[0] = 0;
+  if (first < last) {
+    lx.start(first * kTileK, a.kbytes, at0);
+    lw.start(first * kTileK, a.kbytes, at0 + BM * kTileK);
+    start_scales(first);
+  }
+  for (uint32_t kt = first; kt < last; ++kt) {
+    const uint32_t b = (kt - first) & 1;
+    lx.put(lds[b]);
+    lw.put(lds[b] + BM * kTileK);
+    take_scales();
+    wait_tiles();
+    if (kt + 1 < last) {
+      const uint32_t to = at0 + (b ^ 1) * kBuffer;
+      lx.start((kt + 1) * kTileK, a.kbytes, to);
+      lw.start((kt + 1) * kTileK, a.kbytes, to + BM * kTileK);
+      start_scales(kt + 1);
+    }
+    multiply(lds[b]);
+  }
+
+  // A lane's results: row `xrow` + 16 i of the tile, columns from wcol(j) on, 4G
+  // consecutive ones over the G tiles of a group.
+  const auto wcol = [&](int j) {
+    return wn * (TJ * 16) + (j / G) * (16 * G) + g * (4 * G) + (j % G) * 4;
+  };
+  float* partial = a.splits > 1 ? a.partial + static_cast<int64_t>(part) * a.M * a.N : nullptr;
+  const auto put = [&](auto act, int64_t m, int64_t n, int count, float(&v)[8]) {
+    if (partial != nullptr) {
+      Chunk<kF32> c;
+      narrow_chunk<kF32>(v, c);
+      store_chunk<kF32>(partial + m * a.N + n, count, c);
+    } else {
+      finish<OP, decltype(act)::value>(a.e, m, n, count, v);
+    }
+  };
+  if (m0 + BM <= a.M && n0 + BN <= a.N) {
+    // a whole tile, from the registers
+    with_act(partial != nullptr ? MHC_ACT_NONE : a.e.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; j += 2) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = acc[i][j][e];
+            v[4 + e] = acc[i][j + 1][e];
+          }
+          put(act, m0 + xrow + 16 * i, n0 + wcol(j), 8, v);
+        }
+    });
+    return;
+  }
+  // A tile at the edge: through LDS (each wave in its own part of it), so that
+  // the cases of a row's end are one loop and not TI * TJ / 2 copies.
+  constexpr int kWide = TJ * 16;
+  constexpr int kHalves = BM * BN * 4 > 2 * static_cast<int>(kBuffer) ? 2 : 1;
+  constexpr int kRows = TI * 16 / kHalves;
+  static_assert(TI % kHalves == 0 && BM * BN * 4 / kHalves <= 2 * static_cast<int>(kBuffer), "the results fit");
+  __syncthreads();  // every wave is done with the tiles
+  float* mine = reinterpret_cast<float*>(&lds[0][0]) + wave * (kRows * kWide);
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) {
+#pragma unroll
+    for (int i = 0; i < TI / kHalves; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        *reinterpret_cast<f32x4*>(mine + (16 * i + low) * kWide + wcol(j) - wn * kWide) =
+            acc[half * (TI / kHalves) + i][j];
+    __syncthreads();
+    for (uint32_t id = lane; id < kRows * kWide / 8; id += 64) {
+      const uint32_t row = id / (kWide / 8), col = id % (kWide / 8) * 8;
+      const int64_t m = m0 + wm * (TI * 16) + half * kRows + row;
+      const int64_t n = n0 + wn * kWide + col;
+      if (m < a.M && n < a.N) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = mine[row * kWide + col + e];
+        const int count = static_cast<int>(min(a.N - n, static_cast<int64_t>(8)));
+        with_act(partial != nullptr ? MHC_ACT_NONE : a.e.act,
+                 [&](auto act) { put(act, m, n, count, v); });
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The parts of a split sum, added in ascending order, and the epilogue.
+template <int OP>
+__global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ partial,
+                                                          uint32_t splits, int64_t M, Epilogue e) {
+  const int64_t chunks = (e.N + 7) / 8;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < M * chunks;
+       id += step) {
+    const int64_t m = id / chunks, n = (id - m * chunks) * 8;
+    const int count = static_cast<int>(min(e.N - n, static_cast<int64_t>(8)));
+    const float* p = partial + m * e.N + n;
+    float v[8], b[8];
+    widen_chunk<kF32>(load_chunk<kF32>(p, count), v);
+    for (uint32_t s = 1; s < splits; ++s) {
+      p += M * e.N;
+      widen_chunk<kF32>(load_chunk<kF32>(p, count), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
+    }
+    with_act(e.act, [&](auto act) { finish<OP, decltype(act)::value>(e, m, n, count, v); });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Up to 16 rows of x
+//
+// Bound by W's bytes: each is read once, straight into registers. A block
+// takes 16 rows of W; its waves take turns over the sum in units of kTileK
+// bytes of each row (4 units of a wave in flight), multiply them with x's rows
+// as the second operand (rows past M are zeros), and are joined through LDS in
+// ascending order.
+// ---------------------------------------------------------------------------
+
+struct RowsArgs {
+  const uint8_t* x;
+  const uint8_t* w;
+  const uint8_t* xs;  // kMX
+  const uint8_t* ws;  // kMX
+  int64_t M, N;
+  uint32_t kbytes;
+  Epilogue e;
+};
+
+template <int OP, bool FULL>
+__device__ __forceinline__ void load_unit(const uint8_t* row, bool in, uint32_t k, uint32_t kbytes,
+                                          uint32_t g, Frag<OP> (&f)[is8(OP) ? 1 : 2]) {
+  typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
+  typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    // piece p of the unit: the lane group's 16 bytes
+    const uint32_t at = k + p * 64 + g * 16;
+    i32x4 v = {0, 0, 0, 0};
+    if (in) {
+      if (FULL || at + 16 <= kbytes) {
+        if constexpr (is8(OP)) v = *reinterpret_cast<const i32x4_at1*>(row + at);
+        else v = *reinterpret_cast<const i32x4_at2*>(row + at);
+      } else {
+        uint32_t u[4] = {0, 0, 0, 0};
+        for (uint32_t i = 0; i < 16; i += is8(OP) ? 1 : 2) {
+          if (at + i < kbytes) {
+            const uint32_t b = is8(OP) ? row[at + i]
+                                       : *reinterpret_cast<const uint16_t*>(row + at + i);
+            const uint32_t word = i / 4, s = b << (8 * (i % 4));
+            u[0] |= word == 0 ? s : 0;
+            u[1] |= word == 1 ? s : 0;
+            u[2] |= word == 2 ? s : 0;
+            u[3] |= word == 3 ? s : 0;
+          }
+        }
+        v = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
+                  static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
+      }
+    }
+    if constexpr (is8(OP)) f[0].w[p] = v;
+    else f[p].w[0] = v;
+  }
+}
+
+template <int OP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
+  constexpr int kAhead = 4;
+  constexpr int kFrags = is8(OP) ? 1 : 2;
+  __shared__ float sums[WAVES][16][17];
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const bool in_w = n0 + low < a.N, in_x = low < a.M;
+  const uint8_t* w = a.w + (in_w ? n0 + low : 0) * a.kbytes;
+  const uint8_t* x = a.x + (in_x ? low : 0) * static_cast<int64_t>(a.kbytes);
+  const uint32_t kblocks = (a.kbytes + 31) / 32;
+  const uint8_t* ws = OP == kOpMX ? a.ws + (in_w ? n0 + low : 0) * kblocks : nullptr;
+  const uint8_t* xs = OP == kOpMX ? a.xs + (in_x ? low : 0) * static_cast<int64_t>(kblocks) : nullptr;
+  f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+
+  const uint32_t full = a.kbytes / kTileK, units = (a.kbytes + kTileK - 1) / kTileK;
+  uint32_t u = wave;
+  for (; u < full; u += WAVES * kAhead) {
+    Frag<OP> fw[kAhead][kFrags], fx[kAhead][kFrags];
+    int sw[kAhead], sx[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t at = u + k * WAVES;
+      const bool in = at < full;
+      load_unit<OP, true>(w, in && in_w, at * kTileK, a.kbytes, g, fw[k]);
+      load_unit<OP, true>(x, in && in_x, at * kTileK, a.kbytes, g, fx[k]);
+      sw[k] = sx[k] = 0;
+      if constexpr (OP == kOpMX) {
+        if (in) {
+          sw[k] = ws[at * 4 + g];
+          sx[k] = xs[at * 4 + g];
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int p = 0; p < kFrags; ++p)
+        acc[(k + p) % 2] = mma<OP>(fw[k][p], fx[k][p], acc[(k + p) % 2], sw[k], sx[k]);
+  }
+  if (full < units && wave == full % WAVES) {
+    Frag<OP> fw[kFrags], fx[kFrags];
+    load_unit<OP, false>(w, in_w, full * kTileK, a.kbytes, g, fw);
+    load_unit<OP, false>(x, in_x, full * kTileK, a.kbytes, g, fx);
+    int sw = 0, sx = 0;
+    if constexpr (OP == kOpMX) {
+      if (full * 4 + g < kblocks) {
+        sw = ws[full * 4 + g];
+        sx = xs[full * 4 + g];
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < kFrags; ++p) acc[p % 2] = mma<OP>(fw[p], fx[p], acc[p % 2], sw, sx);
+  }
+  // sums[wave][row of x][column]
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float s0 = acc[0][i], s1 = acc[1][i];
+    sums[wave][low][g * 4 + i] = s0 + s1;
+  }
+  __syncthreads();
+  const int64_t m = threadIdx.x / 2;
+  const uint32_t half = threadIdx.x % 2;
+  const int64_t n = n0 + half * 8;
+  if (threadIdx.x < 32 && m < a.M && n < a.N) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = sums[0][m][half * 8 + i];
+#pragma unroll
+      for (int k = 1; k < WAVES; ++k) v[i] = v[i] + sums[k][m][half * 8 + i];
+    }
+    const int count = static_cast<int>(min(a.N - n, static_cast<int64_t>(8)));
+    with_act(a.e.act, [&](auto act) { finish<OP, decltype(act)::value>(a.e, m, n, count, v); });
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+//
+// gz and the bias's sums come from one pass over grad_out and z; the two
+// products read their operands along the sum, so W, x and gz are laid out
+// transposed in the workspace first (rows padded with zeros to a multiple of 8,
+// so that every row is 16-byte aligned).
+// ---------------------------------------------------------------------------
+
+// gz = rnd(grad_out * act'(z)) where gz is given, and this block's rows of the
+// bias's sums where partial is: 512 columns to a block, 8 to a lane; each of
+// the four waves takes every fourth row, joined in ascending order.
+template <int F, int ACT>
+__global__ __launch_bounds__(256) void linear_gz_kernel(
+    const typename Store<F>::type* __restrict__ grad_out,
+    const typename Store<F>::type* __restrict__ z, typename Store<F>::type* __restrict__ gz,
+    float* __restrict__ partial, int64_t M, int64_t N, int64_t rows) {
+  __shared__ float sums[4][512];
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 512 + lane * 8;
+  const int64_t m0 = blockIdx.y * rows, m1 = min(M, m0 + rows);
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n < N) {
+    const int count = static_cast<int>(min(N - n, static_cast<int64_t>(8)));
+    for (int64_t m = m0 + wave; m < m1; m += 4) {
+      float v[8], s[8];
+      widen_chunk<F>(load_chunk<F>(grad_out + m * N + n, count), v);
+      if constexpr (ACT != MHC_ACT_NONE) {
+        widen_chunk<F>(load_chunk<F>(z + m * N + n, count), s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * slope<ACT>(s[i]);
+        Chunk<F> c;
+        narrow_chunk<F>(v, c);
+        store_chunk<F>(gz + m * N + n, count, c);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = sum[i] + v[i];
+    }
+  }
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sums[wave][lane * 8 + i] = sum[i];
+  __syncthreads();
+  for (int k = threadIdx.x; k < 512; k += 256) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 512 + k;
+    if (c < N)
+      partial[blockIdx.y * N + c] = ((sums[0][k] + sums[1][k]) + sums[2][k]) + sums[3][k];
+  }
+}
+
+// grad_bias[n] = the parts' sum in ascending order, rounded once (+0.0 of none).
+template <int F>
+__global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ partial,
+                                                          typename Store<F>::type* __restrict__ out,
+                                                          int64_t parts, int64_t N) {
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= N) return;
+  float s = 0.0f;
+#pragma unroll 8
+  for (int64_t k = 0; k < parts; ++k) s = s + partial[k * N + n];
+  out[n] = narrow<F>(s);
+}
+
+// out [C, ld] = in [R, C] transposed, 16-bit values, zeros from R to ld (a
+// multiple of 8). A block moves 64 x 64 through LDS.
+__global__ __launch_bounds__(256) void linear_transpose_kernel(const uint16_t* __restrict__ in,
+                                                               uint16_t* __restrict__ out,
+                                                               int64_t R, int64_t C, int64_t ld,
+                                                               uint32_t tiles_c) {
+  __shared__ uint16_t tile[64][66];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles_c) * 64;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x % tiles_c) * 64;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = q * 32 + threadIdx.x / 8, col = (threadIdx.x % 8) * 8;
+    Chunk<kBF16> c = zero_chunk<kBF16>();
+    if (r0 + row < R && c0 + col < C)
+      c = load_chunk<kBF16>(in + (r0 + row) * C + c0 + col,
+                            static_cast<int>(min(C - c0 - col, static_cast<int64_t>(8))));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      tile[row][col + i] = static_cast<uint16_t>(c.w[0][i / 2] >> (16 * (i % 2)));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int col = q * 32 + threadIdx.x / 8, row = (threadIdx.x % 8) * 8;
+    if (c0 + col < C && r0 + row < ld) {
+      Chunk<kBF16> c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c.w[0][i] = static_cast<uint32_t>(tile[row + 2 * i][col]) |
+                    (static_cast<uint32_t>(tile[row + 2 * i + 1][col]) << 16);
+      store_chunk<kBF16>(out + (c0 + col) * ld + r0 + row, 8, c);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* __restrict__ p, int64_t count) {
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += step)
+    p[i] = 0;
+}
+
+// ---------------------------------------------------------------------------
+// Host side: sizes and the choice of a launch
+// ---------------------------------------------------------------------------
+
+bool known_dtype(int32_t d) { return d >= MHC_LINEAR_BF16 && d <= MHC_LINEAR_E4M3_MX; }
+int64_t elem(int32_t dtype) { return is8(dtype) ? 1 : 2; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Shape {
+  int bm, bn;
+};
+
+Shape shape_of(int32_t kernel) {
+  switch (kernel) {
+    case MHC_LINEAR_NARROW: return {64, 32};
+    case MHC_LINEAR_SMALL: return {64, 64};
+    case MHC_LINEAR_MEDIUM: return {128, 128};
+    default: return {256, 256};
+  }
+}
+
+mhc_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
+  if (M < 0 || M > INT32_MAX) return fail(MHC_ERROR_INVALID_VALUE, "M must be in [0, 2^31 - 1]");
+  if (N < 1 || N > INT32_MAX) return fail(MHC_ERROR_INVALID_VALUE, "N must be in [1, 2^31 - 1]");
+  if (K < 1 || K > MHC_LINEAR_MAX_K)
+    return fail(MHC_ERROR_INVALID_VALUE, "K must be in [1, %lld] (got %lld)", MHC_LINEAR_MAX_K,
+                static_cast<long long>(K));
+  if (!known_dtype(dtype))
+    return fail(MHC_ERROR_INVALID_VALUE,
+                "dtype must be MHC_LINEAR_BF16, _F16, _E4M3_ROW or _E4M3_MX (got %d)", dtype);
+  return ok();
+}
+
+constexpr int32_t kMaxSplits = 64;
+
+mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
+                     const mhc_linear_launch* launch, mhc_linear_launch* plan) {
+  const int32_t want = launch != nullptr ? launch->kernel : 0;
+  const int32_t parts = launch != nullptr ? launch->splits : 0;
+  if (want < 0 || want > MHC_LINEAR_LARGE || parts < 0 || parts > kMaxSplits)
+    return fail(MHC_ERROR_INVALID_VALUE, "launch: kernel %d with %d splits does not exist", want,
+                parts);
+  const auto tiles = [&](int32_t k) {
+    const Shape s = shape_of(k);
+    return ceil_div(M, s.bm) * ceil_div(N, s.bn);
+  };
+  int32_t k = want;
+  if (k == 0) {
+    if (M <= 16) k = MHC_LINEAR_ROWS;
+    else if (N <= 32) k = MHC_LINEAR_NARROW;
+    else if (tiles(MHC_LINEAR_LARGE) >= 192) k = MHC_LINEAR_LARGE;
+    else if (tiles(MHC_LINEAR_MEDIUM) >= 128) k = MHC_LINEAR_MEDIUM;
+    else k = MHC_LINEAR_SMALL;
+  }
+  if (k == MHC_LINEAR_ROWS) {
+    if (M > 16 || parts > 1)
+      return fail(MHC_ERROR_INVALID_VALUE,
+                  "launch: the row kernel takes at most 16 rows and one part");
+    *plan = {k, 1};
+    return ok();
+  }
+  if (tiles(k) > INT32_MAX / kMaxSplits)
+    return fail(MHC_ERROR_INVALID_VALUE, "M and N make too many tiles");
+  const int64_t all = ceil_div(K * elem(dtype), kTileK);
+  int64_t s = parts;
+  if (s == 0) {
+    // two blocks for each CU, and at least 4 tiles of the sum in each part
+    s = 1;
+    while (s < kMaxSplits && M > 0 && tiles(k) * s * 2 <= 512 && all / (s * 2) >= 4) s *= 2;
+  }
+  if (s > all) s = all;
+  // no empty part
+  s = ceil_div(all, ceil_div(all, s));
+  *plan = {k, static_cast<int32_t>(s)};
+  return ok();
+}
+
+int64_t fwd_workspace(int64_t M, int64_t N, const mhc_linear_launch& plan) {
+  return plan.splits > 1 ? mul_bytes(mul_bytes(M, N, 4), plan.splits, 1) : 0;
+}
+
+mhc_status validate_fwd(const void* x, const void* xs, const void* w, const void* ws,
+                        const void* bias, const void* residual, const void* out, const void* z,
+                        const void* workspace, int64_t workspace_bytes, int64_t M, int64_t N,
+                        int64_t K, int32_t dtype, int32_t act, const mhc_linear_launch* launch,
+                        mhc_linear_launch* plan) {
+  mhc_status st = check_sizes(M, N, K, dtype);
+  if (st != MHC_SUCCESS) return st;
+  if (act < MHC_ACT_NONE || act > MHC_ACT_GELU)
+    return fail(MHC_ERROR_INVALID_VALUE, "unknown activation %d", act);
+  if ((st = make_plan(M, N, K, dtype, launch, plan)) != MHC_SUCCESS) return st;
+  if (!is8(dtype) && (xs != nullptr || ws != nullptr))
+    return fail(MHC_ERROR_INVALID_VALUE, "16-bit operands have no scales");
+  if (M == 0) return ok();
+  const int64_t need = fwd_workspace(M, N, *plan);
+  if (need < 0) return fail(MHC_ERROR_INVALID_VALUE, "the workspace's size does not fit 64 bits");
+  if (workspace_bytes < need)
+    return fail(MHC_ERROR_INVALID_VALUE, "workspace_bytes %lld < %lld needed",
+                static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+  const int64_t E = elem(dtype), MN = mul_bytes(M, N, 2);
+  const int64_t blocks = ceil_div(K, 32);
+  const bool row = dtype == MHC_LINEAR_E4M3_ROW;
+  const auto scales = [&](int64_t r) { return !is8(dtype) ? 0 : row ? r * 4 : mul_bytes(r, blocks, 1); };
+  const Tensor in[] = {{x, mul_bytes(M, K, E), E, "x"},
+                       {xs, scales(M), row ? 4 : 1, "x_scales"},
+                       {w, mul_bytes(N, K, E), E, "weight"},
+                       {ws, scales(N), row ? 4 : 1, "weight_scales"},
+                       {bias, bias != nullptr ? N * 2 : 0, 2, "bias"},
+                       {residual, residual != nullptr ? MN : 0, 2, "residual"}};
+  const Tensor outs[] = {{out, MN, 2, "out"},
+                         {z, z != nullptr ? MN : 0, 2, "z"},
+                         {workspace, need, 4, "workspace"}};
+  return check_tensors(in, outs);
+}
+
+bool whole_pieces(const TileArgs& a) {
+  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 &&
+         a.ldx % 16 == 0 && a.ldw % 16 == 0 && a.kbytes % 16 == 0;
+}
+
+template <int OP, int BM, int BN, int WM, int WN>
+hipError_t launch_tile(TileArgs a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  a.tiles_m = static_cast<uint32_t>(ceil_div(a.M, BM));
+  a.tiles_n = static_cast<uint32_t>(ceil_div(a.N, BN));
+  const dim3 grid(a.tiles_m * a.tiles_n * a.splits), block(64 * WM * WN);
+  // straight into LDS only from rows that are whole 16-byte pieces
+  if (whole_pieces(a))
+    return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, true>, grid, block, s, start, stop, a);
+  if constexpr (BM == 256)
+    return launch_tile<OP, 128, 128, 2, 2>(a, s, start, stop);  // the same sums in the same order
+  else
+    return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, false>, grid, block, s, start, stop, a);
+}
+
+// One product and its epilogue, as planned.
+template <int OP>
+hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t s,
+                          hipEvent_t start, hipEvent_t stop) {
+  const int64_t all = ceil_div(a.kbytes, kTileK);
+  a.splits = static_cast<uint32_t>(plan.splits);
+  a.per_split = static_cast<uint32_t>(ceil_div(all, plan.splits));
+  const bool join = a.splits > 1;
+  const hipEvent_t end = join ? nullptr : stop;
+  hipError_t e;
+  switch (plan.kernel) {
+    case MHC_LINEAR_NARROW: e = launch_tile<OP, 64, 32, 4, 1>(a, s, start, end); break;
+    case MHC_LINEAR_SMALL: e = launch_tile<OP, 64, 64, 2, 2>(a, s, start, end); break;
+    case MHC_LINEAR_MEDIUM: e = launch_tile<OP, 128, 128, 2, 2>(a, s, start, end); break;
+    default: e = launch_tile<OP, 256, 256, 2, 4>(a, s, start, end); break;
+  }
+  if (e != hipSuccess || !join) return e;
+  const int64_t blocks = ceil_div(a.M * ceil_div(a.N, 8), 256);
+  return launch_kernel(linear_join_kernel<OP>, dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096)),
+                       dim3(256), s, nullptr, stop, a.partial, a.splits, a.M, a.e);
+}
+
+template <int OP>
+hipError_t launch_rows(const TileArgs& t, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  const RowsArgs a = {static_cast<const uint8_t*>(t.x), static_cast<const uint8_t*>(t.w), t.xs,
+                      t.ws, t.M, t.N, t.kbytes, t.e};
+  const dim3 grid(static_cast<uint32_t>(ceil_div(t.N, 16)));
+  return launch_kernel(linear_rows_kernel<OP, 8>, grid, dim3(512), s, start, stop, a);
+}
+
+template <int OP>
+hipError_t launch_fwd(const TileArgs& a, const mhc_linear_launch& plan, hipStream_t s,
+                      hipEvent_t start, hipEvent_t stop) {
+  if (plan.kernel == MHC_LINEAR_ROWS) return launch_rows<OP>(a, s, start, stop);
+  return launch_product<OP>(a, plan, s, start, stop);
+}
+
+// --- backward ---
+
+// Rows of grad_out that one block sums: at most 256 parts.
+int64_t bias_rows(int64_t M) {
+  const int64_t r = ceil_div(M, 256);
+  return r < 32 ? 32 : r;
+}
+
+struct BwdPlan {
+  int64_t ldn, ldm;           // padded rows (elements) along N and along M
+  int64_t gz, wt, xt, gzt, bias, part, total;  // byte offsets in the workspace; part: split sums
+  mhc_linear_launch px, pw;   // the two products
+};
+
+int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
+
+// -1 in total where a size does not fit.
+BwdPlan plan_bwd(int64_t M, int64_t N, int64_t K, int32_t dtype) {
+  BwdPlan p = {};
+  p.ldn = round_up(N, 8);
+  p.ldm = round_up(M, 8);
+  if (M == 0) return p;
+  int64_t at = 0;
+  bool bad = false;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    if (bytes < 0 || __builtin_add_overflow(at, round_up(bytes, 256), &at)) bad = true;
+    return here;
+  };
+  p.gz = take(mul_bytes(M, p.ldn, 2));
+  p.wt = take(mul_bytes(K, p.ldn, 2));
+  p.xt = take(mul_bytes(K, p.ldm, 2));
+  p.gzt = take(mul_bytes(N, p.ldm, 2));
+  p.bias = take(mul_bytes(ceil_div(M, bias_rows(M)), N, 4));
+  if (make_plan(M, K, p.ldn, dtype, nullptr, &p.px) != MHC_SUCCESS ||
+      make_plan(N, K, p.ldm, dtype, nullptr, &p.pw) != MHC_SUCCESS)
+    bad = true;
+  const int64_t a = fwd_workspace(M, K, p.px), b = fwd_workspace(N, K, p.pw);
+  p.part = take(a < 0 || b < 0 ? -1 : a > b ? a : b);
+  p.total = bad ? -1 : at;
+  return p;
+}
+
+mhc_status check_bwd_sizes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
+  const mhc_status st = check_sizes(M, N, K, dtype);
+  if (st != MHC_SUCCESS) return st;
+  if (is8(dtype)) return fail(MHC_ERROR_INVALID_VALUE, "the backward takes 16-bit types");
+  if (M > MHC_LINEAR_MAX_K || N > MHC_LINEAR_MAX_K)
+    return fail(MHC_ERROR_INVALID_VALUE, "the backward sums over M and N: at most %lld of each",
+                MHC_LINEAR_MAX_K);
+  return ok();
+}
+
+mhc_status validate_bwd(const void* grad_out, const void* x, const void* w, const void* z,
+                        const void* gx, const void* gw, const void* gb, const void* workspace,
+                        int64_t workspace_bytes, int64_t M, int64_t N, int64_t K, int32_t dtype,
+                        int32_t act) {
+  const mhc_status st = check_bwd_sizes(M, N, K, dtype);
+  if (st != MHC_SUCCESS) return st;
+  if (act < MHC_ACT_NONE || act > MHC_ACT_GELU)
+    return fail(MHC_ERROR_INVALID_VALUE, "unknown activation %d", act);
+  const int64_t need = plan_bwd(M, N, K, dtype).total;
+  if (need < 0) return fail(MHC_ERROR_INVALID_VALUE, "the workspace's size does not fit 64 bits");
+  if (workspace_bytes < need)
+    return fail(MHC_ERROR_INVALID_VALUE, "workspace_bytes %lld < %lld needed",
+                static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+  const int64_t MN = mul_bytes(M, N, 2), MK = mul_bytes(M, K, 2);
+  // with M == 0 only the gradients of the weight and the bias exist
+  const int64_t NK = mul_bytes(N, K, 2);
+  const Tensor in[] = {{grad_out, MN, 2, "grad_out"},
+                       {x, MK, 2, "x"},
+                       {w, M > 0 ? NK : 0, 2, "weight"},
+                       {z, act != MHC_ACT_NONE ? MN : 0, 2, "z"}};
+  const Tensor outs[] = {{gx, gx != nullptr ? MK : 0, 2, "grad_x"},
+                         {gw, gw != nullptr ? NK : 0, 2, "grad_weight"},
+                         {gb, gb != nullptr ? N * 2 : 0, 2, "grad_bias"},
+                         {workspace, need, 16, "workspace"}};
+  return check_tensors(in, outs);
+}
+
+struct BwdArgs {
+  const void *grad_out, *x, *w, *z;
+  void *gx, *gw, *gb;
+  uint8_t* ws;
+  int64_t M, N, K;
+  int32_t act;
+};
+
+hipError_t launch_transpose(const void* in, void* out, int64_t R, int64_t C, int64_t ld,
+                            hipStream_t s, hipEvent_t start) {
+  const int64_t tc = ceil_div(C, 64), tr = ceil_div(ld, 64);
+  return launch_kernel(linear_transpose_kernel, dim3(static_cast<uint32_t>(tc * tr)), dim3(256), s,
+                       start, nullptr, static_cast<const uint16_t*>(in),
+                       static_cast<uint16_t*>(out), R, C, ld, static_cast<uint32_t>(tc));
+}
+
+hipError_t launch_zero(void* p, int64_t count, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  const int64_t blocks = ceil_div(count, 256);
+  return launch_kernel(linear_zero_kernel, dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096)),
+                       dim3(256), s, start, stop, static_cast<uint16_t*>(p), count);
+}
+
+// Events of a call of several launches: the start goes to the first, the stop
+// is recorded by an own (empty) marker after the last.
+struct Marks {
+  hipEvent_t start, stop;
+  hipEvent_t first() {
+    const hipEvent_t e = start;
+    start = nullptr;
+    return e;
+  }
+};
+
+template <int OP>
+hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t start,
+                      hipEvent_t stop) {
+  constexpr int F = out_format(OP);
+  typedef typename Store<F>::type S;
+  Marks marks = {start, stop};
+  hipError_t e = hipSuccess;
+  if (a.M == 0) {
+    if (a.gw != nullptr) e = launch_zero(a.gw, a.N * a.K, s, marks.first(), nullptr);
+    if (e == hipSuccess && a.gb != nullptr) e = launch_zero(a.gb, a.N, s, marks.first(), nullptr);
+  } else {
+    const BwdPlan p = plan_bwd(a.M, a.N, a.K, dtype);
+    const S* gz = static_cast<const S*>(a.grad_out);
+    if (a.act != MHC_ACT_NONE || a.gb != nullptr) {
+      const int64_t rows = bias_rows(a.M), parts = ceil_div(a.M, rows);
+      S* made = a.act != MHC_ACT_NONE ? reinterpret_cast<S*>(a.ws + p.gz) : nullptr;
+      float* sums = a.gb != nullptr ? reinterpret_cast<float*>(a.ws + p.bias) : nullptr;
+      const auto run = [&](auto kernel) {
+        return launch_kernel(kernel, dim3(static_cast<uint32_t>(ceil_div(a.N, 512)), static_cast<uint32_t>(parts)),
+                             dim3(256), s, marks.first(), nullptr, static_cast<const S*>(a.grad_out),
+                             static_cast<const S*>(a.z), made, sums, a.M, a.N, rows);
+      };
+      switch (a.act) {
+        case MHC_ACT_RELU: e = run(linear_gz_kernel<F, MHC_ACT_RELU>); break;
+        case MHC_ACT_SILU: e = run(linear_gz_kernel<F, MHC_ACT_SILU>); break;
+        case MHC_ACT_GELU: e = run(linear_gz_kernel<F, MHC_ACT_GELU>); break;
+        default: e = run(linear_gz_kernel<F, MHC_ACT_NONE>); break;
+      }
+      if (e != hipSuccess) return e;
+      if (made != nullptr) gz = made;
+      if (a.gb != nullptr) {
+        e = launch_kernel(linear_bias_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(a.N, 256))), dim3(256),
+                          s, nullptr, nullptr, sums, static_cast<S*>(a.gb), parts, a.N);
+        if (e != hipSuccess) return e;
+      }
+    }
+    if (a.gx != nullptr) {
+      // grad_x [M, K] = gz [M, N] . (W^T [K, N])^T; gz's rows are used as they are
+      e = launch_transpose(a.w, a.ws + p.wt, a.N, a.K, p.ldn, s, marks.first());
+      if (e != hipSuccess) return e;
+      TileArgs t = {};
+      t.x = gz;
+      t.w = a.ws + p.wt;
+      t.M = a.M; t.N = a.K;
+      t.ldx = a.N * 2; t.ldw = p.ldn * 2;
+      t.kbytes = static_cast<uint32_t>(a.N * 2);
+      t.partial = reinterpret_cast<float*>(a.ws + p.part);
+      t.e.out = a.gx; t.e.N = a.K;
+      mhc_linear_launch plan = p.px;
+      if (plan.kernel == MHC_LINEAR_ROWS) plan = {MHC_LINEAR_SMALL, 1};
+      e = launch_product<OP>(t, plan, s, nullptr, nullptr);
+      if (e != hipSuccess) return e;
+    }
+    if (a.gw != nullptr) {
+      // grad_weight [N, K] = gz^T [N, M] . (x^T [K, M])^T
+      e = launch_transpose(gz, a.ws + p.gzt, a.M, a.N, p.ldm, s, marks.first());
+      if (e == hipSuccess) e = launch_transpose(a.x, a.ws + p.xt, a.M, a.K, p.ldm, s, nullptr);
+      if (e != hipSuccess) return e;
+      TileArgs t = {};
+      t.x = a.ws + p.gzt;
+      t.w = a.ws + p.xt;
+      t.M = a.N; t.N = a.K;
+      t.ldx = t.ldw = p.ldm * 2;
+      t.kbytes = static_cast<uint32_t>(p.ldm * 2);
+      t.partial = reinterpret_cast<float*>(a.ws + p.part);
+      t.e.out = a.gw; t.e.N = a.K;
+      mhc_linear_launch plan = p.pw;
+      if (plan.kernel == MHC_LINEAR_ROWS) plan = {MHC_LINEAR_SMALL, 1};
+      e = launch_product<OP>(t, plan, s, nullptr, nullptr);
+    }
+  }
+  if (e == hipSuccess && marks.start != nullptr) e = hipEventRecord(marks.first(), s);
+  if (e == hipSuccess && stop != nullptr) e = hipEventRecord(stop, s);
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mhc_linear_abi_version(void) { return MHC_LINEAR_ABI_VERSION; }
+
+const char* mhc_linear_last_error_message(void) { return g_msg; }
+
+mhc_status mhc_linear_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
+                           const mhc_linear_launch* launch, mhc_linear_launch* plan) {
+  mhc_linear_launch p;
+  mhc_status st = check_sizes(M, N, K, dtype);
+  if (st == MHC_SUCCESS) st = make_plan(M, N, K, dtype, launch, &p);
+  if (st == MHC_SUCCESS && plan != nullptr) *plan = p;
+  return st;
+}
+
+int64_t mhc_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t dtype,
+                                       const mhc_linear_launch* launch) {
+  mhc_linear_launch p;
+  if (check_sizes(M, N, K, dtype) != MHC_SUCCESS ||
+      make_plan(M, N, K, dtype, launch, &p) != MHC_SUCCESS)
+    return -1;
+  return fwd_workspace(M, N, p);
+}
+
+int64_t mhc_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
+  if (check_bwd_sizes(M, N, K, dtype) != MHC_SUCCESS) return -1;
+  return plan_bwd(M, N, K, dtype).total;
+}
+
+mhc_status mhc_linear_validate_fwd(const void* x, const void* x_scales, const void* weight,
+                                   const void* weight_scales, const void* bias,
+                                   const void* residual, const void* out, const void* z,
+                                   const void* workspace, int64_t workspace_bytes, int64_t M,
+                                   int64_t N, int64_t K, int32_t dtype, int32_t act,
+                                   const mhc_linear_launch* launch) {
+  mhc_linear_launch plan;
+  return validate_fwd(x, x_scales, weight, weight_scales, bias, residual, out, z, workspace,
+                      workspace_bytes, M, N, K, dtype, act, launch, &plan);
+}
+
+mhc_status mhc_linear_validate_bwd(const void* grad_out, const void* x, const void* weight,
+                                   const void* z, const void* grad_x, const void* grad_weight,
+                                   const void* grad_bias, const void* workspace,
+                                   int64_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                                   int32_t dtype, int32_t act) {
+  return validate_bwd(grad_out, x, weight, z, grad_x, grad_weight, grad_bias, workspace,
+                      workspace_bytes, M, N, K, dtype, act);
+}
+
+mhc_status mhc_linear_fwd(const void* x, const void* x_scales, const void* weight,
+                          const void* weight_scales, const void* bias, const void* residual,
+                          void* out, void* z, void* workspace, int64_t workspace_bytes, int64_t M,
+                          int64_t N, int64_t K, int32_t dtype, int32_t act, void* stream,
+                          const mhc_linear_launch* launch, void* start_event, void* stop_event) {
+  mhc_linear_launch plan;
+  const mhc_status st = validate_fwd(x, x_scales, weight, weight_scales, bias, residual, out, z,
+                                     workspace, workspace_bytes, M, N, K, dtype, act, launch, &plan);
+  if (st != MHC_SUCCESS) return st;
+  if (M == 0) return record_empty(stream, start_event, stop_event);
+  TileArgs a = {};
+  a.x = x;
+  a.w = weight;
+  if (dtype == MHC_LINEAR_E4M3_MX) {
+    a.xs = static_cast<const uint8_t*>(x_scales);
+    a.ws = static_cast<const uint8_t*>(weight_scales);
+  } else {
+    a.e.x_scales = static_cast<const float*>(x_scales);
+    a.e.weight_scales = static_cast<const float*>(weight_scales);
+  }
+  a.M = M;
+  a.N = N;
+  a.ldx = a.ldw = K * elem(dtype);
+  a.kbytes = static_cast<uint32_t>(K * elem(dtype));
+  a.partial = static_cast<float*>(workspace);
+  a.e.bias = bias;
+  a.e.residual = residual;
+  a.e.out = out;
+  a.e.z = z;
+  a.e.N = N;
+  a.e.act = act;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipEvent_t b = static_cast<hipEvent_t>(start_event), f = static_cast<hipEvent_t>(stop_event);
+  hipError_t e;
+  switch (dtype) {
+    case MHC_LINEAR_BF16: e = launch_fwd<kOpBF16>(a, plan, s, b, f); break;
+    case MHC_LINEAR_F16: e = launch_fwd<kOpF16>(a, plan, s, b, f); break;
+    case MHC_LINEAR_E4M3_ROW: e = launch_fwd<kOpE4M3>(a, plan, s, b, f); break;
+    default: e = launch_fwd<kOpMX>(a, plan, s, b, f); break;
+  }
+  return launch_status(e, "product launch");
+}
+
+mhc_status mhc_linear_bwd(const void* grad_out, const void* x, const void* weight, const void* z,
+                          void* grad_x, void* grad_weight, void* grad_bias, void* workspace,
+                          int64_t workspace_bytes, int64_t M, int64_t N, int64_t K, int32_t dtype,
+                          int32_t act, void* stream, void* start_event, void* stop_event) {
+  const mhc_status st = validate_bwd(grad_out, x, weight, z, grad_x, grad_weight, grad_bias,
+                                     workspace, workspace_bytes, M, N, K, dtype, act);
+  if (st != MHC_SUCCESS) return st;
+  const BwdArgs a = {grad_out, x, weight, z, grad_x, grad_weight, grad_bias,
+                     static_cast<uint8_t*>(workspace), M, N, K, act};
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipEvent_t b = static_cast<hipEvent_t>(start_event), f = static_cast<hipEvent_t>(stop_event);
+  const hipError_t e = dtype == MHC_LINEAR_BF16 ? launch_bwd<kOpBF16>(a, dtype, s, b, f)
+                                                : launch_bwd<kOpF16>(a, dtype, s, b, f);
+  return launch_status(e, "product backward launch");
+}
+
+}  // extern "C"

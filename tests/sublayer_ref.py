@@ -150,3 +150,63 @@ class Guarded:
 def same_bytes(a: torch.Tensor, b: torch.Tensor) -> bool:
     a, b = a.contiguous().cpu(), b.contiguous().cpu()
     return a.shape == b.shape and torch.equal(a.flatten().view(torch.uint8), b.flatten().view(torch.uint8))
+
+
+# ---------------------------------------------------------------------------
+# Product
+# ---------------------------------------------------------------------------
+
+def tail(a: torch.Tensor) -> torch.Tensor:
+    """The normal distribution's tail past a."""
+    return 0.5 * torch.special.erfc(a * 0.5 ** 0.5)
+
+
+def act(z: torch.Tensor, name: str) -> torch.Tensor:
+    if name == "relu":
+        return z.clamp_min(0)
+    if name == "silu":
+        return z * torch.sigmoid(z)
+    return z * tail(-z) if name == "gelu" else z
+
+
+def act_slope(z: torch.Tensor, name: str) -> torch.Tensor:
+    if name == "relu":
+        return (z > 0).double()
+    if name == "silu":
+        s = torch.sigmoid(z)
+        return s * (1 + z * (1 - s))
+    if name == "gelu":
+        return tail(-z) + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    return torch.ones_like(z)
+
+
+def linear(x, w, bias=None, activation="none", residual=None):
+    """(out, z), all fp64."""
+    z = x @ w.t()
+    z = z if bias is None else z + bias
+    out = act(z, activation)
+    return (out if residual is None else out + residual), z
+
+
+def linear_grads(g, x, w, z, activation):
+    """(grad_x, grad_weight, grad_bias, gz) without the rounding of gz."""
+    gz = g * act_slope(z, activation)
+    return gz @ w, gz.t() @ x, gz.sum(0), gz
+
+
+def dequantise(q: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """fp64 values of e4m3 codes with fp32 row scales or e8m0 scales of 32 columns."""
+    v = d(q)
+    if scales.dtype == torch.float32:
+        return v * d(scales)[:, None]
+    return v * d(scales).repeat_interleave(32, 1)[:, :q.shape[1]]
+
+
+def quantise(v: torch.Tensor, kind: str) -> tuple[torch.Tensor, torch.Tensor]:
+    """fp32 rows on the CPU in e4m3 with "row" or "mx" scales."""
+    if kind == "row":
+        s = (v.abs().amax(1) / 448).clamp_min(2.0 ** -126)
+        return (v / s[:, None]).to(torch.float8_e4m3fn), s
+    p = mx_power(block_amax(v))
+    scale = (2.0 ** p.double()).repeat_interleave(32, 1)[:, :v.shape[1]]
+    return (v.double() / scale).float().to(torch.float8_e4m3fn), (p + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
