@@ -230,6 +230,28 @@ __device__ __forceinline__ uint32_t swap_of(uint32_t row) {
   return (row & 3) | (((row >> SH) & 1) << 2);
 }
 
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t*)p));
+}
+
+// Starts a load of BYTES for each lane from `offset` + `at` of the buffer to the
+// wave's consecutive places in LDS from `to` on; a lane at kOutside brings zeros.
+// No register is written; the loads are waited for by wait_tiles().
+template <int BYTES>
+__device__ __forceinline__ void load_to_lds(uint32_t offset, i32x4 rsrc, uint32_t at, uint32_t to) {
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(offset), "s"(rsrc), "s"(at)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(offset), "s"(rsrc), "s"(at)
+                 : "memory");
+}
+
 // Loads ROWS rows x kTileK bytes into LDS.
 template <int ROWS, int THREADS, int SH, bool DMA, int ELEM>
 struct Loader {
@@ -265,11 +287,7 @@ struct Loader {
       for (int q = 0; q < Q; ++q) {
         const uint32_t at = k + piece[q] < kbytes ? offset[q] : kOutside;
         const uint32_t dst = to + (q * THREADS + wave * 64) * 16;
-        // No register is written; the tile is waited for by wait_tiles().
-        asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                     :
-                     : "s"(dst), "v"(at), "s"(rsrc), "s"(k)
-                     : "memory");
+        load_to_lds<16>(at, rsrc, k, dst);
       }
     } else {
 #pragma unroll
@@ -316,12 +334,109 @@ __device__ __forceinline__ void wait_tiles() {
   asm volatile("" ::: "memory");
 }
 
+// The lanes of a wave see each other's LDS writes (which a wave's own LDS
+// instructions do in order; this keeps the compiler's order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // e8m0 bytes of TILES rows of 16, for the tile at kTileK: one byte a lane.
 template <int TILES>
 struct Scales {
   uint32_t offset[TILES];
   uint32_t now[TILES], next[TILES];
 };
+
+// Which tile a block takes: blocks go round the 8 XCDs, so consecutive tiles
+// are given to every eighth block, and tiles run down 4 rows of tiles before
+// the next column: the blocks of one XCD share rows of x and W in its L2.
+struct Place {
+  int64_t m0, n0;
+  uint32_t part;
+};
+
+template <int BM, int BN>
+__device__ __forceinline__ Place place_of(const TileArgs& a) {
+  const uint32_t tiles = a.tiles_m * a.tiles_n;
+  uint32_t id = blockIdx.x;
+  const uint32_t part = id / tiles;
+  id -= part * tiles;
+  const uint32_t each = tiles / 8, more = tiles % 8, xcd = id % 8, k = id / 8;
+  id = xcd * each + (xcd < more ? xcd : more) + k;
+  const uint32_t band = id / (4 * a.tiles_n);
+  const uint32_t high = min(4u, a.tiles_m - 4 * band);
+  id -= band * 4 * a.tiles_n;
+  return {static_cast<int64_t>(4 * band + id % high) * BM, static_cast<int64_t>(id / high) * BN, part};
+}
+
+// The tile's results, written. Lane l of wave (wm, wn) holds in acc[i][j] four
+// consecutive columns of row 16 i + l % 16 of the wave's part; over the G tiles
+// of a group they are 4 G consecutive ones. LDS: SIZE bytes.
+template <int OP, int BM, int BN, int WM, int WN, int SIZE>
+__device__ __forceinline__ void write_tile(const TileArgs& a, const Place& at, uint8_t* lds,
+                                           f32x4 (&acc)[BM / WM / 16][BN / WN / 16]) {
+  constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
+  constexpr int G = group_of(TJ);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const uint32_t wm = wave / WN, wn = wave % WN;
+  // A wave's results go through its own part of LDS, from where its lanes take
+  // 8 consecutive columns each of whole rows: one loop for every activation
+  // instead of TI * TJ / 2 copies (3% of a 256 x 256 tile's time at K = 4096).
+  constexpr int kWide = TJ * 16;
+  constexpr int kHalves = BM * BN * 4 > SIZE ? 2 : 1;
+  constexpr int kRows = TI * 16 / kHalves;
+  static_assert(TI % kHalves == 0 && BM * BN * 4 / kHalves <= SIZE, "the results fit");
+  __syncthreads();  // every wave is done with the tiles
+  float* mine = reinterpret_cast<float*>(lds) + wave * (kRows * kWide);
+  const bool whole = at.m0 + BM <= a.M && at.n0 + BN <= a.N;
+#pragma unroll
+  for (int half = 0; half < kHalves; ++half) {
+#pragma unroll
+    for (int i = 0; i < TI / kHalves; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        *reinterpret_cast<f32x4*>(mine + (16 * i + low) * kWide + (j / G) * (16 * G) +
+                                  g * (4 * G) + (j % G) * 4) = acc[half * (TI / kHalves) + i][j];
+    wave_sync();
+    const int64_t m0 = at.m0 + wm * (TI * 16) + half * kRows;
+    const int64_t n0 = at.n0 + wn * kWide;
+    const auto each = [&](const auto& sink) {
+#pragma unroll 2
+      for (uint32_t id = lane; id < kRows * kWide / 8; id += 64) {
+        const uint32_t row = id / (kWide / 8), col = id % (kWide / 8) * 8;
+        const int64_t m = m0 + row, n = n0 + col;
+        if (whole || (m < a.M && n < a.N)) {
+          const f32x4 p = *reinterpret_cast<const f32x4*>(mine + row * kWide + col);
+          const f32x4 q = *reinterpret_cast<const f32x4*>(mine + row * kWide + col + 4);
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] = p[e];
+            v[4 + e] = q[e];
+          }
+          sink(m, n, whole ? 8 : static_cast<int>(min(a.N - n, static_cast<int64_t>(8))), v);
+        }
+      }
+    };
+    if (a.splits > 1) {
+      float* partial = a.partial + static_cast<int64_t>(at.part) * a.M * a.N;
+      each([&](int64_t m, int64_t n, int count, float(&v)[8]) {
+        Chunk<kF32> c;
+        narrow_chunk<kF32>(v, c);
+        store_chunk<kF32>(partial + m * a.N + n, count, c);
+      });
+    } else {
+      with_act(a.e.act, [&](auto act) {
+        each([&](int64_t m, int64_t n, int count, float(&v)[8]) {
+          finish<OP, decltype(act)::value>(a.e, m, n, count, v);
+        });
+      });
+    }
+    wave_sync();
+  }
+}
 
 template <int OP, int BM, int BN, int WM, int WN, bool DMA>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
@@ -333,23 +448,9 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
   constexpr int kSteps = is8(OP) ? 1 : 2;
   __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kTileK];
 
-  // Which tile: blocks go round the 8 XCDs, so consecutive tiles are given to
-  // every eighth block, and tiles run down 4 rows of tiles before the next
-  // column: the blocks of one XCD share rows of x and W in its L2.
-  const uint32_t tiles = a.tiles_m * a.tiles_n;
-  uint32_t id = blockIdx.x;
-  const uint32_t part = id / tiles;
-  id -= part * tiles;
-  {
-    const uint32_t each = tiles / 8, more = tiles % 8, xcd = id % 8, k = id / 8;
-    id = xcd * each + (xcd < more ? xcd : more) + k;
-  }
-  const uint32_t band = id / (4 * a.tiles_n);
-  const uint32_t high = min(4u, a.tiles_m - 4 * band);
-  id -= band * 4 * a.tiles_n;
-  const int64_t m0 = static_cast<int64_t>(4 * band + id % high) * BM;
-  const int64_t n0 = static_cast<int64_t>(id / high) * BN;
-
+  const Place place = place_of<BM, BN>(a);
+  const int64_t m0 = place.m0, n0 = place.n0;
+  const uint32_t part = place.part;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
   const uint32_t wm = wave / WN, wn = wave % WN;
@@ -452,8 +553,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
   const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
   const uint32_t first = part * a.per_split;
   const uint32_t last = min(all, first + a.per_split);
-  const uint32_t at0 = static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)&lds[0][0]));
+  const uint32_t at0 = lds_address(&lds[0][0]);
   constexpr uint32_t kBuffer = (BM + BN) * kTileK;
   sx.now[0] = sw.now[0] = 0;
   if (first < last) {
@@ -475,72 +575,177 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
     }
     multiply(lds[b]);
   }
+  write_tile<OP, BM, BN, WM, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
+}
 
-  // A lane's results: row `xrow` + 16 i of the tile, columns from wcol(j) on, 4G
-  // consecutive ones over the G tiles of a group.
-  const auto wcol = [&](int j) {
-    return wn * (TJ * 16) + (j / G) * (16 * G) + g * (4 * G) + (j % G) * 4;
+// ---------------------------------------------------------------------------
+// Large tiles
+//
+// 256 x 256 outputs to a block of eight waves, 128 x 64 each, two waves to a
+// SIMD. A wave's reads run ahead of its matrix instructions: its W rows and the
+// first half of its x rows of a pass are in registers when the pass begins; the
+// second half is read under the first half's instructions, and then, once the
+// next tile has arrived in the other buffer and every wave has its values of
+// this one, the next pass's W rows and first x rows are read under the second
+// half's, while this buffer is loaded again, so each load has a whole pass to
+// arrive. Reads and loads are spread between the instructions of one W row
+// (sched_barrier): a run of other instructions leaves the matrix unit idle.
+//
+// 8192^3 in bf16 (1373 TFLOP/s; the library's product 1430-1465): four waves of 128 x 128, one to a SIMD,
+// 1230 (nobody fills a wave's gaps); all loads at the start of the half 1140;
+// reads not ahead of the pass 1280; without the raised priority of the
+// matrix instructions 1346. Matrix units are busy 57-63% of the cycles, at a clock that the
+// load itself brings down to 1.7 GHz (bf16) and 1.95 GHz (e4m3). e4m3: 2550
+// TFLOP/s with row scales, 2060 with block scales (their bytes come 16 of a row
+// at a time, for four passes: a pass's 4 alone cost as many requests as its
+// values, 1880).
+// ---------------------------------------------------------------------------
+
+template <int OP, int WN>
+__global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
+  constexpr int BM = 256, BN = 256, kThreads = 128 * WN;
+  constexpr int TI = 8, TJ = 16 / WN, HALF = TI / 2;
+  constexpr int kPieces = is8(OP) ? 1 : 2;  // matrix instructions for one result in a pass
+  constexpr uint32_t kBuffer = (BM + BN) * kTileK;
+  // kMX: the e8m0 bytes of four passes, 16 for each row of x and of W
+  constexpr uint32_t kScaleBytes = OP == kOpMX ? (BM + BN) * 16 : 0;
+  __shared__ __align__(1024) uint8_t lds[2][kBuffer];
+  __shared__ __align__(1024) uint8_t scales[2][OP == kOpMX ? kScaleBytes : 16];
+  const Place place = place_of<BM, BN>(a);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const uint32_t wm = wave / WN, wn = wave % WN;
+
+  Loader<BM, kThreads, 2, true, 1> lx;
+  Loader<BN, kThreads, 4, true, 1> lw;
+  lx.init(a.x, place.m0, a.M, a.ldx);
+  lw.init(a.w, place.n0, a.N, a.ldw);
+
+  const uint32_t xrow = wm * 128 + low, wrow = wn * (TJ * 16) + (low / 4) * 16 + low % 4;
+  const uint32_t fx = swap_of<2>(xrow) * 16, fw = swap_of<4>(wrow) * 16;
+  // byte places of this lane's pieces: x rows 16 apart, W rows 4 apart in groups 64 apart
+  const uint32_t px[2] = {xrow * kTileK + ((g * 16) ^ fx), xrow * kTileK + ((64 + g * 16) ^ fx)};
+  const uint32_t pw[2] = {BM * kTileK + wrow * kTileK + ((g * 16) ^ fw),
+                          BM * kTileK + wrow * kTileK + ((64 + g * 16) ^ fw)};
+
+  // kMX: each of the first four waves brings the bytes of 64 x rows, the others of 64 W rows.
+  const uint32_t kblocks = a.kbytes / 32;
+  uint32_t so = 0;
+  i32x4 sr = {0, 0, 0, 0};
+  if constexpr (OP == kOpMX) {
+    const uint32_t thread = threadIdx.x % 256;
+    const bool of_x = __builtin_amdgcn_readfirstlane(threadIdx.x / 256) == 0;
+    const int64_t row0 = of_x ? place.m0 : place.n0, left = (of_x ? a.M : a.N) - row0;
+    const uint32_t here = static_cast<uint32_t>(left < 256 ? left : 256);
+    const uint64_t p = reinterpret_cast<uint64_t>((of_x ? a.xs : a.ws) + row0 * kblocks);
+    sr = i32x4{static_cast<int32_t>(p), static_cast<int32_t>(p >> 32),
+               static_cast<int32_t>(here * kblocks), kRsrcFormat};
+    so = thread < here ? thread * kblocks : kOutside;
+  }
+  const uint32_t at0 = lds_address(&lds[0][0]);
+  const uint32_t at1 = lds_address(&scales[0][0]);
+  // The range check of a buffer counts the scalar offset too, so rows past the
+  // end read zeros from one offset a lane and a scalar for each load's rows.
+  const uint32_t ox = threadIdx.x / 8 * static_cast<uint32_t>(a.ldx) + lx.piece[0];
+  const uint32_t ow = threadIdx.x / 8 * static_cast<uint32_t>(a.ldw) + lw.piece[0];
+  // Loads of the tile at kt into buffer b, a part of them a call.
+  const auto start = [&](uint32_t kt, uint32_t b, int q) {
+    const uint32_t to = at0 + b * kBuffer + (q * kThreads + wave * 64) * 16;
+    const uint32_t k = kt * kTileK;
+    const uint32_t rows = q * (kThreads / 8);
+    load_to_lds<16>(k + lx.piece[0] < a.kbytes ? ox : kOutside, lx.rsrc, k + rows * static_cast<uint32_t>(a.ldx), to);
+    load_to_lds<16>(k + lw.piece[0] < a.kbytes ? ow : kOutside, lw.rsrc, k + rows * static_cast<uint32_t>(a.ldw), to + BM * kTileK);
   };
-  float* partial = a.splits > 1 ? a.partial + static_cast<int64_t>(part) * a.M * a.N : nullptr;
-  const auto put = [&](auto act, int64_t m, int64_t n, int count, float(&v)[8]) {
-    if (partial != nullptr) {
-      Chunk<kF32> c;
-      narrow_chunk<kF32>(v, c);
-      store_chunk<kF32>(partial + m * a.N + n, count, c);
-    } else {
-      finish<OP, decltype(act)::value>(a.e, m, n, count, v);
-    }
+
+  // kMX: the scales of four tiles from kt on, 16 bytes of each row.
+  const auto start_scales = [&](uint32_t kt, uint32_t b) {
+    if constexpr (OP == kOpMX)
+      load_to_lds<16>(kt * 4 < kblocks ? so : kOutside, sr, kt * 4, at1 + b * kScaleBytes + wave * 1024);
   };
-  if (m0 + BM <= a.M && n0 + BN <= a.N) {
-    // a whole tile, from the registers
-    with_act(partial != nullptr ? MHC_ACT_NONE : a.e.act, [&](auto act) {
+
+  // Both 16-byte pieces of a pass, and the scale byte.
+  struct Row {
+    i32x4 w[2];
+    int s;
+  };
+  Row w[TJ], xa[HALF], xb[HALF];
+  const auto scale_at = [&](uint32_t step, uint32_t row) {
+    return OP == kOpMX ? scales[step / 4 % 2][row * 16 + step % 4 * 4 + g] : 0;
+  };
+  const auto read_w = [&](uint32_t b, uint32_t step, int j) {
+    const uint32_t row = (j / 4) * 64 + (j % 4) * 4;
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
+    for (int h = 0; h < 2; ++h)
+      w[j].w[h] = *reinterpret_cast<const i32x4*>(&lds[0][0] + b * kBuffer + pw[h] + row * kTileK);
+    w[j].s = scale_at(step, BM + wrow + row);
+  };
+  const auto read_x = [&](uint32_t b, uint32_t step, int i, Row& r) {
 #pragma unroll
-        for (int j = 0; j < TJ; j += 2) {
-          float v[8];
+    for (int h = 0; h < 2; ++h)
+      r.w[h] = *reinterpret_cast<const i32x4*>(&lds[0][0] + b * kBuffer + px[h] + i * 16 * kTileK);
+    r.s = scale_at(step, xrow + i * 16);
+  };
+
+  f32x4 acc[TI][TJ];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] = acc[i][j][e];
-            v[4 + e] = acc[i][j + 1][e];
-          }
-          put(act, m0 + xrow + 16 * i, n0 + wcol(j), 8, v);
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const auto multiply = [&](int half, int j, const Row (&x)[HALF]) {
+#pragma unroll
+    for (int h = 0; h < kPieces; ++h)
+#pragma unroll
+      for (int i = 0; i < HALF; ++i) {
+        f32x4& c = acc[half * HALF + i][j];
+        if constexpr (is8(OP)) {
+          const Frag<OP> p = {w[j].w[0], w[j].w[1]}, q = {x[i].w[0], x[i].w[1]};
+          c = mma<OP>(p, q, c, w[j].s, x[i].s);
+        } else {
+          const Frag<OP> p = {w[j].w[h]}, q = {x[i].w[h]};
+          c = mma<OP>(p, q, c, 0, 0);
         }
-    });
-    return;
-  }
-  // A tile at the edge: through LDS (each wave in its own part of it), so that
-  // the cases of a row's end are one loop and not TI * TJ / 2 copies.
-  constexpr int kWide = TJ * 16;
-  constexpr int kHalves = BM * BN * 4 > 2 * static_cast<int>(kBuffer) ? 2 : 1;
-  constexpr int kRows = TI * 16 / kHalves;
-  static_assert(TI % kHalves == 0 && BM * BN * 4 / kHalves <= 2 * static_cast<int>(kBuffer), "the results fit");
-  __syncthreads();  // every wave is done with the tiles
-  float* mine = reinterpret_cast<float*>(&lds[0][0]) + wave * (kRows * kWide);
-#pragma unroll
-  for (int half = 0; half < kHalves; ++half) {
-#pragma unroll
-    for (int i = 0; i < TI / kHalves; ++i)
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        *reinterpret_cast<f32x4*>(mine + (16 * i + low) * kWide + wcol(j) - wn * kWide) =
-            acc[half * (TI / kHalves) + i][j];
-    __syncthreads();
-    for (uint32_t id = lane; id < kRows * kWide / 8; id += 64) {
-      const uint32_t row = id / (kWide / 8), col = id % (kWide / 8) * 8;
-      const int64_t m = m0 + wm * (TI * 16) + half * kRows + row;
-      const int64_t n = n0 + wn * kWide + col;
-      if (m < a.M && n < a.N) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = mine[row * kWide + col + e];
-        const int count = static_cast<int>(min(a.N - n, static_cast<int64_t>(8)));
-        with_act(partial != nullptr ? MHC_ACT_NONE : a.e.act,
-                 [&](auto act) { put(act, m, n, count, v); });
       }
+  };
+
+  const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
+  const uint32_t first = place.part * a.per_split;
+  const uint32_t last = min(all, first + a.per_split);
+#pragma unroll
+  for (int q = 0; q < TJ; ++q) start(first, 0, q);
+  start_scales(first, 0);
+  wait_tiles();
+#pragma unroll
+  for (int q = 0; q < TJ; ++q) start(first + 1, 1, q);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) read_w(0, 0, j);
+#pragma unroll
+  for (int i = 0; i < HALF; ++i) read_x(0, 0, i, xa[i]);
+  for (uint32_t kt = first; kt < last; ++kt) {
+    const uint32_t step = kt - first, b = step & 1;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      if (j < HALF) read_x(b, step, HALF + j, xb[j]);
+      __builtin_amdgcn_s_setprio(1);
+      multiply(0, j, xa);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __syncthreads();
+    wait_tiles();
+    if (step % 4 == 2) start_scales(kt + 2, (step + 2) / 4 % 2);
+    // past the last tile: zeros are loaded and old values read, and neither is used
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      start(kt + 2, b, j);
+      __builtin_amdgcn_s_setprio(1);
+      multiply(1, j, xb);
+      __builtin_amdgcn_s_setprio(0);
+      read_w(b ^ 1, step + 1, j);
+      if (j < HALF) read_x(b ^ 1, step + 1, j, xa[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
+  wait_tiles();  // nothing arrives in LDS any more
+  write_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
 
 // The parts of a split sum, added in ascending order, and the epilogue.
@@ -872,7 +1077,8 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
   if (s == 0) {
     // two blocks for each CU, and at least 4 tiles of the sum in each part
     s = 1;
-    while (s < kMaxSplits && M > 0 && tiles(k) * s * 2 <= 512 && all / (s * 2) >= 4) s *= 2;
+    const int64_t slots = k == MHC_LINEAR_LARGE ? 256 : 512;
+    while (s < kMaxSplits && M > 0 && tiles(k) * s * 2 <= slots && all / (s * 2) >= 4) s *= 2;
   }
   if (s > all) s = all;
   // no empty part
@@ -932,10 +1138,21 @@ hipError_t launch_tile(TileArgs a, hipStream_t s, hipEvent_t start, hipEvent_t s
   // straight into LDS only from rows that are whole 16-byte pieces
   if (whole_pieces(a))
     return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, true>, grid, block, s, start, stop, a);
-  if constexpr (BM == 256)
-    return launch_tile<OP, 128, 128, 2, 2>(a, s, start, stop);  // the same sums in the same order
-  else
-    return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, false>, grid, block, s, start, stop, a);
+  return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, false>, grid, block, s, start, stop, a);
+}
+
+// The large tiles take whole pieces only (and scales by the four); other
+// operands go through the medium tiles, whose sums have the same order.
+template <int OP>
+hipError_t launch_large(TileArgs a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  const bool scales = OP != kOpMX || (a.kbytes % kTileK == 0 &&
+                                      reinterpret_cast<uintptr_t>(a.xs) % 4 == 0 &&
+                                      reinterpret_cast<uintptr_t>(a.ws) % 4 == 0);
+  if (!whole_pieces(a) || !scales) return launch_tile<OP, 128, 128, 2, 2>(a, s, start, stop);
+  a.tiles_m = static_cast<uint32_t>(ceil_div(a.M, 256));
+  a.tiles_n = static_cast<uint32_t>(ceil_div(a.N, 256));
+  return launch_kernel(linear_large_kernel<OP, 4>, dim3(a.tiles_m * a.tiles_n * a.splits), dim3(512),
+                       s, start, stop, a);
 }
 
 // One product and its epilogue, as planned.
@@ -952,7 +1169,7 @@ hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t
     case MHC_LINEAR_NARROW: e = launch_tile<OP, 64, 32, 4, 1>(a, s, start, end); break;
     case MHC_LINEAR_SMALL: e = launch_tile<OP, 64, 64, 2, 2>(a, s, start, end); break;
     case MHC_LINEAR_MEDIUM: e = launch_tile<OP, 128, 128, 2, 2>(a, s, start, end); break;
-    default: e = launch_tile<OP, 256, 256, 2, 4>(a, s, start, end); break;
+    default: e = launch_large<OP>(a, s, start, end); break;
   }
   if (e != hipSuccess || !join) return e;
   const int64_t blocks = ceil_div(a.M * ceil_div(a.N, 8), 256);
