@@ -182,30 +182,45 @@ __device__ __forceinline__ f32x4 mma(const Frag<OP>& a, const Frag<OP>& b, f32x4
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel
+// Tiles in LDS
 //
-// A block computes BM x BN outputs from tiles of x and W rows in LDS, kTileK
-// bytes of each row at a time, in two buffers: while one is multiplied the
-// next is loaded, straight into LDS where rows are 16-byte aligned (no
-// registers, no waits but one before the barrier), through registers where
-// they are not. A row's eight 16-byte pieces are stored at places that are
-// exchanged by its number (piece ^ swap(row)), so that the matrix
-// instructions' reads, 16 rows at the same k, spread over all banks.
+// A block computes BM x BN outputs from tiles of x and W in LDS, kTileK bytes
+// of k at a time. x's rows are the second operand of the matrix instruction and
+// W's the first, so a lane's four results are consecutive columns of one row;
+// which W row stands at which place is chosen (4 consecutive rows out of every
+// 4 G) so that over G tiles a lane's results are 4 G consecutive columns, which
+// the epilogue moves in 16-byte accesses.
 //
-// W's rows are the first operand of the matrix instruction and x's the second,
-// so a lane's four results are consecutive columns of one row; which W row
-// stands at which place is chosen (column()) so that over four tiles they are
-// 16 consecutive columns, which the epilogue moves in 16-byte accesses.
+// An operand lies in memory with k along its rows ([rows, k]), or, in the
+// backward's products, with k down its columns ([k, columns], TURNED): its tile
+// is then 64 rows of k, and gfx950's transposing LDS read hands each lane 4
+// consecutive k of one column. Either way the tile is a run of 16-byte pieces
+// whose places within a row are exchanged by the row's number (swap), so that
+// the lanes of a read spread over all banks:
+//   k along the rows: x reads 16 rows at one k: piece ^ (row % 8);
+//     W reads 4 consecutive rows of every 4 G: two bits of row % 4, and the
+//     row's bit 4 G as the third;
+//   k down the columns: a read touches 4 rows (k % 4) at 4 places: bits that
+//     keep the 16 apart modulo 256 bytes, by what the places' distance is.
+// Pieces are loaded straight into LDS where they are whole and 16-byte aligned
+// (DMA: no registers, the range check of the buffer gives the zeros past the
+// ends), through registers otherwise.
 // ---------------------------------------------------------------------------
 
+// Two loads' operands: where they start, how far their rows are apart, and what
+// of them counts.
+struct Matrix {
+  const void* p;
+  int64_t count;  // rows, or columns where k runs down
+  int64_t ld;     // bytes from row to row
+};
+
 struct TileArgs {
-  const void* x;
-  const void* w;
+  Matrix x, w;
   const uint8_t* xs;  // kMX
   const uint8_t* ws;  // kMX
   int64_t M, N;
-  int64_t ldx, ldw;   // bytes from row to row
-  uint32_t kbytes;    // bytes of a row that count
+  uint32_t kbytes;    // bytes of k that count
   uint32_t tiles_m, tiles_n;
   uint32_t splits, per_split;  // parts of the sum, and tiles of kTileK in each
   float* partial;              // [splits][M][N] where splits > 1
@@ -223,21 +238,15 @@ constexpr int log2_of() {
 // How many consecutive tiles of 16 columns a lane's results run through.
 constexpr int group_of(int tj) { return tj < 4 ? tj : 4; }
 
-// The XOR of a row's pieces. SH = 3 is row % 8; the W rows that one
-// instruction reads are 4 consecutive ones out of every 2^SH.
-template <int SH>
-__device__ __forceinline__ uint32_t swap_of(uint32_t row) {
-  return (row & 3) | (((row >> SH) & 1) << 2);
-}
-
-__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const uint8_t*)p));
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
 }
 
 // Starts a load of BYTES for each lane from `offset` + `at` of the buffer to the
-// wave's consecutive places in LDS from `to` on; a lane at kOutside brings zeros.
-// No register is written; the loads are waited for by wait_tiles().
+// wave's consecutive places in LDS from `to` on; a lane past the buffer's end
+// brings zeros (the check counts `at` too). No register is written; the loads
+// are waited for by wait_tiles().
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(uint32_t offset, i32x4 rsrc, uint32_t at, uint32_t to) {
   if constexpr (BYTES == 16)
@@ -252,66 +261,102 @@ __device__ __forceinline__ void load_to_lds(uint32_t offset, i32x4 rsrc, uint32_
                  : "memory");
 }
 
-// Loads ROWS rows x kTileK bytes into LDS.
-template <int ROWS, int THREADS, int SH, bool DMA, int ELEM>
-struct Loader {
-  static constexpr int Q = ROWS * 8 / THREADS;
-  static_assert(ROWS * 8 % THREADS == 0, "whole pieces for every thread");
+// The buffer of up to 2^31 - 1 bytes from p on, in scalar registers.
+__device__ __forceinline__ i32x4 buffer_of(const void* p, int64_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(p);
+  const int64_t most = 0x7FFFFFFF;
+  const int32_t size = static_cast<int32_t>(bytes < 0 ? 0 : bytes < most ? bytes : most);
+  return i32x4{__builtin_amdgcn_readfirstlane(static_cast<int32_t>(b)),
+               __builtin_amdgcn_readfirstlane(static_cast<int32_t>(b >> 32)),
+               __builtin_amdgcn_readfirstlane(size), kRsrcFormat};
+}
+
+// The part of an operand that a block loads: SPAN rows (or columns) of it. IS_W
+// and G choose the places.
+template <int SPAN, int THREADS, bool TURNED, bool IS_W, int G, bool DMA, int ELEM>
+struct Operand {
+  static constexpr int Q = SPAN * 8 / THREADS;   // pieces a thread brings of one tile
+  static constexpr int P = TURNED ? SPAN / 8 : 8;  // pieces of a row of the tile
+  static constexpr int kRowBytes = P * 16;
+  static constexpr uint32_t kEach = THREADS / P;   // rows that one round of the threads covers
+  static_assert(SPAN * 8 % THREADS == 0 && kEach % (TURNED ? 4 : 32) == 0, "swap() is the same in every round");
   const uint8_t* base;
   i32x4 rsrc;
-  uint32_t offset[Q];  // row * ld + piece * 16, or kOutside
-  uint32_t piece[Q];   // the piece's place in the row, in bytes
+  uint32_t offset;  // of this thread's first piece
+  uint32_t row, piece;
+  uint32_t ld;
+  uint32_t here;    // rows (columns) that exist
   i32x4 held[DMA ? 1 : Q];
 
-  __device__ __forceinline__ void init(const void* p, int64_t row0, int64_t rows, int64_t ld) {
-    const int64_t left = rows - row0;
-    const uint32_t here = static_cast<uint32_t>(left < ROWS ? left : ROWS);
-    base = static_cast<const uint8_t*>(p) + row0 * ld;
-    const uint64_t b = reinterpret_cast<uint64_t>(base);
-    rsrc = i32x4{static_cast<int32_t>(b), static_cast<int32_t>(b >> 32),
-                 static_cast<int32_t>(here * static_cast<uint32_t>(ld)), kRsrcFormat};
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const uint32_t id = q * THREADS + threadIdx.x;
-      const uint32_t row = id / 8;
-      piece[q] = ((id % 8) ^ swap_of<SH>(row)) * 16;
-      offset[q] = row < here ? row * static_cast<uint32_t>(ld) + piece[q] : kOutside;
+  static __device__ __forceinline__ uint32_t swap(uint32_t row) {
+    if constexpr (!TURNED) {
+      if constexpr (IS_W) return (row & 3) | (((row >> log2_of<4 * G>()) & 1) << 2);
+      return row & 7;
+    } else if constexpr (!IS_W) {
+      return (row & 3) << 1;
+    } else if constexpr (G == 4) {
+      return ((row & 1) << 3) | ((row >> 1) & 1);
+    } else {
+      return P == 8 ? ((row >> 1) & 1) << 2 : 0;
     }
   }
 
-  // Starts the loads of the tile at byte k of every row into `to`.
-  __device__ __forceinline__ void start(uint32_t k, uint32_t kbytes, uint32_t to) {
+  __device__ __forceinline__ void init(const Matrix& m, int64_t first, uint32_t kbytes) {
+    const int64_t left = m.count - first;
+    here = static_cast<uint32_t>(left < SPAN ? left : SPAN);
+    ld = static_cast<uint32_t>(m.ld);
+    base = static_cast<const uint8_t*>(m.p) + (TURNED ? first * ELEM : first * m.ld);
+    rsrc = buffer_of(base, TURNED ? kbytes / ELEM * m.ld - first * ELEM : here * m.ld);
+    row = threadIdx.x / P;
+    piece = ((threadIdx.x % P) ^ swap(row)) * 16;
+    offset = row * ld + piece;
+  }
+
+  // Starts the loads of round q of the tile kt into `to`, the tile's place in LDS.
+  __device__ __forceinline__ void start(uint32_t kt, uint32_t kbytes, uint32_t to, int q) {
+    const uint32_t rows = q * kEach;
     if constexpr (DMA) {
       const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const uint32_t at = k + piece[q] < kbytes ? offset[q] : kOutside;
-        const uint32_t dst = to + (q * THREADS + wave * 64) * 16;
-        load_to_lds<16>(at, rsrc, k, dst);
-      }
+      const uint32_t dst = to + (q * THREADS + wave * 64) * 16;
+      // a tile's last rows end inside it where k runs along them; where k runs
+      // down, what is past the end is past the buffer's end
+      if constexpr (TURNED)
+        load_to_lds<16>(offset, rsrc, (kt * (kTileK / ELEM) + rows) * ld, dst);
+      else
+        load_to_lds<16>(kt * kTileK + piece < kbytes ? offset : kOutside, rsrc,
+                        kt * kTileK + rows * ld, dst);
     } else {
+      held[q] = i32x4{0, 0, 0, 0};
+      uint32_t left;  // bytes of the piece that exist
+      const uint8_t* p = base;
+      if constexpr (TURNED) {
+        const uint32_t k = kt * (kTileK / ELEM) + rows + row;
+        left = k * ELEM < kbytes && piece < here * ELEM ? here * ELEM - piece : 0;
+        p += static_cast<int64_t>(k) * ld + piece;
+      } else {
+        const uint32_t k = kt * kTileK + piece;
+        left = rows + row < here && k < kbytes ? kbytes - k : 0;
+        p += static_cast<int64_t>(rows + row) * ld + k;
+      }
+      if (left >= 16) {
+        if constexpr (ELEM == 2) {
+          typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
+          held[q] = *reinterpret_cast<const i32x4_at2*>(p);
+        } else {
+          typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
+          held[q] = *reinterpret_cast<const i32x4_at1*>(p);
+        }
+      } else if (left > 0) {
+        uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        held[q] = i32x4{0, 0, 0, 0};
-        if (offset[q] != kOutside && k + piece[q] < kbytes) {
-          const uint8_t* p = base + offset[q] + k;
-          const uint32_t left = kbytes - (k + piece[q]);
-          if constexpr (ELEM == 2) {
-            const Chunk<kBF16> c = load_chunk<kBF16>(reinterpret_cast<const uint16_t*>(p), left / 2 < 8 ? left / 2 : 8);
-            const u32x4 v = c.w[0];
-            held[q] = __builtin_bit_cast(i32x4, v);
-          } else if (left >= 16) {
-            typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
-            held[q] = *reinterpret_cast<const i32x4_at1*>(p);
-          } else {
-            uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (uint32_t i = 0; i < 16; ++i)
-              if (i < left) u[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
-            held[q] = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
-                            static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
+        for (uint32_t i = 0; i < 16; i += ELEM) {
+          if (i < left) {
+            const uint32_t b = ELEM == 2 ? *reinterpret_cast<const uint16_t*>(p + i) : p[i];
+            u[i / 4] |= b << (8 * (i % 4));
           }
         }
+        held[q] = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
+                        static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
       }
     }
   }
@@ -326,10 +371,69 @@ struct Loader {
   }
 };
 
-// Every load into LDS that this wave has started has arrived; then every
-// wave's has, and every wave is done with the other buffer.
+// This lane's reads of an operand's tile: `first` is the wave's first row (or
+// column) of the SPAN; tile t is 16 rows of x, or 16 of W spread over its group.
+template <typename O, bool TURNED, bool IS_W, int G>
+struct Reader {
+  uint32_t at[2];  // !TURNED: the places of the two pieces of a pass; TURNED: at[0]
+
+  __device__ __forceinline__ void init(uint32_t first) {
+    const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+    if constexpr (!TURNED) {
+      const uint32_t row = first + (IS_W ? (low / 4) * (4 * G) + low % 4 : low);
+      const uint32_t f = O::swap(row) * 16;
+      at[0] = row * kTileK + ((g * 16) ^ f);
+      at[1] = row * kTileK + ((64 + g * 16) ^ f);
+    } else {
+      // rows k = 8 g + low / 4 (and 4 more), 4 columns from `column` on
+      const uint32_t r = low / 4, q = low % 4;
+      const uint32_t column = first + q * (IS_W ? 4 * G : 4);
+      at[0] = (g * 8 + r) * O::kRowBytes + (((column / 8) ^ O::swap(r)) * 16) + column % 8 * 2;
+    }
+  }
+
+  // Row of the tile that this lane's values of tile t are.
+  static __device__ __forceinline__ uint32_t row_of(uint32_t first, int t) {
+    const uint32_t low = threadIdx.x % 16;
+    return first + (IS_W ? (t / G) * (16 * G) + (low / 4) * (4 * G) + (t % G) * 4 + low % 4
+                         : t * 16 + low);
+  }
+
+  // Piece h of tile t: 16 bytes along k, the pass's half h.
+  __device__ __forceinline__ i32x4 read(const uint8_t* tile, int t, int h) const {
+    if constexpr (!TURNED) {
+      const uint32_t row = IS_W ? (t / G) * (16 * G) + (t % G) * 4 : t * 16;
+      return *reinterpret_cast<const i32x4*>(tile + at[h] + row * kTileK);
+    } else {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+      // the tile's columns from the reader's: an XOR where they fall within the
+      // pieces that are exchanged
+      uint32_t place = at[0];
+      if constexpr (!IS_W)
+        place = (place ^ ((t % 4) * 32)) + t / 4 * 128;
+      else if constexpr (G == 4)
+        place = (place ^ (((t % 4) / 2) * 16 + (t / 4) % 2 * 128)) + t % 2 * 8 + t / 8 * 256;
+      else
+        place += t * 8;
+      const uint8_t* p = tile + place + h * 32 * O::kRowBytes;
+      i32x2 v[2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        v[half] = __builtin_bit_cast(
+            i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                       (__attribute__((address_space(3))) s16x4*)(p + half * 4 * O::kRowBytes)));
+      const i32x2 lo = v[0], hi = v[1];
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3);
+    }
+  }
+};
+
+// At most LEFT of this wave's loads into LDS are still on their way; then so it
+// is for every wave, and every wave is done with the tile before this one.
+template <int LEFT>
 __device__ __forceinline__ void wait_tiles() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(LEFT) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -341,13 +445,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// e8m0 bytes of TILES rows of 16, for the tile at kTileK: one byte a lane.
-template <int TILES>
-struct Scales {
-  uint32_t offset[TILES];
-  uint32_t now[TILES], next[TILES];
-};
-
 // Which tile a block takes: blocks go round the 8 XCDs, so consecutive tiles
 // are given to every eighth block, and tiles run down 4 rows of tiles before
 // the next column: the blocks of one XCD share rows of x and W in its L2.
@@ -358,16 +455,20 @@ struct Place {
 
 template <int BM, int BN>
 __device__ __forceinline__ Place place_of(const TileArgs& a) {
+  // Quotients are made in vector registers; what is the same in every lane is
+  // taken back to scalar ones, or all that follows from it would stay there.
   const uint32_t tiles = a.tiles_m * a.tiles_n;
   uint32_t id = blockIdx.x;
-  const uint32_t part = id / tiles;
+  const uint32_t part = __builtin_amdgcn_readfirstlane(id / tiles);
   id -= part * tiles;
   const uint32_t each = tiles / 8, more = tiles % 8, xcd = id % 8, k = id / 8;
   id = xcd * each + (xcd < more ? xcd : more) + k;
-  const uint32_t band = id / (4 * a.tiles_n);
+  const uint32_t band = __builtin_amdgcn_readfirstlane(id / (4 * a.tiles_n));
   const uint32_t high = min(4u, a.tiles_m - 4 * band);
   id -= band * 4 * a.tiles_n;
-  return {static_cast<int64_t>(4 * band + id % high) * BM, static_cast<int64_t>(id / high) * BN, part};
+  const uint32_t column = __builtin_amdgcn_readfirstlane(id / high);
+  return {static_cast<int64_t>(4 * band + id - column * high) * BM,
+          static_cast<int64_t>(column) * BN, part};
 }
 
 // The tile's results, written. Lane l of wave (wm, wn) holds in acc[i][j] four
@@ -438,72 +539,96 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Place& at, u
   }
 }
 
-template <int OP, int BM, int BN, int WM, int WN, bool DMA>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
+// ---------------------------------------------------------------------------
+// Tile kernel
+//
+// Small and middling products: blocks are few or the tiles small, so what
+// counts is the time from one tile to the next. With DMA, STAGES tiles are in
+// LDS and all but one of them on their way; block scales (kMX, where a
+// row's come by the four) go the same way. Through registers there are two
+// stages, and block scales are read for each tile by the lanes that use them.
+//
+// 64 x 64 tiles in three stages (three blocks to a CU): 512 x 4096 x 4096 in
+// bf16 27.3 us, two stages 33.6, four 27.7. 128 x 128 in two stages (two blocks
+// to a CU, which fill each other's waits): 1024 x 4096 x 4096 44 us, three or
+// four stages and one block 50. Block scales through LDS: 128 x 4096 x 7168 18.3
+// us, by each lane 23.9. At least two waves to a SIMD are asked for: with more
+// registers than that the compiler moves results between the two register
+// files (1024 x 4096 x 4096: 49.6 us).
+// ---------------------------------------------------------------------------
+
+template <int OP, int BM, int BN, int WM, int WN, int STAGES, bool DMA, bool TX, bool TW>
+__global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a) {
   constexpr int kThreads = 64 * WM * WN;
   constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
   constexpr int G = group_of(TJ);
-  constexpr int SH = log2_of<4 * G>();
   constexpr int ELEM = is8(OP) ? 1 : 2;
-  constexpr int kSteps = is8(OP) ? 1 : 2;
-  __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kTileK];
+  constexpr int kStages = DMA ? STAGES : 2;
+  constexpr uint32_t kBuffer = (BM + BN) * kTileK;
+  constexpr bool kScales = OP == kOpMX;
+  typedef Operand<BM, kThreads, TX, false, 1, DMA, ELEM> OpX;
+  typedef Operand<BN, kThreads, TW, true, G, DMA, ELEM> OpW;
+  constexpr int kLoads = OpX::Q + OpW::Q + (kScales ? 1 : 0);  // of a wave, for a tile
+  static_assert(!kScales || BM + BN <= kThreads, "a scale load for each row");
+  __shared__ __align__(1024) uint8_t lds[kStages][kBuffer];
+  __shared__ __align__(1024) uint8_t scales[kStages][kScales && DMA ? kThreads * 4 : 16];
 
   const Place place = place_of<BM, BN>(a);
-  const int64_t m0 = place.m0, n0 = place.n0;
-  const uint32_t part = place.part;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const uint32_t lane = threadIdx.x % 64, g = lane / 16;
   const uint32_t wm = wave / WN, wn = wave % WN;
+  OpX lx;
+  OpW lw;
+  lx.init(a.x, place.m0, a.kbytes);
+  lw.init(a.w, place.n0, a.kbytes);
+  Reader<OpX, TX, false, 1> rx;
+  Reader<OpW, TW, true, G> rw;
+  rx.init(wm * (TI * 16));
+  rw.init(wn * (TJ * 16));
 
-  Loader<BM, kThreads, 2, DMA, ELEM> lx;
-  Loader<BN, kThreads, SH, DMA, ELEM> lw;
-  lx.init(a.x, m0, a.M, a.ldx);
-  lw.init(a.w, n0, a.N, a.ldw);
-
-  // Place of this lane's reads: x rows 16 apart, W rows 4 apart in a group.
-  const uint32_t xrow = wm * (TI * 16) + low;
-  const uint32_t wrow = wn * (TJ * 16) + (low / 4) * (4 * G) + low % 4;
-
-  Scales<OP == kOpMX ? TI : 1> sx;
-  Scales<OP == kOpMX ? TJ : 1> sw;
+  // Block scales. DMA: thread r brings the 4 bytes of row r, x's then W's.
+  // Else: each lane the bytes of its own rows; rows past the end read the last
+  // row's (their values are zeros), and past the last block of a row any finite
+  // scale does (those values are zeros too).
   const uint32_t kblocks = (a.kbytes + 31) / 32;
-  if constexpr (OP == kOpMX) {
-    // rows past the end read the last row's scales: their values are zeros
+  i32x4 sr = {0, 0, 0, 0};
+  uint32_t so = kOutside;
+  uint32_t ox[kScales && !DMA ? TI : 1], ow[kScales && !DMA ? TJ : 1];
+  uint32_t sx[kScales ? TI : 1], sw[kScales ? TJ : 1], nx[kScales ? TI : 1], nw[kScales ? TJ : 1];
+  const uint8_t* xs = kScales ? a.xs + place.m0 * kblocks : nullptr;
+  const uint8_t* ws = kScales ? a.ws + place.n0 * kblocks : nullptr;
+  sx[0] = sw[0] = 0;
+  if constexpr (kScales && DMA) {
+    const bool of_x = wave < BM / 64;
+    const uint32_t r = threadIdx.x - (of_x ? 0 : BM);
+    sr = buffer_of(of_x ? xs : ws, static_cast<int64_t>(of_x ? lx.here : lw.here) * kblocks);
+    if (r < (of_x ? lx.here : lw.here)) so = r * kblocks;
+  } else if constexpr (kScales) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
-      sx.offset[i] = static_cast<uint32_t>(min(m0 + xrow + 16 * i, a.M - 1) - m0) * kblocks + g;
+    for (int i = 0; i < TI; ++i) ox[i] = min(rx.row_of(wm * (TI * 16), i), lx.here - 1) * kblocks + g;
 #pragma unroll
-    for (int j = 0; j < TJ; ++j)
-      sw.offset[j] = static_cast<uint32_t>(
-          min(n0 + wrow + (j / G) * (16 * G) + (j % G) * 4, a.N - 1) - n0) * kblocks + g;
+    for (int j = 0; j < TJ; ++j) ow[j] = min(rw.row_of(wn * (TJ * 16), j), lw.here - 1) * kblocks + g;
   }
-  const uint8_t* xs = OP == kOpMX ? a.xs + m0 * kblocks : nullptr;
-  const uint8_t* ws = OP == kOpMX ? a.ws + n0 * kblocks : nullptr;
-  const auto start_scales = [&](uint32_t kt) {
-    if constexpr (OP == kOpMX) {
-      // past the last block of a row the values are zeros; any finite scale does
-      const uint32_t at = kt * 4 + g < kblocks ? kt * 4 : 0;
+  const auto read_scales = [&](uint32_t kt) {
+    if constexpr (kScales && !DMA) {
       const bool in = kt * 4 + g < kblocks;
 #pragma unroll
-      for (int i = 0; i < TI; ++i) sx.next[i] = in ? xs[sx.offset[i] + at] : 0;
+      for (int i = 0; i < TI; ++i) nx[i] = in ? xs[ox[i] + kt * 4] : 0;
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) sw.next[j] = in ? ws[sw.offset[j] + at] : 0;
+      for (int j = 0; j < TJ; ++j) nw[j] = in ? ws[ow[j] + kt * 4] : 0;
     }
   };
-  // The scales are settled before the next tile's loads are started, so that
-  // waiting for them never waits for those.
-  const auto take_scales = [&]() {
-    if constexpr (OP == kOpMX) {
+  const auto take_scales = [&](uint32_t stage) {
+    if constexpr (kScales && DMA) {
 #pragma unroll
-      for (int i = 0; i < TI; ++i) {
-        asm volatile("" : "+v"(sx.next[i]));
-        sx.now[i] = sx.next[i];
-      }
+      for (int i = 0; i < TI; ++i) sx[i] = scales[stage][rx.row_of(wm * (TI * 16), i) * 4 + g];
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        asm volatile("" : "+v"(sw.next[j]));
-        sw.now[j] = sw.next[j];
-      }
+      for (int j = 0; j < TJ; ++j) sw[j] = scales[stage][(BM + rw.row_of(wn * (TJ * 16), j)) * 4 + g];
+    } else if constexpr (kScales) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i) sx[i] = nx[i];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) sw[j] = nw[j];
     }
   };
 
@@ -512,70 +637,72 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
   for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
   const auto multiply = [&](const uint8_t* tile) {
-    const uint8_t* tx = tile + xrow * kTileK;
-    const uint8_t* tw = tile + BM * kTileK + wrow * kTileK;
-    const uint32_t fx = swap_of<2>(low) * 16;
+    constexpr int kHalves = is8(OP) ? 1 : 2;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int h = 0; h < kHalves; ++h) {
       Frag<OP> fw[TJ];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        const uint32_t row = (j / G) * (16 * G) + (j % G) * 4;
-        const uint32_t f = swap_of<SH>(wrow + row) * 16;
-        const uint8_t* p = tw + row * kTileK;
-        if constexpr (is8(OP)) {
-          fw[j].w[0] = *reinterpret_cast<const i32x4*>(p + ((g * 16) ^ f));
-          fw[j].w[1] = *reinterpret_cast<const i32x4*>(p + ((64 + g * 16) ^ f));
-        } else {
-          fw[j].w[0] = *reinterpret_cast<const i32x4*>(p + ((s * 64 + g * 16) ^ f));
-        }
+        fw[j].w[0] = rw.read(tile + BM * kTileK, j, h);
+        if constexpr (is8(OP)) fw[j].w[1] = rw.read(tile + BM * kTileK, j, 1);
       }
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         Frag<OP> f;
-        const uint8_t* p = tx + i * 16 * kTileK;
-        if constexpr (is8(OP)) {
-          f.w[0] = *reinterpret_cast<const i32x4*>(p + ((g * 16) ^ fx));
-          f.w[1] = *reinterpret_cast<const i32x4*>(p + ((64 + g * 16) ^ fx));
-        } else {
-          f.w[0] = *reinterpret_cast<const i32x4*>(p + ((s * 64 + g * 16) ^ fx));
-        }
+        f.w[0] = rx.read(tile, i, h);
+        if constexpr (is8(OP)) f.w[1] = rx.read(tile, i, 1);
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
-          acc[i][j] = mma<OP>(fw[j], f, acc[i][j], static_cast<int>(sw.now[OP == kOpMX ? j : 0]),
-                              static_cast<int>(sx.now[OP == kOpMX ? i : 0]));
+          acc[i][j] = mma<OP>(fw[j], f, acc[i][j], static_cast<int>(sw[kScales ? j : 0]),
+                              static_cast<int>(sx[kScales ? i : 0]));
       }
     }
   };
 
   const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
-  const uint32_t first = part * a.per_split;
+  const uint32_t first = place.part * a.per_split;
   const uint32_t last = min(all, first + a.per_split);
-  const uint32_t at0 = lds_address(&lds[0][0]);
-  constexpr uint32_t kBuffer = (BM + BN) * kTileK;
-  sx.now[0] = sw.now[0] = 0;
-  if (first < last) {
-    lx.start(first * kTileK, a.kbytes, at0);
-    lw.start(first * kTileK, a.kbytes, at0 + BM * kTileK);
-    start_scales(first);
-  }
-  for (uint32_t kt = first; kt < last; ++kt) {
-    const uint32_t b = (kt - first) & 1;
-    lx.put(lds[b]);
-    lw.put(lds[b] + BM * kTileK);
-    take_scales();
-    wait_tiles();
-    if (kt + 1 < last) {
-      const uint32_t to = at0 + (b ^ 1) * kBuffer;
-      lx.start((kt + 1) * kTileK, a.kbytes, to);
-      lw.start((kt + 1) * kTileK, a.kbytes, to + BM * kTileK);
-      start_scales(kt + 1);
+  const uint32_t at0 = lds_address(&lds[0][0]), at1 = lds_address(&scales[0][0]);
+  // DMA: past the last tile zeros are loaded, so that each tile is as many loads.
+  const auto start = [&](uint32_t kt, uint32_t stage) {
+    const uint32_t to = at0 + stage * kBuffer;
+#pragma unroll
+    for (int q = 0; q < OpX::Q; ++q) lx.start(kt, a.kbytes, to, q);
+#pragma unroll
+    for (int q = 0; q < OpW::Q; ++q) lw.start(kt, a.kbytes, to + BM * kTileK, q);
+    if constexpr (kScales && DMA)
+      load_to_lds<4>(kt < all ? so : kOutside, sr, kt * 4, at1 + stage * (kThreads * 4) + wave * 256);
+  };
+  if constexpr (DMA) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) start(first + s, s);
+    uint32_t stage = 0;
+    for (uint32_t kt = first; kt < last; ++kt) {
+      wait_tiles<(kStages - 2) * kLoads>();
+      start(kt + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      take_scales(stage);
+      multiply(lds[stage]);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    multiply(lds[b]);
+    wait_tiles<0>();  // nothing arrives in LDS any more
+  } else {
+    start(first, 0);
+    read_scales(first);
+    for (uint32_t kt = first; kt < last; ++kt) {
+      const uint32_t b = (kt - first) & 1;
+      lx.put(lds[b]);
+      lw.put(lds[b] + BM * kTileK);
+      take_scales(b);
+      __syncthreads();
+      if (kt + 1 < last) {
+        start(kt + 1, b ^ 1);
+        read_scales(kt + 1);
+      }
+      multiply(lds[b]);
+    }
   }
-  write_tile<OP, BM, BN, WM, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
+  write_tile<OP, BM, BN, WM, WN, kStages * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -601,11 +728,12 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(TileArgs a) {
 // values, 1880).
 // ---------------------------------------------------------------------------
 
-template <int OP, int WN>
-__global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
-  constexpr int BM = 256, BN = 256, kThreads = 128 * WN;
-  constexpr int TI = 8, TJ = 16 / WN, HALF = TI / 2;
+template <int OP, bool TX, bool TW>
+__global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
+  constexpr int BM = 256, BN = 256, WN = 4, kThreads = 512;
+  constexpr int TI = 8, TJ = 4, HALF = TI / 2;
   constexpr int kPieces = is8(OP) ? 1 : 2;  // matrix instructions for one result in a pass
+  constexpr int ELEM = is8(OP) ? 1 : 2;
   constexpr uint32_t kBuffer = (BM + BN) * kTileK;
   // kMX: the e8m0 bytes of four passes, 16 for each row of x and of W
   constexpr uint32_t kScaleBytes = OP == kOpMX ? (BM + BN) * 16 : 0;
@@ -613,50 +741,37 @@ __global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
   __shared__ __align__(1024) uint8_t scales[2][OP == kOpMX ? kScaleBytes : 16];
   const Place place = place_of<BM, BN>(a);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const uint32_t lane = threadIdx.x % 64, g = lane / 16;
   const uint32_t wm = wave / WN, wn = wave % WN;
 
-  Loader<BM, kThreads, 2, true, 1> lx;
-  Loader<BN, kThreads, 4, true, 1> lw;
-  lx.init(a.x, place.m0, a.M, a.ldx);
-  lw.init(a.w, place.n0, a.N, a.ldw);
-
-  const uint32_t xrow = wm * 128 + low, wrow = wn * (TJ * 16) + (low / 4) * 16 + low % 4;
-  const uint32_t fx = swap_of<2>(xrow) * 16, fw = swap_of<4>(wrow) * 16;
-  // byte places of this lane's pieces: x rows 16 apart, W rows 4 apart in groups 64 apart
-  const uint32_t px[2] = {xrow * kTileK + ((g * 16) ^ fx), xrow * kTileK + ((64 + g * 16) ^ fx)};
-  const uint32_t pw[2] = {BM * kTileK + wrow * kTileK + ((g * 16) ^ fw),
-                          BM * kTileK + wrow * kTileK + ((64 + g * 16) ^ fw)};
+  typedef Operand<BM, kThreads, TX, false, 1, true, ELEM> OpX;
+  typedef Operand<BN, kThreads, TW, true, 4, true, ELEM> OpW;
+  static_assert(OpX::Q == TJ && OpW::Q == TJ, "one round of loads for each W tile");
+  OpX lx;
+  OpW lw;
+  lx.init(a.x, place.m0, a.kbytes);
+  lw.init(a.w, place.n0, a.kbytes);
+  Reader<OpX, TX, false, 1> rx;
+  Reader<OpW, TW, true, 4> rw;
+  rx.init(wm * (TI * 16));
+  rw.init(wn * (TJ * 16));
 
   // kMX: each of the first four waves brings the bytes of 64 x rows, the others of 64 W rows.
   const uint32_t kblocks = a.kbytes / 32;
   uint32_t so = 0;
   i32x4 sr = {0, 0, 0, 0};
   if constexpr (OP == kOpMX) {
-    const uint32_t thread = threadIdx.x % 256;
-    const bool of_x = __builtin_amdgcn_readfirstlane(threadIdx.x / 256) == 0;
-    const int64_t row0 = of_x ? place.m0 : place.n0, left = (of_x ? a.M : a.N) - row0;
-    const uint32_t here = static_cast<uint32_t>(left < 256 ? left : 256);
-    const uint64_t p = reinterpret_cast<uint64_t>((of_x ? a.xs : a.ws) + row0 * kblocks);
-    sr = i32x4{static_cast<int32_t>(p), static_cast<int32_t>(p >> 32),
-               static_cast<int32_t>(here * kblocks), kRsrcFormat};
-    so = thread < here ? thread * kblocks : kOutside;
+    const bool of_x = wave < 4;
+    const uint32_t r = threadIdx.x % 256, here = of_x ? lx.here : lw.here;
+    sr = buffer_of(of_x ? a.xs + place.m0 * kblocks : a.ws + place.n0 * kblocks,
+                   static_cast<int64_t>(here) * kblocks);
+    so = r < here ? r * kblocks : kOutside;
   }
-  const uint32_t at0 = lds_address(&lds[0][0]);
-  const uint32_t at1 = lds_address(&scales[0][0]);
-  // The range check of a buffer counts the scalar offset too, so rows past the
-  // end read zeros from one offset a lane and a scalar for each load's rows.
-  const uint32_t ox = threadIdx.x / 8 * static_cast<uint32_t>(a.ldx) + lx.piece[0];
-  const uint32_t ow = threadIdx.x / 8 * static_cast<uint32_t>(a.ldw) + lw.piece[0];
-  // Loads of the tile at kt into buffer b, a part of them a call.
+  const uint32_t at0 = lds_address(&lds[0][0]), at1 = lds_address(&scales[0][0]);
   const auto start = [&](uint32_t kt, uint32_t b, int q) {
-    const uint32_t to = at0 + b * kBuffer + (q * kThreads + wave * 64) * 16;
-    const uint32_t k = kt * kTileK;
-    const uint32_t rows = q * (kThreads / 8);
-    load_to_lds<16>(k + lx.piece[0] < a.kbytes ? ox : kOutside, lx.rsrc, k + rows * static_cast<uint32_t>(a.ldx), to);
-    load_to_lds<16>(k + lw.piece[0] < a.kbytes ? ow : kOutside, lw.rsrc, k + rows * static_cast<uint32_t>(a.ldw), to + BM * kTileK);
+    lx.start(kt, a.kbytes, at0 + b * kBuffer, q);
+    lw.start(kt, a.kbytes, at0 + b * kBuffer + BM * kTileK, q);
   };
-
   // kMX: the scales of four tiles from kt on, 16 bytes of each row.
   const auto start_scales = [&](uint32_t kt, uint32_t b) {
     if constexpr (OP == kOpMX)
@@ -673,17 +788,14 @@ __global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
     return OP == kOpMX ? scales[step / 4 % 2][row * 16 + step % 4 * 4 + g] : 0;
   };
   const auto read_w = [&](uint32_t b, uint32_t step, int j) {
-    const uint32_t row = (j / 4) * 64 + (j % 4) * 4;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[j].w[h] = *reinterpret_cast<const i32x4*>(&lds[0][0] + b * kBuffer + pw[h] + row * kTileK);
-    w[j].s = scale_at(step, BM + wrow + row);
+    for (int h = 0; h < 2; ++h) w[j].w[h] = rw.read(lds[b] + BM * kTileK, j, h);
+    w[j].s = scale_at(step, BM + rw.row_of(wn * (TJ * 16), j));
   };
   const auto read_x = [&](uint32_t b, uint32_t step, int i, Row& r) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      r.w[h] = *reinterpret_cast<const i32x4*>(&lds[0][0] + b * kBuffer + px[h] + i * 16 * kTileK);
-    r.s = scale_at(step, xrow + i * 16);
+    for (int h = 0; h < 2; ++h) r.w[h] = rx.read(lds[b], i, h);
+    r.s = scale_at(step, rx.row_of(wm * (TI * 16), i));
   };
 
   f32x4 acc[TI][TJ];
@@ -713,7 +825,7 @@ __global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
 #pragma unroll
   for (int q = 0; q < TJ; ++q) start(first, 0, q);
   start_scales(first, 0);
-  wait_tiles();
+  wait_tiles<0>();
 #pragma unroll
   for (int q = 0; q < TJ; ++q) start(first + 1, 1, q);
 #pragma unroll
@@ -730,7 +842,7 @@ __global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
-    wait_tiles();
+    wait_tiles<0>();
     if (step % 4 == 2) start_scales(kt + 2, (step + 2) / 4 % 2);
     // past the last tile: zeros are loaded and old values read, and neither is used
 #pragma unroll
@@ -744,7 +856,7 @@ __global__ __launch_bounds__(128 * WN) void linear_large_kernel(TileArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  wait_tiles();  // nothing arrives in LDS any more
+  wait_tiles<0>();  // nothing arrives in LDS any more
   write_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
 
@@ -909,9 +1021,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
 // Backward
 //
 // gz and the bias's sums come from one pass over grad_out and z; the two
-// products read their operands along the sum, so W, x and gz are laid out
-// transposed in the workspace first (rows padded with zeros to a multiple of 8,
-// so that every row is 16-byte aligned).
+// products are tile kernels whose operands are turned on their way out of LDS.
 // ---------------------------------------------------------------------------
 
 // gz = rnd(grad_out * act'(z)) where gz is given, and this block's rows of the
@@ -968,41 +1078,6 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restric
   out[n] = narrow<F>(s);
 }
 
-// out [C, ld] = in [R, C] transposed, 16-bit values, zeros from R to ld (a
-// multiple of 8). A block moves 64 x 64 through LDS.
-__global__ __launch_bounds__(256) void linear_transpose_kernel(const uint16_t* __restrict__ in,
-                                                               uint16_t* __restrict__ out,
-                                                               int64_t R, int64_t C, int64_t ld,
-                                                               uint32_t tiles_c) {
-  __shared__ uint16_t tile[64][66];
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles_c) * 64;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x % tiles_c) * 64;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int row = q * 32 + threadIdx.x / 8, col = (threadIdx.x % 8) * 8;
-    Chunk<kBF16> c = zero_chunk<kBF16>();
-    if (r0 + row < R && c0 + col < C)
-      c = load_chunk<kBF16>(in + (r0 + row) * C + c0 + col,
-                            static_cast<int>(min(C - c0 - col, static_cast<int64_t>(8))));
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      tile[row][col + i] = static_cast<uint16_t>(c.w[0][i / 2] >> (16 * (i % 2)));
-  }
-  __syncthreads();
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int col = q * 32 + threadIdx.x / 8, row = (threadIdx.x % 8) * 8;
-    if (c0 + col < C && r0 + row < ld) {
-      Chunk<kBF16> c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        c.w[0][i] = static_cast<uint32_t>(tile[row + 2 * i][col]) |
-                    (static_cast<uint32_t>(tile[row + 2 * i + 1][col]) << 16);
-      store_chunk<kBF16>(out + (c0 + col) * ld + r0 + row, 8, c);
-    }
-  }
-}
-
 __global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* __restrict__ p, int64_t count) {
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < count; i += step)
@@ -1043,6 +1118,7 @@ mhc_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
 }
 
 constexpr int32_t kMaxSplits = 64;
+constexpr int kMediumStages = 2;  // see the tile kernel
 
 mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
                      const mhc_linear_launch* launch, mhc_linear_launch* plan) {
@@ -1125,38 +1201,53 @@ mhc_status validate_fwd(const void* x, const void* xs, const void* w, const void
   return check_tensors(in, outs);
 }
 
-bool whole_pieces(const TileArgs& a) {
-  return reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0 &&
-         a.ldx % 16 == 0 && a.ldw % 16 == 0 && a.kbytes % 16 == 0;
+// Whether an operand can be loaded straight into LDS: whole, aligned 16-byte
+// pieces, and where k runs down the rows all of it within a buffer's 31 bits.
+template <bool TURNED>
+bool whole(const Matrix& m, uint32_t kbytes) {
+  if (reinterpret_cast<uintptr_t>(m.p) % 16 != 0 || m.ld % 16 != 0) return false;
+  return TURNED ? static_cast<int64_t>(kbytes / 2) * m.ld <= INT32_MAX : kbytes % 16 == 0;
 }
 
-template <int OP, int BM, int BN, int WM, int WN>
+template <int OP, bool TX, bool TW>
+bool straight(const TileArgs& a) {
+  if (!whole<TX>(a.x, a.kbytes) || !whole<TW>(a.w, a.kbytes)) return false;
+  // block scales come four of a row at a time
+  return OP != kOpMX || (a.kbytes % kTileK == 0 && reinterpret_cast<uintptr_t>(a.xs) % 4 == 0 &&
+                         reinterpret_cast<uintptr_t>(a.ws) % 4 == 0);
+}
+
+template <int OP, int BM, int BN, int WM, int WN, int STAGES, bool TX, bool TW>
 hipError_t launch_tile(TileArgs a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
   a.tiles_m = static_cast<uint32_t>(ceil_div(a.M, BM));
   a.tiles_n = static_cast<uint32_t>(ceil_div(a.N, BN));
   const dim3 grid(a.tiles_m * a.tiles_n * a.splits), block(64 * WM * WN);
-  // straight into LDS only from rows that are whole 16-byte pieces
-  if (whole_pieces(a))
-    return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, true>, grid, block, s, start, stop, a);
-  return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, false>, grid, block, s, start, stop, a);
-}
-
-// The large tiles take whole pieces only (and scales by the four); other
-// operands go through the medium tiles, whose sums have the same order.
-template <int OP>
-hipError_t launch_large(TileArgs a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
-  const bool scales = OP != kOpMX || (a.kbytes % kTileK == 0 &&
-                                      reinterpret_cast<uintptr_t>(a.xs) % 4 == 0 &&
-                                      reinterpret_cast<uintptr_t>(a.ws) % 4 == 0);
-  if (!whole_pieces(a) || !scales) return launch_tile<OP, 128, 128, 2, 2>(a, s, start, stop);
-  a.tiles_m = static_cast<uint32_t>(ceil_div(a.M, 256));
-  a.tiles_n = static_cast<uint32_t>(ceil_div(a.N, 256));
-  return launch_kernel(linear_large_kernel<OP, 4>, dim3(a.tiles_m * a.tiles_n * a.splits), dim3(512),
+  if (straight<OP, TX, TW>(a))
+    return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, STAGES, true, TX, TW>, grid, block,
+                         s, start, stop, a);
+  return launch_kernel(linear_tile_kernel<OP, BM, BN, WM, WN, STAGES, false, TX, TW>, grid, block,
                        s, start, stop, a);
 }
 
-// One product and its epilogue, as planned.
-template <int OP>
+template <int OP, bool TX, bool TW>
+hipError_t launch_medium(const TileArgs& a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  return launch_tile<OP, 128, 128, 2, 2, kMediumStages, TX, TW>(a, s, start, stop);
+}
+
+// The large tiles are loaded straight into LDS only; other operands go through
+// the medium tiles, whose sums have the same order.
+template <int OP, bool TX, bool TW>
+hipError_t launch_large(TileArgs a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  if (!straight<OP, TX, TW>(a)) return launch_medium<OP, TX, TW>(a, s, start, stop);
+  a.tiles_m = static_cast<uint32_t>(ceil_div(a.M, 256));
+  a.tiles_n = static_cast<uint32_t>(ceil_div(a.N, 256));
+  return launch_kernel(linear_large_kernel<OP, TX, TW>, dim3(a.tiles_m * a.tiles_n * a.splits),
+                       dim3(512), s, start, stop, a);
+}
+
+// One product and its epilogue, as planned. The backward's products (TW) have
+// no narrow form.
+template <int OP, bool TX, bool TW>
 hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t s,
                           hipEvent_t start, hipEvent_t stop) {
   const int64_t all = ceil_div(a.kbytes, kTileK);
@@ -1166,10 +1257,14 @@ hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t
   const hipEvent_t end = join ? nullptr : stop;
   hipError_t e;
   switch (plan.kernel) {
-    case MHC_LINEAR_NARROW: e = launch_tile<OP, 64, 32, 4, 1>(a, s, start, end); break;
-    case MHC_LINEAR_SMALL: e = launch_tile<OP, 64, 64, 2, 2>(a, s, start, end); break;
-    case MHC_LINEAR_MEDIUM: e = launch_tile<OP, 128, 128, 2, 2>(a, s, start, end); break;
-    default: e = launch_large<OP>(a, s, start, end); break;
+    case MHC_LINEAR_NARROW:
+      if constexpr (!TW) {
+        e = launch_tile<OP, 64, 32, 4, 1, 3, TX, TW>(a, s, start, end);
+        break;
+      }
+    case MHC_LINEAR_SMALL: e = launch_tile<OP, 64, 64, 2, 2, 3, TX, TW>(a, s, start, end); break;
+    case MHC_LINEAR_MEDIUM: e = launch_medium<OP, TX, TW>(a, s, start, end); break;
+    default: e = launch_large<OP, TX, TW>(a, s, start, end); break;
   }
   if (e != hipSuccess || !join) return e;
   const int64_t blocks = ceil_div(a.M * ceil_div(a.N, 8), 256);
@@ -1179,7 +1274,7 @@ hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t
 
 template <int OP>
 hipError_t launch_rows(const TileArgs& t, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
-  const RowsArgs a = {static_cast<const uint8_t*>(t.x), static_cast<const uint8_t*>(t.w), t.xs,
+  const RowsArgs a = {static_cast<const uint8_t*>(t.x.p), static_cast<const uint8_t*>(t.w.p), t.xs,
                       t.ws, t.M, t.N, t.kbytes, t.e};
   const dim3 grid(static_cast<uint32_t>(ceil_div(t.N, 16)));
   return launch_kernel(linear_rows_kernel<OP, 8>, grid, dim3(512), s, start, stop, a);
@@ -1189,7 +1284,7 @@ template <int OP>
 hipError_t launch_fwd(const TileArgs& a, const mhc_linear_launch& plan, hipStream_t s,
                       hipEvent_t start, hipEvent_t stop) {
   if (plan.kernel == MHC_LINEAR_ROWS) return launch_rows<OP>(a, s, start, stop);
-  return launch_product<OP>(a, plan, s, start, stop);
+  return launch_product<OP, false, false>(a, plan, s, start, stop);
 }
 
 // --- backward ---
@@ -1201,33 +1296,36 @@ int64_t bias_rows(int64_t M) {
 }
 
 struct BwdPlan {
-  int64_t ldn, ldm;           // padded rows (elements) along N and along M
-  int64_t gz, wt, xt, gzt, bias, part, total;  // byte offsets in the workspace; part: split sums
-  mhc_linear_launch px, pw;   // the two products
+  int64_t gz, bias, part, total;  // byte offsets in the workspace; part: split sums
+  mhc_linear_launch px, pw;       // the two products
 };
 
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 
+// A product of the backward: the tile kernels from 64 x 64 on.
+mhc_status plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, mhc_linear_launch* p) {
+  const mhc_status st = make_plan(M, N, K, dtype, nullptr, p);
+  if (st != MHC_SUCCESS || p->kernel >= MHC_LINEAR_SMALL) return st;
+  const mhc_linear_launch small = {MHC_LINEAR_SMALL, 0};
+  return make_plan(M, N, K, dtype, &small, p);
+}
+
 // -1 in total where a size does not fit.
 BwdPlan plan_bwd(int64_t M, int64_t N, int64_t K, int32_t dtype) {
   BwdPlan p = {};
-  p.ldn = round_up(N, 8);
-  p.ldm = round_up(M, 8);
   if (M == 0) return p;
   int64_t at = 0;
   bool bad = false;
   const auto take = [&](int64_t bytes) {
     const int64_t here = at;
-    if (bytes < 0 || __builtin_add_overflow(at, round_up(bytes, 256), &at)) bad = true;
+    if (bytes < 0 || bytes > INT64_MAX - 256 || __builtin_add_overflow(at, round_up(bytes, 256), &at))
+      bad = true;
     return here;
   };
-  p.gz = take(mul_bytes(M, p.ldn, 2));
-  p.wt = take(mul_bytes(K, p.ldn, 2));
-  p.xt = take(mul_bytes(K, p.ldm, 2));
-  p.gzt = take(mul_bytes(N, p.ldm, 2));
+  p.gz = take(mul_bytes(M, N, 2));
   p.bias = take(mul_bytes(ceil_div(M, bias_rows(M)), N, 4));
-  if (make_plan(M, K, p.ldn, dtype, nullptr, &p.px) != MHC_SUCCESS ||
-      make_plan(N, K, p.ldm, dtype, nullptr, &p.pw) != MHC_SUCCESS)
+  if (plan_product(M, K, N, dtype, &p.px) != MHC_SUCCESS ||
+      plan_product(N, K, M, dtype, &p.pw) != MHC_SUCCESS)
     bad = true;
   const int64_t a = fwd_workspace(M, K, p.px), b = fwd_workspace(N, K, p.pw);
   p.part = take(a < 0 || b < 0 ? -1 : a > b ? a : b);
@@ -1279,14 +1377,6 @@ struct BwdArgs {
   int64_t M, N, K;
   int32_t act;
 };
-
-hipError_t launch_transpose(const void* in, void* out, int64_t R, int64_t C, int64_t ld,
-                            hipStream_t s, hipEvent_t start) {
-  const int64_t tc = ceil_div(C, 64), tr = ceil_div(ld, 64);
-  return launch_kernel(linear_transpose_kernel, dim3(static_cast<uint32_t>(tc * tr)), dim3(256), s,
-                       start, nullptr, static_cast<const uint16_t*>(in),
-                       static_cast<uint16_t*>(out), R, C, ld, static_cast<uint32_t>(tc));
-}
 
 hipError_t launch_zero(void* p, int64_t count, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
   const int64_t blocks = ceil_div(count, 256);
@@ -1342,38 +1432,27 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
       }
     }
     if (a.gx != nullptr) {
-      // grad_x [M, K] = gz [M, N] . (W^T [K, N])^T; gz's rows are used as they are
-      e = launch_transpose(a.w, a.ws + p.wt, a.N, a.K, p.ldn, s, marks.first());
-      if (e != hipSuccess) return e;
+      // grad_x [M, K]: rows of gz, with W [N, K] turned
       TileArgs t = {};
-      t.x = gz;
-      t.w = a.ws + p.wt;
+      t.x = {gz, a.M, a.N * 2};
+      t.w = {a.w, a.K, a.K * 2};
       t.M = a.M; t.N = a.K;
-      t.ldx = a.N * 2; t.ldw = p.ldn * 2;
       t.kbytes = static_cast<uint32_t>(a.N * 2);
       t.partial = reinterpret_cast<float*>(a.ws + p.part);
       t.e.out = a.gx; t.e.N = a.K;
-      mhc_linear_launch plan = p.px;
-      if (plan.kernel == MHC_LINEAR_ROWS) plan = {MHC_LINEAR_SMALL, 1};
-      e = launch_product<OP>(t, plan, s, nullptr, nullptr);
+      e = launch_product<OP, false, true>(t, p.px, s, marks.first(), nullptr);
       if (e != hipSuccess) return e;
     }
     if (a.gw != nullptr) {
-      // grad_weight [N, K] = gz^T [N, M] . (x^T [K, M])^T
-      e = launch_transpose(gz, a.ws + p.gzt, a.M, a.N, p.ldm, s, marks.first());
-      if (e == hipSuccess) e = launch_transpose(a.x, a.ws + p.xt, a.M, a.K, p.ldm, s, nullptr);
-      if (e != hipSuccess) return e;
+      // grad_weight [N, K]: gz [M, N] and x [M, K], both turned
       TileArgs t = {};
-      t.x = a.ws + p.gzt;
-      t.w = a.ws + p.xt;
+      t.x = {gz, a.N, a.N * 2};
+      t.w = {a.x, a.K, a.K * 2};
       t.M = a.N; t.N = a.K;
-      t.ldx = t.ldw = p.ldm * 2;
-      t.kbytes = static_cast<uint32_t>(p.ldm * 2);
+      t.kbytes = static_cast<uint32_t>(a.M * 2);
       t.partial = reinterpret_cast<float*>(a.ws + p.part);
       t.e.out = a.gw; t.e.N = a.K;
-      mhc_linear_launch plan = p.pw;
-      if (plan.kernel == MHC_LINEAR_ROWS) plan = {MHC_LINEAR_SMALL, 1};
-      e = launch_product<OP>(t, plan, s, nullptr, nullptr);
+      e = launch_product<OP, true, true>(t, p.pw, s, marks.first(), nullptr);
     }
   }
   if (e == hipSuccess && marks.start != nullptr) e = hipEventRecord(marks.first(), s);
@@ -1443,8 +1522,9 @@ mhc_status mhc_linear_fwd(const void* x, const void* x_scales, const void* weigh
   if (st != MHC_SUCCESS) return st;
   if (M == 0) return record_empty(stream, start_event, stop_event);
   TileArgs a = {};
-  a.x = x;
-  a.w = weight;
+  const int64_t ld = K * elem(dtype);
+  a.x = {x, M, ld};
+  a.w = {weight, N, ld};
   if (dtype == MHC_LINEAR_E4M3_MX) {
     a.xs = static_cast<const uint8_t*>(x_scales);
     a.ws = static_cast<const uint8_t*>(weight_scales);
@@ -1454,8 +1534,7 @@ mhc_status mhc_linear_fwd(const void* x, const void* x_scales, const void* weigh
   }
   a.M = M;
   a.N = N;
-  a.ldx = a.ldw = K * elem(dtype);
-  a.kbytes = static_cast<uint32_t>(K * elem(dtype));
+  a.kbytes = static_cast<uint32_t>(ld);
   a.partial = static_cast<float*>(workspace);
   a.e.bias = bias;
   a.e.residual = residual;

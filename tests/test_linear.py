@@ -441,9 +441,24 @@ def test_backward_sizes(device, kind, activation):
 
 
 @pytest.mark.gpu
-def test_backward_large_tiles(device):
-    """Sizes at which both products take the largest tiles, with ragged edges."""
-    check_backward(device, "bf16", 4000, 3700, 260, "gelu", seed=1)
+@pytest.mark.parametrize("M,N,K", [(3800, 3704, 3528), (3801, 3704, 3592), (2100, 2050, 1000), (130, 1024, 3000)])
+def test_backward_large_tiles(device, M, N, K):
+    """Sizes at which the products take the large and the middling tiles, with ragged edges; fp64 on the GPU."""
+    from hyper_connection_residual_mhc_amd import linear as L
+    say(f"backward M={M} N={N} K={K}")
+    gen = torch.Generator(device=device).manual_seed(M)
+    g, x, w = (torch.randn(s, device=device, generator=gen).to(BF16) for s in ((M, N), (M, K), (N, K)))
+    gx, gw, gb = L.linear_backward(g, x, w, bias=True)
+    for got, want, size, length in ((gx, g.double() @ w.double(), g.double().abs() @ w.double().abs(), N),
+                                    (gw, g.double().t() @ x.double(), g.double().abs().t() @ x.double().abs(), M)):
+        tol = size * additions(length, 32) * STEP
+        tol = tol + (want.abs() + tol) * R.HALF_STEP[BF16] + R.HALF_TINY[BF16]
+        over = (got.double() - want).abs() - tol
+        assert float(over.max()) <= 0, int((over > 0).sum())
+    want = g.double().sum(0)
+    rows = max(32, math.ceil(M / 256))
+    tol = g.double().abs().sum(0) * (math.ceil(rows / 4) + 4 + math.ceil(M / rows)) * STEP
+    assert float(((gb.double() - want).abs() - tol - (want.abs() + tol) * R.HALF_STEP[BF16]).max()) <= 0
 
 
 @pytest.mark.gpu
