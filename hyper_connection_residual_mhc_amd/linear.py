@@ -10,13 +10,14 @@ missing library raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Mapping, NamedTuple
 
 import torch
 
 from . import _lib
+from ._call import address, on, require, stream_handle, workspace_of
 from ._lib import check_linear, mhc_linear_launch
-from .ops import _require, _stream_handle
 
 _DTYPES = {torch.bfloat16: _lib.MHC_LINEAR_BF16, torch.float16: _lib.MHC_LINEAR_F16}
 ACTIVATIONS = {"none": _lib.MHC_ACT_NONE, "relu": _lib.MHC_ACT_RELU, "silu": _lib.MHC_ACT_SILU,
@@ -58,37 +59,35 @@ def _operands(x: torch.Tensor, weight: torch.Tensor, x_scales, weight_scales
     if x.dtype in _DTYPES:
         if x_scales is not None or weight_scales is not None:
             raise ValueError("scales need float8_e4m3fn operands")
-        _require(x, "x", x.dtype, (M, K))
-        _require(weight, "weight", x.dtype, (N, K), dev)
+        require(x, "x", x.dtype, (M, K), dev)
+        require(weight, "weight", x.dtype, (N, K), dev)
         return M, N, K, _DTYPES[x.dtype], x.dtype
     if x.dtype != torch.float8_e4m3fn:
         raise TypeError(f"x must be bfloat16, float16 or float8_e4m3fn (got {x.dtype})")
-    _require(x, "x", torch.float8_e4m3fn, (M, K))
-    _require(weight, "weight", torch.float8_e4m3fn, (N, K), dev)
+    require(x, "x", torch.float8_e4m3fn, (M, K), dev)
+    require(weight, "weight", torch.float8_e4m3fn, (N, K), dev)
     if not isinstance(x_scales, torch.Tensor) or not isinstance(weight_scales, torch.Tensor):
         raise ValueError("float8_e4m3fn operands need x_scales and weight_scales")
     if x_scales.dtype == torch.float32:
-        _require(x_scales, "x_scales", torch.float32, (M,), dev)
-        _require(weight_scales, "weight_scales", torch.float32, (N,), dev)
+        require(x_scales, "x_scales", torch.float32, (M,), dev)
+        require(weight_scales, "weight_scales", torch.float32, (N,), dev)
         return M, N, K, _lib.MHC_LINEAR_E4M3_ROW, torch.bfloat16
     blocks = -(-K // 32)
-    _require(x_scales, "x_scales", torch.float8_e8m0fnu, (M, blocks), dev)
-    _require(weight_scales, "weight_scales", torch.float8_e8m0fnu, (N, blocks), dev)
+    require(x_scales, "x_scales", torch.float8_e8m0fnu, (M, blocks), dev)
+    require(weight_scales, "weight_scales", torch.float8_e8m0fnu, (N, blocks), dev)
     return M, N, K, _lib.MHC_LINEAR_E4M3_MX, torch.bfloat16
 
 
-def _workspace(workspace, need: int, dev, stream) -> tuple[int | None, int]:
-    """(address, bytes) of the caller's workspace, or of a fresh one."""
-    if workspace is None:
-        if need <= 0:
-            return None, 0
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or \
-            not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+@functools.lru_cache(maxsize=4096)
+def _fwd_workspace(M: int, N: int, K: int, dtype: int) -> int:
+    """Workspace bytes of a forward call with the policy's launch (they follow
+    from the sizes alone)."""
+    return _lib.linear_lib().mhc_linear_fwd_workspace_bytes(M, N, K, dtype, None)
+
+
+@functools.lru_cache(maxsize=4096)
+def _bwd_workspace(M: int, N: int, K: int, dtype: int) -> int:
+    return _lib.linear_lib().mhc_linear_bwd_workspace_bytes(M, N, K, dtype)
 
 
 def mhc_linear_plan(M: int, N: int, K: int, dtype: int, launch=None) -> dict:
@@ -125,30 +124,43 @@ def mhc_linear_fwd(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *,
     """out [M, N] <- act(x [M, K] . weight [N, K]^T + bias [N]) + residual
     [M, N]; z, where given, takes the value before the activation. Without a
     workspace one is allocated. Asynchronous."""
-    M, N, K, dtype, kind = _operands(x, weight, x_scales, weight_scales)
+    sizes = _check_fwd_inputs(x, weight, bias, residual, x_scales, weight_scales)
+    M, N, _, _, kind = sizes
+    require(out, "out", kind, (M, N), x.device)
+    if z is not None:
+        require(z, "z", kind, (M, N), x.device)
+    _launch_fwd(x, weight, out, bias, activation, residual, x_scales, weight_scales, z, sizes,
+                workspace, stream, _launch_arg(launch), start_event, stop_event)
+    return out
+
+
+def _check_fwd_inputs(x, weight, bias, residual, x_scales, weight_scales):
+    sizes = _operands(x, weight, x_scales, weight_scales)
+    M, N, _, _, kind = sizes
+    if bias is not None:
+        require(bias, "bias", kind, (N,), x.device)
+    if residual is not None:
+        require(residual, "residual", kind, (M, N), x.device)
+    return sizes
+
+
+def _launch_fwd(x, weight, out, bias, activation, residual, x_scales, weight_scales, z, sizes,
+                workspace, stream, launch, start_event, stop_event) -> None:
+    M, N, K, dtype, _ = sizes
     act = _act(activation)
     dev = x.device
-    _require(out, "out", kind, (M, N), dev)
-    if bias is not None:
-        _require(bias, "bias", kind, (N,), dev)
-    if residual is not None:
-        _require(residual, "residual", kind, (M, N), dev)
-    if z is not None:
-        _require(z, "z", kind, (M, N), dev)
-    launch = _launch_arg(launch)
     lib = _lib.linear_lib()
-    ws, ws_bytes = _workspace(
-        workspace, lib.mhc_linear_fwd_workspace_bytes(M, N, K, dtype, launch), dev, stream)
-    with torch.cuda.device(dev):
+    need = 0
+    if workspace is None:
+        need = _fwd_workspace(M, N, K, dtype) if launch is None else \
+            lib.mhc_linear_fwd_workspace_bytes(M, N, K, dtype, launch)
+    ws, ws_bytes, _owner = workspace_of(workspace, need, dev, stream)
+    with on(dev):
         st = lib.mhc_linear_fwd(
-            x.data_ptr(), None if x_scales is None else x_scales.data_ptr(), weight.data_ptr(),
-            None if weight_scales is None else weight_scales.data_ptr(),
-            None if bias is None else bias.data_ptr(),
-            None if residual is None else residual.data_ptr(), out.data_ptr(),
-            None if z is None else z.data_ptr(), ws, ws_bytes, M, N, K, dtype, act,
-            _stream_handle(dev, stream), launch, start_event, stop_event)
+            x.data_ptr(), address(x_scales), weight.data_ptr(), address(weight_scales),
+            address(bias), address(residual), out.data_ptr(), address(z), ws, ws_bytes, M, N, K,
+            dtype, act, stream_handle(dev, stream), launch, start_event, stop_event)
     check_linear(st)
-    return out
 
 
 def mhc_linear_bwd(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *,
@@ -163,26 +175,23 @@ def mhc_linear_bwd(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor
     M, N, K, dtype, kind = _operands(x, weight, None, None)
     act = _act(activation)
     dev = x.device
-    _require(grad_out, "grad_out", kind, (M, N), dev)
+    require(grad_out, "grad_out", kind, (M, N), dev)
     if activation != "none":
-        _require(z, "z", kind, (M, N), dev)
+        require(z, "z", kind, (M, N), dev)
     if grad_x is not None:
-        _require(grad_x, "grad_x", kind, (M, K), dev)
+        require(grad_x, "grad_x", kind, (M, K), dev)
     if grad_weight is not None:
-        _require(grad_weight, "grad_weight", kind, (N, K), dev)
+        require(grad_weight, "grad_weight", kind, (N, K), dev)
     if grad_bias is not None:
-        _require(grad_bias, "grad_bias", kind, (N,), dev)
-    lib = _lib.linear_lib()
-    ws, ws_bytes = _workspace(workspace, lib.mhc_linear_bwd_workspace_bytes(M, N, K, dtype), dev,
-                              stream)
-    with torch.cuda.device(dev):
-        st = lib.mhc_linear_bwd(
+        require(grad_bias, "grad_bias", kind, (N,), dev)
+    ws, ws_bytes, _owner = workspace_of(
+        workspace, _bwd_workspace(M, N, K, dtype) if workspace is None else 0, dev, stream)
+    with on(dev):
+        st = _lib.linear_lib().mhc_linear_bwd(
             grad_out.data_ptr(), x.data_ptr(), weight.data_ptr(),
-            z.data_ptr() if activation != "none" else None,
-            None if grad_x is None else grad_x.data_ptr(),
-            None if grad_weight is None else grad_weight.data_ptr(),
-            None if grad_bias is None else grad_bias.data_ptr(), ws, ws_bytes, M, N, K, dtype,
-            act, _stream_handle(dev, stream), start_event, stop_event)
+            z.data_ptr() if activation != "none" else None, address(grad_x),
+            address(grad_weight), address(grad_bias), ws, ws_bytes, M, N, K, dtype, act,
+            stream_handle(dev, stream), start_event, stop_event)
     check_linear(st)
 
 
@@ -197,11 +206,12 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     """The product with freshly allocated outputs (no autograd). return_z:
     also the value before the activation, which the backward needs unless
     the activation is "none"."""
-    M, N, _, _, kind = _operands(x, weight, x_scales, weight_scales)
-    out = torch.empty((M, N), dtype=kind, device=x.device)
+    sizes = _check_fwd_inputs(x, weight, bias, residual, x_scales, weight_scales)
+    M, N, _, _, kind = sizes
+    out = x.new_empty((M, N), dtype=kind)
     z = torch.empty_like(out) if return_z and activation != "none" else None
-    mhc_linear_fwd(x, weight, out, bias=bias, activation=activation, residual=residual,
-                   x_scales=x_scales, weight_scales=weight_scales, z=z)
+    _launch_fwd(x, weight, out, bias, activation, residual, x_scales, weight_scales, z, sizes,
+                None, None, None, None, None)
     return LinearOut(out, z)
 
 
@@ -211,7 +221,6 @@ def linear_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     """Backward with freshly allocated gradients: (grad_x, grad_weight,
     grad_bias; the last None unless bias). The residual's gradient is
     grad_out itself."""
-    _operands(x, weight, None, None)
     grad_x, grad_weight = torch.empty_like(x), torch.empty_like(weight)
     grad_bias = torch.empty((weight.shape[0],), dtype=x.dtype, device=x.device) if bias else None
     mhc_linear_bwd(grad_out, x, weight, grad_x=grad_x, grad_weight=grad_weight,

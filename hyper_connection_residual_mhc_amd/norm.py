@@ -14,8 +14,8 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
+from ._call import address, on, require, stream_handle, workspace_of
 from ._lib import check_norm
-from .ops import _require, _stream_handle
 
 _DTYPES = {torch.float32: _lib.MHC_NORM_F32, torch.bfloat16: _lib.MHC_NORM_BF16,
            torch.float16: _lib.MHC_NORM_F16}
@@ -44,10 +44,36 @@ def _shapes(x: torch.Tensor, pre) -> tuple[int, int, int]:
     return int(x.shape[0]), int(x.shape[1]), int(x.shape[2])
 
 
-def _weight_dtype(weight: torch.Tensor, dtype: torch.dtype) -> torch.dtype:
-    if not isinstance(weight, torch.Tensor):
-        raise TypeError("weight must be a torch.Tensor")
-    return torch.float32 if weight.dtype == torch.float32 else dtype
+def _check_inputs(x, weight, residual, pre, quant) -> tuple[int, int, int]:
+    """(T, n, H) of a forward call whose inputs are sound."""
+    T, n, H = _shapes(x, pre)
+    if quant not in _FORMATS:
+        raise ValueError(f'quant must be None, "row" or "mx" (got {quant!r})')
+    dev, dt = x.device, x.dtype
+    require(x, "x", dt, (T, n, H) if n else (T, H), dev)
+    _check_weight(weight, dt, H, dev)
+    if residual is not None:
+        require(residual, "residual", dt, (T, H), dev)
+    if pre is not None:
+        require(pre, "pre", torch.float32, (T, n), dev)
+    return T, n, H
+
+
+def _check_weight(weight, dtype: torch.dtype, H: int, device: torch.device) -> None:
+    fp32 = isinstance(weight, torch.Tensor) and weight.dtype is torch.float32
+    require(weight, "weight", torch.float32 if fp32 else dtype, (H,), device)
+
+
+def _launch_fwd(x, weight, out, eps, residual, pre, scales, stored, rstd, quant, T, n, H, stream,
+                start_event, stop_event) -> None:
+    dev = x.device
+    with on(dev):
+        st = _lib.norm_lib().mhc_rms_norm_fwd(
+            x.data_ptr(), address(residual), address(pre), n, weight.data_ptr(),
+            _DTYPES[weight.dtype], float(eps), out.data_ptr(), address(scales), address(stored),
+            address(rstd), T, H, _DTYPES[x.dtype], _FORMATS[quant], stream_handle(dev, stream),
+            start_event, stop_event)
+    check_norm(st)
 
 
 def mhc_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *,
@@ -60,36 +86,21 @@ def mhc_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *
     """out <- norm of x [T, H], of x + residual, or of streams x [T, n, H]
     collapsed with pre [T, n]; writes scales, stored and rstd where given.
     quant: None, "row" or "mx". Asynchronous."""
-    T, n, H = _shapes(x, pre)
-    if quant not in _FORMATS:
-        raise ValueError(f'quant must be None, "row" or "mx" (got {quant!r})')
+    T, n, H = _check_inputs(x, weight, residual, pre, quant)
     dev, dt = x.device, x.dtype
-    _require(x, "x", dt, (T, n, H) if n else (T, H))
-    _require(weight, "weight", _weight_dtype(weight, dt), (H,), dev)
-    _require(out, "out", dt if quant is None else torch.float8_e4m3fn, (T, H), dev)
-    if residual is not None:
-        _require(residual, "residual", dt, (T, H), dev)
-    if pre is not None:
-        _require(pre, "pre", torch.float32, (T, n), dev)
+    require(out, "out", dt if quant is None else torch.float8_e4m3fn, (T, H), dev)
     if stored is not None:
-        _require(stored, "stored", dt, (T, H), dev)
+        require(stored, "stored", dt, (T, H), dev)
     if rstd is not None:
-        _require(rstd, "rstd", torch.float32, (T,), dev)
+        require(rstd, "rstd", torch.float32, (T,), dev)
     if quant == "row":
-        _require(scales, "scales", torch.float32, (T,), dev)
+        require(scales, "scales", torch.float32, (T,), dev)
     elif quant == "mx":
-        _require(scales, "scales", torch.float8_e8m0fnu, (T, -(-H // 32)), dev)
+        require(scales, "scales", torch.float8_e8m0fnu, (T, -(-H // 32)), dev)
     elif scales is not None:
         raise ValueError("scales need quant")
-    with torch.cuda.device(dev):
-        st = _lib.norm_lib().mhc_rms_norm_fwd(
-            x.data_ptr(), None if residual is None else residual.data_ptr(),
-            None if pre is None else pre.data_ptr(), n, weight.data_ptr(), _DTYPES[weight.dtype],
-            float(eps), out.data_ptr(), None if scales is None else scales.data_ptr(),
-            None if stored is None else stored.data_ptr(),
-            None if rstd is None else rstd.data_ptr(), T, H, _DTYPES[dt], _FORMATS[quant],
-            _stream_handle(dev, stream), start_event, stop_event)
-    check_norm(st)
+    _launch_fwd(x, weight, out, eps, residual, pre, scales, stored, rstd, quant, T, n, H, stream,
+                start_event, stop_event)
     return out
 
 
@@ -110,33 +121,40 @@ def mhc_rms_norm_bwd(grad_y: torch.Tensor, stored: torch.Tensor, weight: torch.T
     """(grad_x [T, H], grad_weight [H] fp32) <- backward of the norm of the
     rows `stored`; grad_stored is added to grad_x where given. Without a
     workspace one is allocated. Asynchronous."""
+    T, H = _check_bwd_inputs(grad_y, stored, weight, rstd, grad_stored)
+    dev = stored.device
+    require(grad_x, "grad_x", stored.dtype, (T, H), dev)
+    require(grad_weight, "grad_weight", torch.float32, (H,), dev)
+    _launch_bwd(grad_y, stored, weight, rstd, grad_stored, grad_x, grad_weight, workspace, T, H,
+                stream, start_event, stop_event)
+    return grad_x, grad_weight
+
+
+def _check_bwd_inputs(grad_y, stored, weight, rstd, grad_stored) -> tuple[int, int]:
     T, _, H = _shapes(stored, None)
     dev, dt = stored.device, stored.dtype
-    _require(stored, "stored", dt, (T, H))
-    _require(grad_y, "grad_y", dt, (T, H), dev)
-    _require(weight, "weight", _weight_dtype(weight, dt), (H,), dev)
-    _require(rstd, "rstd", torch.float32, (T,), dev)
-    _require(grad_x, "grad_x", dt, (T, H), dev)
-    _require(grad_weight, "grad_weight", torch.float32, (H,), dev)
+    require(stored, "stored", dt, (T, H), dev)
+    require(grad_y, "grad_y", dt, (T, H), dev)
+    _check_weight(weight, dt, H, dev)
+    require(rstd, "rstd", torch.float32, (T,), dev)
     if grad_stored is not None:
-        _require(grad_stored, "grad_stored", dt, (T, H), dev)
-    if workspace is None:
-        workspace = torch.empty((mhc_rms_norm_bwd_workspace_bytes(T, H),), dtype=torch.uint8,
-                                device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or \
-            not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    with torch.cuda.device(dev):
-        st = _lib.norm_lib().mhc_rms_norm_bwd(
+        require(grad_stored, "grad_stored", dt, (T, H), dev)
+    return T, H
+
+
+def _launch_bwd(grad_y, stored, weight, rstd, grad_stored, grad_x, grad_weight, workspace, T, H,
+                stream, start_event, stop_event) -> None:
+    dev = stored.device
+    lib = _lib.norm_lib()
+    need = lib.mhc_rms_norm_bwd_workspace_bytes(T, H) if workspace is None else 0
+    ws, ws_bytes, _owner = workspace_of(workspace, need, dev, stream)
+    with on(dev):
+        st = lib.mhc_rms_norm_bwd(
             grad_y.data_ptr(), stored.data_ptr(), weight.data_ptr(), _DTYPES[weight.dtype],
-            rstd.data_ptr(), None if grad_stored is None else grad_stored.data_ptr(),
-            grad_x.data_ptr(), grad_weight.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), T, H, _DTYPES[dt],
-            _stream_handle(dev, stream), start_event, stop_event)
+            rstd.data_ptr(), address(grad_stored), grad_x.data_ptr(), grad_weight.data_ptr(), ws,
+            ws_bytes, T, H, _DTYPES[stored.dtype], stream_handle(dev, stream), start_event,
+            stop_event)
     check_norm(st)
-    return grad_x, grad_weight
 
 
 # ---------------------------------------------------------------------------
@@ -148,20 +166,23 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
              quant: str | None = None, return_rstd: bool = False) -> RMSNormOut:
     """The norm with freshly allocated outputs (no autograd); `stored` is
     returned with a residual or pre."""
-    T, _, H = _shapes(x, pre)
+    T, n, H = _check_inputs(x, weight, residual, pre, quant)
     dev = x.device
-    y = torch.empty((T, H), dtype=x.dtype if quant is None else torch.float8_e4m3fn, device=dev)
     scales = stored = rstd = None
-    if quant == "row":
-        scales = torch.empty((T,), dtype=torch.float32, device=dev)
-    elif quant == "mx":
-        scales = torch.empty((T, -(-H // 32)), dtype=torch.float8_e8m0fnu, device=dev)
-    if residual is not None or pre is not None:
-        stored = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if quant is None:
+        y = x.new_empty((T, H))
+    else:
+        y = x.new_empty((T, H), dtype=torch.float8_e4m3fn)
+        if quant == "row":
+            scales = torch.empty((T,), dtype=torch.float32, device=dev)
+        else:
+            scales = torch.empty((T, -(-H // 32)), dtype=torch.float8_e8m0fnu, device=dev)
+    if n or residual is not None:
+        stored = x.new_empty((T, H))
     if return_rstd:
         rstd = torch.empty((T,), dtype=torch.float32, device=dev)
-    mhc_rms_norm_fwd(x, weight, y, eps=eps, residual=residual, pre=pre, scales=scales,
-                     stored=stored, rstd=rstd, quant=quant)
+    _launch_fwd(x, weight, y, eps, residual, pre, scales, stored, rstd, quant, T, n, H, None, None,
+                None)
     return RMSNormOut(y, scales, stored, rstd)
 
 
@@ -170,11 +191,12 @@ def rms_norm_backward(grad_y: torch.Tensor, stored: torch.Tensor, weight: torch.
                       ) -> tuple[torch.Tensor, torch.Tensor]:
     """Backward with freshly allocated gradients: (grad_x in stored's type,
     grad_weight in fp32)."""
-    T, _, H = _shapes(stored, None)
-    grad_x = torch.empty((T, H), dtype=stored.dtype, device=stored.device)
+    T, H = _check_bwd_inputs(grad_y, stored, weight, rstd, grad_stored)
+    grad_x = torch.empty_like(stored)
     grad_weight = torch.empty((H,), dtype=torch.float32, device=stored.device)
-    return mhc_rms_norm_bwd(grad_y, stored, weight, rstd, grad_x, grad_weight,
-                            grad_stored=grad_stored)
+    _launch_bwd(grad_y, stored, weight, rstd, grad_stored, grad_x, grad_weight, None, T, H, None,
+                None, None)
+    return grad_x, grad_weight
 
 
 class RMSNorm(torch.autograd.Function):

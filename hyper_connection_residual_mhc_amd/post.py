@@ -10,18 +10,19 @@ from __future__ import annotations
 import torch
 
 from . import _lib
+from ._call import on, require, stream_handle
 from ._lib import check_post
-from .ops import _require, _shapes_n, _stream_handle
+from .ops import _shapes_n
 
 
 def _check_inputs(residual: torch.Tensor, comb: torch.Tensor, post: torch.Tensor,
                   y: torch.Tensor) -> tuple[int, int, int]:
     T, n, H = _shapes_n(residual)
     dev = residual.device
-    _require(residual, "residual", torch.bfloat16, (T, n, H))
-    _require(comb, "comb", torch.float32, (T, n, n), dev)
-    _require(post, "post", torch.float32, (T, n), dev)
-    _require(y, "y", torch.bfloat16, (T, H), dev)
+    require(residual, "residual", torch.bfloat16, (T, n, H), dev)
+    require(comb, "comb", torch.float32, (T, n, n), dev)
+    require(post, "post", torch.float32, (T, n), dev)
+    require(y, "y", torch.bfloat16, (T, H), dev)
     return T, n, H
 
 
@@ -31,12 +32,17 @@ def mhc_post_fwd(residual: torch.Tensor, comb: torch.Tensor, post: torch.Tensor,
     """out [T, n, H] bf16 <- comb [T, n, n] . residual [T, n, H] + post [T, n]
     (x) y [T, H]; the gates are fp32, the rest bf16. Asynchronous."""
     T, n, H = _check_inputs(residual, comb, post, y)
+    require(out, "out", torch.bfloat16, (T, n, H), residual.device)
+    return _launch_fwd(residual, comb, post, y, out, T, n, H, stream, start_event, stop_event)
+
+
+def _launch_fwd(residual, comb, post, y, out, T, n, H, stream, start_event, stop_event
+                ) -> torch.Tensor:
     dev = residual.device
-    _require(out, "out", torch.bfloat16, (T, n, H), dev)
-    with torch.cuda.device(dev):
+    with on(dev):
         st = _lib.post_lib().mhc_post_fwd(
             residual.data_ptr(), comb.data_ptr(), post.data_ptr(), y.data_ptr(), out.data_ptr(),
-            T, n, H, _stream_handle(dev, stream), start_event, stop_event)
+            T, n, H, stream_handle(dev, stream), start_event, stop_event)
     check_post(st)
     return out
 
@@ -51,16 +57,16 @@ def mhc_post_bwd(grad_out: torch.Tensor, residual: torch.Tensor, comb: torch.Ten
     [T, n] fp32, grad_y [T, H] bf16) <- backward. Asynchronous."""
     T, n, H = _check_inputs(residual, comb, post, y)
     dev = residual.device
-    _require(grad_out, "grad_out", torch.bfloat16, (T, n, H), dev)
-    _require(grad_residual, "grad_residual", torch.bfloat16, (T, n, H), dev)
-    _require(grad_comb, "grad_comb", torch.float32, (T, n, n), dev)
-    _require(grad_post, "grad_post", torch.float32, (T, n), dev)
-    _require(grad_y, "grad_y", torch.bfloat16, (T, H), dev)
-    with torch.cuda.device(dev):
+    require(grad_out, "grad_out", torch.bfloat16, (T, n, H), dev)
+    require(grad_residual, "grad_residual", torch.bfloat16, (T, n, H), dev)
+    require(grad_comb, "grad_comb", torch.float32, (T, n, n), dev)
+    require(grad_post, "grad_post", torch.float32, (T, n), dev)
+    require(grad_y, "grad_y", torch.bfloat16, (T, H), dev)
+    with on(dev):
         st = _lib.post_lib().mhc_post_bwd(
             grad_out.data_ptr(), residual.data_ptr(), comb.data_ptr(), post.data_ptr(),
             y.data_ptr(), grad_residual.data_ptr(), grad_comb.data_ptr(), grad_post.data_ptr(),
-            grad_y.data_ptr(), T, n, H, _stream_handle(dev, stream), start_event, stop_event)
+            grad_y.data_ptr(), T, n, H, stream_handle(dev, stream), start_event, stop_event)
     check_post(st)
     return grad_residual, grad_comb, grad_post, grad_y
 
@@ -72,7 +78,9 @@ def mhc_post_bwd(grad_out: torch.Tensor, residual: torch.Tensor, comb: torch.Ten
 def post_update(residual: torch.Tensor, comb: torch.Tensor, post: torch.Tensor,
                 y: torch.Tensor) -> torch.Tensor:
     """The write-back with a freshly allocated output (no autograd)."""
-    return mhc_post_fwd(residual, comb, post, y, torch.empty_like(residual))
+    T, n, H = _check_inputs(residual, comb, post, y)
+    return _launch_fwd(residual, comb, post, y, torch.empty_like(residual), T, n, H, None, None,
+                       None)
 
 
 def post_update_backward(grad_out: torch.Tensor, residual: torch.Tensor, comb: torch.Tensor,
