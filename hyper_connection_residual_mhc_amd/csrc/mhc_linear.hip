@@ -286,7 +286,7 @@ struct Operand {
   uint32_t row, piece;
   uint32_t ld;
   uint32_t here;    // rows (columns) that exist
-  i32x4 held[DMA ? 1 : Q];
+  i32x4 held[2][DMA ? 1 : Q];  // through registers: two tiles on their way
 
   static __device__ __forceinline__ uint32_t swap(uint32_t row) {
     if constexpr (!TURNED) {
@@ -313,6 +313,7 @@ struct Operand {
   }
 
   // Starts the loads of round q of the tile kt into `to`, the tile's place in LDS.
+  template <int SET = 0>
   __device__ __forceinline__ void start(uint32_t kt, uint32_t kbytes, uint32_t to, int q) {
     const uint32_t rows = q * kEach;
     if constexpr (DMA) {
@@ -326,7 +327,7 @@ struct Operand {
         load_to_lds<16>(kt * kTileK + piece < kbytes ? offset : kOutside, rsrc,
                         kt * kTileK + rows * ld, dst);
     } else {
-      held[q] = i32x4{0, 0, 0, 0};
+      held[SET][q] = i32x4{0, 0, 0, 0};
       uint32_t left;  // bytes of the piece that exist
       const uint8_t* p = base;
       if constexpr (TURNED) {
@@ -341,10 +342,10 @@ struct Operand {
       if (left >= 16) {
         if constexpr (ELEM == 2) {
           typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
-          held[q] = *reinterpret_cast<const i32x4_at2*>(p);
+          held[SET][q] = *reinterpret_cast<const i32x4_at2*>(p);
         } else {
           typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
-          held[q] = *reinterpret_cast<const i32x4_at1*>(p);
+          held[SET][q] = *reinterpret_cast<const i32x4_at1*>(p);
         }
       } else if (left > 0) {
         uint32_t u[4] = {0, 0, 0, 0};
@@ -355,18 +356,19 @@ struct Operand {
             u[i / 4] |= b << (8 * (i % 4));
           }
         }
-        held[q] = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
+        held[SET][q] = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
                         static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
       }
     }
   }
 
   // Through registers: writes the loaded tile.
+  template <int SET>
   __device__ __forceinline__ void put(uint8_t* to) {
     if constexpr (!DMA) {
 #pragma unroll
       for (int q = 0; q < Q; ++q)
-        *reinterpret_cast<i32x4*>(to + (q * THREADS + threadIdx.x) * 16) = held[q];
+        *reinterpret_cast<i32x4*>(to + (q * THREADS + threadIdx.x) * 16) = held[SET][q];
     }
   }
 };
@@ -687,20 +689,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
     }
     wait_tiles<0>();  // nothing arrives in LDS any more
   } else {
-    start(first, 0);
-    read_scales(first);
-    for (uint32_t kt = first; kt < last; ++kt) {
-      const uint32_t b = (kt - first) & 1;
-      lx.put(lds[b]);
-      lw.put(lds[b] + BM * kTileK);
-      take_scales(b);
-      __syncthreads();
-      if (kt + 1 < last) {
-        start(kt + 1, b ^ 1);
-        read_scales(kt + 1);
+    const auto load = [&](uint32_t kt, auto set) {
+      constexpr int S = decltype(set)::value;
+      if (kt < last) {
+#pragma unroll
+        for (int q = 0; q < OpX::Q; ++q) lx.template start<S>(kt, a.kbytes, 0, q);
+#pragma unroll
+        for (int q = 0; q < OpW::Q; ++q) lw.template start<S>(kt, a.kbytes, 0, q);
       }
-      multiply(lds[b]);
+    };
+    const auto pass = [&](uint32_t kt, auto set) {
+      constexpr int S = decltype(set)::value;
+      lx.template put<S>(lds[S]);
+      lw.template put<S>(lds[S] + BM * kTileK);
+      take_scales(S);
+      __syncthreads();
+      load(kt + 2, set);
+      if (kt + 1 < last) read_scales(kt + 1);
+      multiply(lds[S]);
+    };
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    load(first, Even());
+    load(first + 1, Odd());
+    read_scales(first);
+    uint32_t kt = first;
+    for (; kt + 1 < last; kt += 2) {
+      pass(kt, Even());
+      pass(kt + 1, Odd());
     }
+    if (kt < last) pass(kt, Even());
   }
   write_tile<OP, BM, BN, WM, WN, kStages * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
@@ -887,10 +905,16 @@ __global__ __launch_bounds__(256) void linear_join_kernel(const float* __restric
 // Up to 16 rows of x
 //
 // Bound by W's bytes: each is read once, straight into registers. A block
-// takes 16 rows of W; its waves take turns over the sum in units of kTileK
-// bytes of each row (4 units of a wave in flight), multiply them with x's rows
-// as the second operand (rows past M are zeros), and are joined through LDS in
-// ascending order.
+// takes up to 16 rows of W; its waves share the sum in units of kTileK bytes of
+// each row, four units' loads of a wave in flight, multiply them with x's rows
+// as the second operand, and are joined through LDS in ascending order.
+//
+// Blocks take as many rows of W as leaves every CU as many blocks as any
+// other: 16 x 24 x 28672 in bf16 50.4 -> 32.9 us, 1 x 1024 x 4096 6.8 -> 5.3, 1 x 7168 x 7168
+// 21.0 -> 19.9 us (5.1 TB/s) against 16 rows always. 1 x 4096 x 7168: 12.7 us (4.6 TB/s);
+// 4 or 16 waves 14.8 and 13.3, 32 rows of W to a block 17.8. Lanes without a row of x or
+// W load nothing: reading the last row again instead 15.3. Block scales, 16 x 7168 x 4096:
+// 11.6 us, one byte a load 13.7.
 // ---------------------------------------------------------------------------
 
 struct RowsArgs {
@@ -900,11 +924,13 @@ struct RowsArgs {
   const uint8_t* ws;  // kMX
   int64_t M, N;
   uint32_t kbytes;
+  uint32_t wide;  // rows of W for each block, at most 16
   Epilogue e;
 };
 
+// The lane's values of the unit at byte k of a row; those past kbytes are zeros.
 template <int OP, bool FULL>
-__device__ __forceinline__ void load_unit(const uint8_t* row, bool in, uint32_t k, uint32_t kbytes,
+__device__ __forceinline__ void load_unit(const uint8_t* row, uint32_t k, uint32_t kbytes,
                                           uint32_t g, Frag<OP> (&f)[is8(OP) ? 1 : 2]) {
   typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
   typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
@@ -913,26 +939,21 @@ __device__ __forceinline__ void load_unit(const uint8_t* row, bool in, uint32_t 
     // piece p of the unit: the lane group's 16 bytes
     const uint32_t at = k + p * 64 + g * 16;
     i32x4 v = {0, 0, 0, 0};
-    if (in) {
-      if (FULL || at + 16 <= kbytes) {
-        if constexpr (is8(OP)) v = *reinterpret_cast<const i32x4_at1*>(row + at);
-        else v = *reinterpret_cast<const i32x4_at2*>(row + at);
-      } else {
-        uint32_t u[4] = {0, 0, 0, 0};
-        for (uint32_t i = 0; i < 16; i += is8(OP) ? 1 : 2) {
-          if (at + i < kbytes) {
-            const uint32_t b = is8(OP) ? row[at + i]
-                                       : *reinterpret_cast<const uint16_t*>(row + at + i);
-            const uint32_t word = i / 4, s = b << (8 * (i % 4));
-            u[0] |= word == 0 ? s : 0;
-            u[1] |= word == 1 ? s : 0;
-            u[2] |= word == 2 ? s : 0;
-            u[3] |= word == 3 ? s : 0;
-          }
+    if (FULL || at + 16 <= kbytes) {
+      if constexpr (is8(OP)) v = *reinterpret_cast<const i32x4_at1*>(row + at);
+      else v = *reinterpret_cast<const i32x4_at2*>(row + at);
+    } else {
+      uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (uint32_t i = 0; i < 16; i += is8(OP) ? 1 : 2) {
+        if (at + i < kbytes) {
+          const uint32_t b = is8(OP) ? row[at + i]
+                                     : *reinterpret_cast<const uint16_t*>(row + at + i);
+          u[i / 4] |= b << (8 * (i % 4));
         }
-        v = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
-                  static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
       }
+      v = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
+                static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
     }
     if constexpr (is8(OP)) f[0].w[p] = v;
     else f[p].w[0] = v;
@@ -941,55 +962,69 @@ __device__ __forceinline__ void load_unit(const uint8_t* row, bool in, uint32_t 
 
 template <int OP, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
-  constexpr int kAhead = 4;
   constexpr int kFrags = is8(OP) ? 1 : 2;
   __shared__ float sums[WAVES][16][17];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-  const bool in_w = n0 + low < a.N, in_x = low < a.M;
-  const uint8_t* w = a.w + (in_w ? n0 + low : 0) * a.kbytes;
-  const uint8_t* x = a.x + (in_x ? low : 0) * static_cast<int64_t>(a.kbytes);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * a.wide;
+  const bool in_w = low < a.wide, in_x = low < a.M;
+  const int64_t wrow = min(n0 + (in_w ? low : 0), a.N - 1);
+  const uint32_t xrow = in_x ? low : 0;
   const uint32_t kblocks = (a.kbytes + 31) / 32;
-  const uint8_t* ws = OP == kOpMX ? a.ws + (in_w ? n0 + low : 0) * kblocks : nullptr;
-  const uint8_t* xs = OP == kOpMX ? a.xs + (in_x ? low : 0) * static_cast<int64_t>(kblocks) : nullptr;
+  const uint8_t* w = a.w + wrow * a.kbytes;
+  const uint8_t* x = a.x + static_cast<int64_t>(xrow) * a.kbytes;
+  const uint8_t* ws = OP == kOpMX ? a.ws + wrow * kblocks : nullptr;
+  const uint8_t* xs = OP == kOpMX ? a.xs + static_cast<int64_t>(xrow) * kblocks : nullptr;
   f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 
   const uint32_t full = a.kbytes / kTileK, units = (a.kbytes + kTileK - 1) / kTileK;
-  uint32_t u = wave;
-  for (; u < full; u += WAVES * kAhead) {
-    Frag<OP> fw[kAhead][kFrags], fx[kAhead][kFrags];
-    int sw[kAhead], sx[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const uint32_t at = u + k * WAVES;
-      const bool in = at < full;
-      load_unit<OP, true>(w, in && in_w, at * kTileK, a.kbytes, g, fw[k]);
-      load_unit<OP, true>(x, in && in_x, at * kTileK, a.kbytes, g, fx[k]);
-      sw[k] = sx[k] = 0;
+  // The waves take turns, unit by unit; with block scales each takes a run of
+  // units, so that the scales of four come in one load (byte 4 k + g of 16).
+  constexpr bool kRun = OP == kOpMX;
+  constexpr uint32_t kStride = kRun ? 1 : WAVES;
+  const uint32_t each = (full + WAVES - 1) / WAVES;
+  uint32_t u = kRun ? min(full, wave * each) : wave;
+  const uint32_t end = kRun ? min(full, u + each) : full;
+  const auto some = [&](auto ahead) {
+    constexpr int kAhead = decltype(ahead)::value;
+    typedef uint32_t Bytes __attribute__((ext_vector_type(kAhead)));
+    typedef Bytes Bytes_at1 __attribute__((aligned(1)));
+    for (; u + (kAhead - 1) * kStride < end; u += kAhead * kStride) {
+      Frag<OP> fw[kAhead][kFrags], fx[kAhead][kFrags];
+      Bytes sw = {}, sx = {};
       if constexpr (OP == kOpMX) {
-        if (in) {
-          sw[k] = ws[at * 4 + g];
-          sx[k] = xs[at * 4 + g];
-        }
+        if (in_w) sw = *reinterpret_cast<const Bytes_at1*>(ws + u * 4);
+        if (in_x) sx = *reinterpret_cast<const Bytes_at1*>(xs + u * 4);
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t at = (u + k * kStride) * kTileK;
+        if (in_w) load_unit<OP, true>(w, at, a.kbytes, g, fw[k]);
+        else fw[k][0] = fw[k][kFrags - 1] = {};
+        if (in_x) load_unit<OP, true>(x, at, a.kbytes, g, fx[k]);
+        else fx[k][0] = fx[k][kFrags - 1] = {};
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t bw = sw[k], bx = sx[k];
+#pragma unroll
+        for (int p = 0; p < kFrags; ++p)
+          acc[(k + p) % 2] = mma<OP>(fw[k][p], fx[k][p], acc[(k + p) % 2],
+                                     static_cast<int>(bw >> (8 * g)), static_cast<int>(bx >> (8 * g)));
       }
     }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-#pragma unroll
-      for (int p = 0; p < kFrags; ++p)
-        acc[(k + p) % 2] = mma<OP>(fw[k][p], fx[k][p], acc[(k + p) % 2], sw[k], sx[k]);
-  }
-  if (full < units && wave == full % WAVES) {
+  };
+  some(std::integral_constant<int, 4>());
+  some(std::integral_constant<int, 2>());
+  some(std::integral_constant<int, 1>());
+  if (full < units && wave == WAVES - 1) {
     Frag<OP> fw[kFrags], fx[kFrags];
-    load_unit<OP, false>(w, in_w, full * kTileK, a.kbytes, g, fw);
-    load_unit<OP, false>(x, in_x, full * kTileK, a.kbytes, g, fx);
+    load_unit<OP, false>(w, full * kTileK, a.kbytes, g, fw);
+    load_unit<OP, false>(x, full * kTileK, a.kbytes, g, fx);
     int sw = 0, sx = 0;
-    if constexpr (OP == kOpMX) {
-      if (full * 4 + g < kblocks) {
-        sw = ws[full * 4 + g];
-        sx = xs[full * 4 + g];
-      }
+    if (OP == kOpMX && full * 4 + g < kblocks) {
+      sw = ws[full * 4 + g];
+      sx = xs[full * 4 + g];
     }
 #pragma unroll
     for (int p = 0; p < kFrags; ++p) acc[p % 2] = mma<OP>(fw[p], fx[p], acc[p % 2], sw, sx);
@@ -1004,7 +1039,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
   const int64_t m = threadIdx.x / 2;
   const uint32_t half = threadIdx.x % 2;
   const int64_t n = n0 + half * 8;
-  if (threadIdx.x < 32 && m < a.M && n < a.N) {
+  if (threadIdx.x < 32 && m < a.M && n < a.N && half * 8 < a.wide) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -1012,7 +1047,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
 #pragma unroll
       for (int k = 1; k < WAVES; ++k) v[i] = v[i] + sums[k][m][half * 8 + i];
     }
-    const int count = static_cast<int>(min(a.N - n, static_cast<int64_t>(8)));
+    const int count = static_cast<int>(min(min(a.N - n, static_cast<int64_t>(8)), static_cast<int64_t>(a.wide - half * 8)));
     with_act(a.e.act, [&](auto act) { finish<OP, decltype(act)::value>(a.e, m, n, count, v); });
   }
 }
@@ -1026,12 +1061,14 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
 
 // gz = rnd(grad_out * act'(z)) where gz is given, and this block's rows of the
 // bias's sums where partial is: 512 columns to a block, 8 to a lane; each of
-// the four waves takes every fourth row, joined in ascending order.
+// the four waves takes every fourth row, four rows' loads in flight, joined in
+// ascending order.
 template <int F, int ACT>
 __global__ __launch_bounds__(256) void linear_gz_kernel(
     const typename Store<F>::type* __restrict__ grad_out,
     const typename Store<F>::type* __restrict__ z, typename Store<F>::type* __restrict__ gz,
     float* __restrict__ partial, int64_t M, int64_t N, int64_t rows) {
+  constexpr int kAhead = 4;
   __shared__ float sums[4][512];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 512 + lane * 8;
@@ -1039,19 +1076,30 @@ __global__ __launch_bounds__(256) void linear_gz_kernel(
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (n < N) {
     const int count = static_cast<int>(min(N - n, static_cast<int64_t>(8)));
-    for (int64_t m = m0 + wave; m < m1; m += 4) {
-      float v[8], s[8];
-      widen_chunk<F>(load_chunk<F>(grad_out + m * N + n, count), v);
-      if constexpr (ACT != MHC_ACT_NONE) {
-        widen_chunk<F>(load_chunk<F>(z + m * N + n, count), s);
+    for (int64_t m = m0 + wave; m < m1; m += 4 * kAhead) {
+      Chunk<F> cg[kAhead], cz[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * slope<ACT>(s[i]);
-        Chunk<F> c;
-        narrow_chunk<F>(v, c);
-        store_chunk<F>(gz + m * N + n, count, c);
-      }
+      for (int k = 0; k < kAhead; ++k)
+        if (m + 4 * k < m1) {
+          cg[k] = load_chunk<F>(grad_out + (m + 4 * k) * N + n, count);
+          if constexpr (ACT != MHC_ACT_NONE) cz[k] = load_chunk<F>(z + (m + 4 * k) * N + n, count);
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] = sum[i] + v[i];
+      for (int k = 0; k < kAhead; ++k)
+        if (m + 4 * k < m1) {
+          float v[8], s[8];
+          widen_chunk<F>(cg[k], v);
+          if constexpr (ACT != MHC_ACT_NONE) {
+            widen_chunk<F>(cz[k], s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = v[i] * slope<ACT>(s[i]);
+            Chunk<F> c;
+            narrow_chunk<F>(v, c);
+            store_chunk<F>(gz + (m + 4 * k) * N + n, count, c);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[i] = sum[i] + v[i];
+        }
     }
   }
   if (partial == nullptr) return;
@@ -1065,17 +1113,24 @@ __global__ __launch_bounds__(256) void linear_gz_kernel(
   }
 }
 
-// grad_bias[n] = the parts' sum in ascending order, rounded once (+0.0 of none).
+// grad_bias[n] = the parts' sum, rounded once (+0.0 of none): 64 columns to a
+// block, each of four waves every fourth part, joined in ascending order.
 template <int F>
 __global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ partial,
                                                           typename Store<F>::type* __restrict__ out,
                                                           int64_t parts, int64_t N) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float sums[4][64];
+  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   float s = 0.0f;
+  if (n < N) {
 #pragma unroll 8
-  for (int64_t k = 0; k < parts; ++k) s = s + partial[k * N + n];
-  out[n] = narrow<F>(s);
+    for (int64_t k = wave; k < parts; k += 4) s = s + partial[k * N + n];
+  }
+  sums[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && n < N)
+    out[n] = narrow<F>(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane]);
 }
 
 __global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* __restrict__ p, int64_t count) {
@@ -1274,9 +1329,11 @@ hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t
 
 template <int OP>
 hipError_t launch_rows(const TileArgs& t, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
+  // the fewest blocks for each of 256 CUs, and W's rows spread evenly over them
+  const int64_t wide = ceil_div(t.N, 256 * ceil_div(t.N, 256 * 16));
   const RowsArgs a = {static_cast<const uint8_t*>(t.x.p), static_cast<const uint8_t*>(t.w.p), t.xs,
-                      t.ws, t.M, t.N, t.kbytes, t.e};
-  const dim3 grid(static_cast<uint32_t>(ceil_div(t.N, 16)));
+                      t.ws, t.M, t.N, t.kbytes, static_cast<uint32_t>(wide), t.e};
+  const dim3 grid(static_cast<uint32_t>(ceil_div(t.N, wide)));
   return launch_kernel(linear_rows_kernel<OP, 8>, grid, dim3(512), s, start, stop, a);
 }
 
@@ -1289,10 +1346,13 @@ hipError_t launch_fwd(const TileArgs& a, const mhc_linear_launch& plan, hipStrea
 
 // --- backward ---
 
-// Rows of grad_out that one block sums: at most 256 parts.
-int64_t bias_rows(int64_t M) {
-  const int64_t r = ceil_div(M, 256);
-  return r < 32 ? 32 : r;
+// Rows of grad_out that one block of linear_gz_kernel takes: about 512 blocks in
+// all, of at least 8 rows, in at most 256 parts of the bias's sums.
+int64_t bias_rows(int64_t M, int64_t N) {
+  const int64_t wide = ceil_div(N, 512);
+  const int64_t parts = wide >= 512 ? 1 : 512 / wide < 256 ? 512 / wide : 256;
+  const int64_t r = ceil_div(M, parts);
+  return r < 8 ? 8 : r;
 }
 
 struct BwdPlan {
@@ -1323,7 +1383,7 @@ BwdPlan plan_bwd(int64_t M, int64_t N, int64_t K, int32_t dtype) {
     return here;
   };
   p.gz = take(mul_bytes(M, N, 2));
-  p.bias = take(mul_bytes(ceil_div(M, bias_rows(M)), N, 4));
+  p.bias = take(mul_bytes(ceil_div(M, bias_rows(M, N)), N, 4));
   if (plan_product(M, K, N, dtype, &p.px) != MHC_SUCCESS ||
       plan_product(N, K, M, dtype, &p.pw) != MHC_SUCCESS)
     bad = true;
@@ -1409,7 +1469,7 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
     const BwdPlan p = plan_bwd(a.M, a.N, a.K, dtype);
     const S* gz = static_cast<const S*>(a.grad_out);
     if (a.act != MHC_ACT_NONE || a.gb != nullptr) {
-      const int64_t rows = bias_rows(a.M), parts = ceil_div(a.M, rows);
+      const int64_t rows = bias_rows(a.M, a.N), parts = ceil_div(a.M, rows);
       S* made = a.act != MHC_ACT_NONE ? reinterpret_cast<S*>(a.ws + p.gz) : nullptr;
       float* sums = a.gb != nullptr ? reinterpret_cast<float*>(a.ws + p.bias) : nullptr;
       const auto run = [&](auto kernel) {
@@ -1426,7 +1486,7 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
       if (e != hipSuccess) return e;
       if (made != nullptr) gz = made;
       if (a.gb != nullptr) {
-        e = launch_kernel(linear_bias_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(a.N, 256))), dim3(256),
+        e = launch_kernel(linear_bias_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(a.N, 64))), dim3(256),
                           s, nullptr, nullptr, sums, static_cast<S*>(a.gb), parts, a.N);
         if (e != hipSuccess) return e;
       }
