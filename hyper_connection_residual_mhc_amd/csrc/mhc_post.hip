@@ -21,6 +21,12 @@ typedef uint16_t bf16_t;
 // work, so any T fits the launch limits.
 constexpr int64_t kMaxBlocks = 1 << 20;
 
+// Calls that read more than the 256 MiB of the memory-side cache read
+// non-temporally: what an earlier kernel wrote is no longer there, and nothing
+// is read twice. n = 4, H = 7168: T = 4096 (294 and 528 MB read) forward 90.0 -> 83.8 us, backward 150.8 ->
+// 140.0; T = 1024 (73 and 132 MB) 20.9 -> 22.9 and 32.9 -> 37.1, so not there.
+constexpr int64_t kStreamBytes = 256LL << 20;
+
 // ---------------------------------------------------------------------------
 // Forward
 //
@@ -32,7 +38,7 @@ constexpr int64_t kMaxBlocks = 1 << 20;
 // ---------------------------------------------------------------------------
 constexpr int kSlice = 512;
 
-template <int N>
+template <int N, bool STREAM>
 __global__ __launch_bounds__(64) void post_fwd_kernel(
     const bf16_t* __restrict__ residual, const float* __restrict__ comb,
     const float* __restrict__ post, const bf16_t* __restrict__ y, bf16_t* __restrict__ out,
@@ -44,8 +50,8 @@ __global__ __launch_bounds__(64) void post_fwd_kernel(
     const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
     Chunk<kBF16> c[N], cy;
 #pragma unroll
-    for (int j = 0; j < N; ++j) c[j] = load_chunk<kBF16>(residual + (t * N + j) * H + h, count);
-    cy = load_chunk<kBF16>(y + t * H + h, count);
+    for (int j = 0; j < N; ++j) c[j] = load_chunk<kBF16, STREAM>(residual + (t * N + j) * H + h, count);
+    cy = load_chunk<kBF16, STREAM>(y + t * H + h, count);
     float m[N][N], p[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -85,7 +91,7 @@ __global__ __launch_bounds__(64) void post_fwd_kernel(
 //
 // The block size depends on H alone (and with it the order of the sums).
 // ---------------------------------------------------------------------------
-template <int N, int THREADS>
+template <int N, int THREADS, bool STREAM>
 __global__ __launch_bounds__(THREADS) void post_bwd_kernel(
     const bf16_t* __restrict__ grad_out, const bf16_t* __restrict__ residual,
     const float* __restrict__ comb, const float* __restrict__ post, const bf16_t* __restrict__ y,
@@ -111,10 +117,10 @@ __global__ __launch_bounds__(THREADS) void post_bwd_kernel(
       const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
       Chunk<kBF16> cg[N], cr[N], cy;
 #pragma unroll
-      for (int i = 0; i < N; ++i) cg[i] = load_chunk<kBF16>(grad_out + (t * N + i) * H + h, count);
+      for (int i = 0; i < N; ++i) cg[i] = load_chunk<kBF16, STREAM>(grad_out + (t * N + i) * H + h, count);
 #pragma unroll
-      for (int j = 0; j < N; ++j) cr[j] = load_chunk<kBF16>(residual + (t * N + j) * H + h, count);
-      cy = load_chunk<kBF16>(y + t * H + h, count);
+      for (int j = 0; j < N; ++j) cr[j] = load_chunk<kBF16, STREAM>(residual + (t * N + j) * H + h, count);
+      cy = load_chunk<kBF16, STREAM>(y + t * H + h, count);
       float g[N][8], v[8];
 #pragma unroll
       for (int i = 0; i < N; ++i) widen_chunk<kBF16>(cg[i], g[i]);
@@ -224,8 +230,10 @@ hipError_t launch_fwd(const bf16_t* residual, const float* comb, const float* po
                       hipEvent_t start, hipEvent_t stop) {
   const int64_t slices = (H + kSlice - 1) / kSlice;
   const int64_t blocks = T > kMaxBlocks / slices ? kMaxBlocks : T * slices;
-  return launch_kernel(post_fwd_kernel<N>, dim3(static_cast<uint32_t>(blocks)), dim3(64), s,
-                       start, stop, residual, comb, post, y, out, T, H, slices);
+  const bool stream = T * H * 2 * (N + 1) > kStreamBytes;
+  return launch_kernel(stream ? post_fwd_kernel<N, true> : post_fwd_kernel<N, false>,
+                       dim3(static_cast<uint32_t>(blocks)), dim3(64), s, start, stop, residual,
+                       comb, post, y, out, T, H, slices);
 }
 
 template <int N, int THREADS>
@@ -234,8 +242,9 @@ hipError_t launch_bwd_t(const bf16_t* grad_out, const bf16_t* residual, const fl
                         float* grad_comb, float* grad_post, bf16_t* grad_y, int64_t T, int64_t H,
                         hipStream_t s, hipEvent_t start, hipEvent_t stop) {
   const int64_t blocks = T < kMaxBlocks ? T : kMaxBlocks;
-  return launch_kernel(post_bwd_kernel<N, THREADS>, dim3(static_cast<uint32_t>(blocks)),
-                       dim3(THREADS), s, start, stop, grad_out, residual, comb, post, y,
+  const bool stream = T * H * 2 * (2 * N + 1) > kStreamBytes;
+  return launch_kernel(stream ? post_bwd_kernel<N, THREADS, true> : post_bwd_kernel<N, THREADS, false>,
+                       dim3(static_cast<uint32_t>(blocks)), dim3(THREADS), s, start, stop, grad_out, residual, comb, post, y,
                        grad_residual, grad_comb, grad_post, grad_y, T, H);
 }
 
@@ -243,7 +252,8 @@ template <int N, typename... A>
 hipError_t launch_bwd(int64_t H, A... a) {
   if (H <= 64 * 8) return launch_bwd_t<N, 64>(a...);
   if (H <= 128 * 8) return launch_bwd_t<N, 128>(a...);
-  return launch_bwd_t<N, 256>(a...);
+  if (H <= 256 * 8 || N == 8) return launch_bwd_t<N, 256>(a...);
+  return launch_bwd_t<N, 512>(a...);  // T = 4096, H = 7168, n = 4: 152.5 us, with 256 158.8
 }
 
 }  // namespace

@@ -24,9 +24,9 @@ constexpr float kE4M3Max = 448.0f;
 constexpr int64_t kMaxBlocks = 1 << 20;
 
 // Rows of up to kHeld columns stay in registers between the two passes (the
-// sum of squares, then the output): 4 chunks of 8 in each of 512 threads.
+// sum of squares, then the output): 2 chunks of 8 in each of 1024 threads.
 // Longer rows are read twice.
-constexpr int64_t kHeld = 512 * 4 * 8;
+constexpr int64_t kHeld = 1024 * 2 * 8;
 
 // Where a row comes from: 0 = x, 1 = x + residual, 2 / 4 / 8 = streams.
 constexpr int kPlain = 0;
@@ -46,6 +46,27 @@ __device__ __forceinline__ void load_weight(const void* weight, bool wide, int64
     widen_chunk<F>(load_chunk<F>(static_cast<const typename Store<F>::type*>(weight) + h, count),
                    w);
   }
+}
+
+// The same, raw: brought before the row's sum is known, widened after.
+template <int F>
+struct Weight {
+  Chunk<kF32> wide;
+  Chunk<F> same;
+};
+
+template <int F>
+__device__ __forceinline__ Weight<F> start_weight(const void* weight, bool wide, int64_t h, int count) {
+  Weight<F> w;
+  if (F == kF32 || wide) w.wide = load_chunk<kF32>(static_cast<const float*>(weight) + h, count);
+  else w.same = load_chunk<F>(static_cast<const typename Store<F>::type*>(weight) + h, count);
+  return w;
+}
+
+template <int F>
+__device__ __forceinline__ void take_weight(const Weight<F>& r, bool wide, float (&w)[8]) {
+  if (F == kF32 || wide) widen_chunk<kF32>(r.wide, w);
+  else widen_chunk<F>(r.same, w);
 }
 
 // Raw chunks of one row source.
@@ -118,7 +139,7 @@ __device__ __forceinline__ u32x2 pack_e4m3(const float (&v)[8]) {
 
 __device__ __forceinline__ void store_e4m3(uint8_t* p, int count, u32x2 c) {
   if (count >= 8) {
-    *reinterpret_cast<u32x2_at1*>(p) = c;
+    __builtin_nontemporal_store(c, reinterpret_cast<u32x2_at1*>(p));
     return;
   }
 #pragma unroll
@@ -186,17 +207,23 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
       if constexpr (kKeep) held[k] = c;
     };
     if constexpr (kKeep) {
-      Source<F, SRC> src[ITER];
-#pragma unroll
-      for (int k = 0; k < ITER; ++k) {
-        const int64_t h = k * kStep + threadIdx.x * 8;
-        if (h < H) load_source<F, SRC>(x, residual, t, H, h, static_cast<int>(min(H - h, static_cast<int64_t>(8))), src[k]);
-      }
+      // all of the thread's loads together, but for eight streams of two chunks
+      // (64 registers for them alone)
+      constexpr int kSets = SRC >= 8 ? 1 : ITER;
+      Source<F, SRC> src[kSets];
 #pragma unroll
       for (int k = 0; k < ITER; ++k) {
         const int64_t h = k * kStep + threadIdx.x * 8;
         held[k] = zero_chunk<F>();
-        if (h < H) first(k, src[k], h, static_cast<int>(min(H - h, static_cast<int64_t>(8))));
+        if (kSets == ITER && h < H)
+          load_source<F, SRC>(x, residual, t, H, h, static_cast<int>(min(H - h, static_cast<int64_t>(8))), src[k % kSets]);
+      }
+#pragma unroll
+      for (int k = 0; k < ITER; ++k) {
+        const int64_t h = k * kStep + threadIdx.x * 8;
+        const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
+        if (kSets != ITER && h < H) load_source<F, SRC>(x, residual, t, H, h, count, src[0]);
+        if (h < H) first(k, src[k % kSets], h, count);
       }
     } else {
       for (int64_t h = threadIdx.x * 8; h < H; h += kStep) {
@@ -204,6 +231,15 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
         Source<F, SRC> src;
         load_source<F, SRC>(x, residual, t, H, h, count, src);
         first(0, src, h, count);
+      }
+    }
+    Weight<F> kw[kKeep ? ITER : 1];
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < ITER; ++k) {
+        const int64_t h = k * kStep + threadIdx.x * 8;
+        if (h < H)
+          kw[k] = start_weight<F>(weight, wide_weight != 0, h, static_cast<int>(min(H - h, static_cast<int64_t>(8))));
       }
     }
     sum = block_sum<THREADS>(sum, part[0]);
@@ -220,7 +256,8 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
         widen_chunk<F>(make_stored<F, SRC>(src, p), v);
       }
       float w[8];
-      load_weight<F>(weight, wide_weight != 0, h, count, w);
+      if constexpr (kKeep) take_weight<F>(kw[k], wide_weight != 0, w);
+      else load_weight<F>(weight, wide_weight != 0, h, count, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = v[e] * r * w[e];
     };
@@ -300,11 +337,12 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
 // Backward
 //
 // Bound by memory: grad_y, s and grad_stored are read once and grad_x written
-// once. A block takes every gridDim.x-th row and keeps its part of the
-// weight's gradient in registers over all of them (8 ITER sums a thread); the
-// blocks' parts go to the workspace once, at the end, and a second kernel adds
-// them in ascending order of the block. The number of blocks depends on T
-// alone (bwd_blocks).
+// once. A block takes every gridDim.x-th row, with the next row's loads under
+// this one's sums, and keeps the weight and its part of the weight's gradient
+// in registers over all of them (8 ITER each a thread); the blocks' parts go to
+// the workspace once, at the end, and a second kernel adds them in ascending
+// order of the block. The number of blocks depends on T and H alone (bwd_blocks).
+// Rows of up to kFused columns: longer ones leave no room for all this.
 // ---------------------------------------------------------------------------
 template <int F, int THREADS, int ITER>
 __global__ __launch_bounds__(THREADS) void rms_norm_bwd_kernel(
@@ -315,164 +353,252 @@ __global__ __launch_bounds__(THREADS) void rms_norm_bwd_kernel(
     typename Store<F>::type* __restrict__ grad_x, float* __restrict__ partial, int64_t T,
     int64_t H) {
   constexpr int kStep = THREADS * 8;
-  __shared__ float part[THREADS / 64];
-  float dw[ITER][8];
+  __shared__ float part[2][THREADS / 64];
+  // chunk k of a row: its first column, and how many of its 8 exist
+  const auto column = [&](int k) { return static_cast<int64_t>(k) * kStep + threadIdx.x * 8; };
+  const auto count_of = [&](int k) {
+    return static_cast<int>(min(H - column(k), static_cast<int64_t>(8)));
+  };
+  struct Row {
+    Chunk<F> g[ITER], s[ITER], gs[ITER];
+    float r;
+  };
+  float w[ITER][8], dw[ITER][8];
 #pragma unroll
-  for (int k = 0; k < ITER; ++k)
+  for (int k = 0; k < ITER; ++k) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[k][e] = 0.0f;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    const float r = rstd[t];
-    Chunk<F> cg[ITER], cs[ITER];
+    for (int e = 0; e < 8; ++e) w[k][e] = dw[k][e] = 0.0f;
+    if (column(k) < H) load_weight<F>(weight, wide_weight != 0, column(k), count_of(k), w[k]);
+  }
+  const auto load = [&](int64_t t, Row& row) {
+    row.r = rstd[t];
 #pragma unroll
     for (int k = 0; k < ITER; ++k) {
-      const int64_t h = k * kStep + threadIdx.x * 8;
-      cg[k] = cs[k] = zero_chunk<F>();
-      if (h < H) {
-        const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
-        cg[k] = load_chunk<F>(grad_y + t * H + h, count);
-        cs[k] = load_chunk<F>(stored + t * H + h, count);
+      row.g[k] = row.s[k] = row.gs[k] = zero_chunk<F>();
+      if (column(k) < H) {
+        row.g[k] = load_chunk<F>(grad_y + t * H + column(k), count_of(k));
+        row.s[k] = load_chunk<F>(stored + t * H + column(k), count_of(k));
+        if (grad_stored != nullptr)
+          row.gs[k] = load_chunk<F>(grad_stored + t * H + column(k), count_of(k));
       }
     }
+  };
+  const auto pass = [&](int64_t t, const Row& row, float* sums) {
     float dot = 0.0f;
 #pragma unroll
     for (int k = 0; k < ITER; ++k) {
-      const int64_t h = k * kStep + threadIdx.x * 8;
-      if (h < H) {
-        const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
-        float g[8], s[8], w[8];
-        widen_chunk<F>(cg[k], g);
-        widen_chunk<F>(cs[k], s);
-        load_weight<F>(weight, wide_weight != 0, h, count, w);
+      float g[8], s[8];
+      widen_chunk<F>(row.g[k], g);
+      widen_chunk<F>(row.s[k], s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dot = fmaf(g[e] * w[e], s[e], dot);
-          dw[k][e] = fmaf(g[e], s[e] * r, dw[k][e]);
-        }
+      for (int e = 0; e < 8; ++e) {
+        dot = fmaf(g[e] * w[k][e], s[e], dot);
+        dw[k][e] = fmaf(g[e], s[e] * row.r, dw[k][e]);
       }
     }
-    dot = block_sum<THREADS>(dot, part);
-    const float c = dot / static_cast<float>(H) * (r * r);
+    dot = block_sum<THREADS>(dot, sums);
+    const float c = dot / static_cast<float>(H) * (row.r * row.r);
 #pragma unroll
     for (int k = 0; k < ITER; ++k) {
-      const int64_t h = k * kStep + threadIdx.x * 8;
-      if (h < H) {
-        const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
-        float g[8], s[8], w[8], o[8];
-        widen_chunk<F>(cg[k], g);
-        widen_chunk<F>(cs[k], s);
-        load_weight<F>(weight, wide_weight != 0, h, count, w);
+      if (column(k) < H) {
+        float g[8], s[8], gs[8], o[8];
+        widen_chunk<F>(row.g[k], g);
+        widen_chunk<F>(row.s[k], s);
+        widen_chunk<F>(row.gs[k], gs);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-s[e], c, g[e] * w[e]);
+        for (int e = 0; e < 8; ++e) o[e] = row.r * fmaf(-s[e], c, g[e] * w[k][e]);
         if (grad_stored != nullptr) {
-          widen_chunk<F>(load_chunk<F>(grad_stored + t * H + h, count), g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = o[e] + g[e];
+          for (int e = 0; e < 8; ++e) o[e] = o[e] + gs[e];
         }
         Chunk<F> q;
         narrow_chunk<F>(o, q);
-        store_chunk<F>(grad_x + t * H + h, count, q);
+        store_chunk<F>(grad_x + t * H + column(k), count_of(k), q);
       }
     }
-    if constexpr (THREADS > 64) __syncthreads();  // `part` is written again for the next row
+  };
+  // Rows in pairs, each row's sums in LDS of its own: a wave that writes a
+  // row's finds every wave past the sums of the row two before.
+  Row a, b;
+  int64_t t = blockIdx.x;
+  if (t < T) load(t, a);
+  while (t < T) {
+    const int64_t t1 = t + gridDim.x, t2 = t1 + gridDim.x;
+    if (t1 < T) load(t1, b);
+    pass(t, a, part[0]);
+    if (t1 >= T) break;
+    if (t2 < T) load(t2, a);
+    pass(t1, b, part[1]);
+    t = t2;
   }
 #pragma unroll
   for (int k = 0; k < ITER; ++k) {
-    const int64_t h = k * kStep + threadIdx.x * 8;
-    if (h < H) {
+    if (column(k) < H) {
       Chunk<kF32> c;
       narrow_chunk<kF32>(dw[k], c);
-      store_chunk<kF32>(partial + blockIdx.x * H + h, static_cast<int>(min(H - h, static_cast<int64_t>(8))), c);
+      store_chunk<kF32>(partial + blockIdx.x * H + column(k), count_of(k), c);
     }
   }
 }
 
-// Rows longer than the registers hold: grad_x in two passes over the row ...
-template <int F>
-__global__ __launch_bounds__(512) void rms_norm_bwd_long_kernel(
+// Longer rows: grad_x alone, a block to a row, ITER chunks of a thread held in
+// registers between the two passes (ITER = 0: read again) ...
+template <int F, int THREADS, int ITER>
+__global__ __launch_bounds__(THREADS) void rms_norm_bwd_row_kernel(
     const typename Store<F>::type* __restrict__ grad_y,
     const typename Store<F>::type* __restrict__ stored, const void* __restrict__ weight,
     int wide_weight, const float* __restrict__ rstd,
     const typename Store<F>::type* __restrict__ grad_stored,
     typename Store<F>::type* __restrict__ grad_x, int64_t T, int64_t H) {
-  __shared__ float part[8];
+  constexpr int kStep = THREADS * 8;
+  constexpr bool kKeep = ITER > 0;
+  constexpr int kSets = kKeep ? ITER : 1;
+  __shared__ float part[THREADS / 64];
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     const float r = rstd[t];
-    float dot = 0.0f;
-    for (int64_t h = threadIdx.x * 8; h < H; h += 512 * 8) {
+    Chunk<F> cg[kSets], cs[kSets], cgs[kSets];
+    const auto load = [&](int64_t h, int k) {
       const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
+      cg[k] = load_chunk<F>(grad_y + t * H + h, count);
+      cs[k] = load_chunk<F>(stored + t * H + h, count);
+    };
+    const auto load_more = [&](int64_t h, int k) {
+      cgs[k] = zero_chunk<F>();
+      if (grad_stored != nullptr)
+        cgs[k] = load_chunk<F>(grad_stored + t * H + h, static_cast<int>(min(H - h, static_cast<int64_t>(8))));
+    };
+    float dot = 0.0f;
+    const auto add = [&](int64_t h, int k) {
       float g[8], s[8], w[8];
-      widen_chunk<F>(load_chunk<F>(grad_y + t * H + h, count), g);
-      widen_chunk<F>(load_chunk<F>(stored + t * H + h, count), s);
-      load_weight<F>(weight, wide_weight != 0, h, count, w);
+      widen_chunk<F>(cg[k], g);
+      widen_chunk<F>(cs[k], s);
+      load_weight<F>(weight, wide_weight != 0, h, static_cast<int>(min(H - h, static_cast<int64_t>(8))), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) dot = fmaf(g[e] * w[e], s[e], dot);
+    };
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < ITER; ++k) {
+        const int64_t h = static_cast<int64_t>(k) * kStep + threadIdx.x * 8;
+        if (h < H) {
+          load(h, k);
+          load_more(h, k);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < ITER; ++k) {
+        const int64_t h = static_cast<int64_t>(k) * kStep + threadIdx.x * 8;
+        if (h < H) add(h, k);
+      }
+    } else {
+      for (int64_t h = threadIdx.x * 8; h < H; h += kStep) {
+        load(h, 0);
+        add(h, 0);
+      }
     }
-    dot = block_sum<512>(dot, part);
+    dot = block_sum<THREADS>(dot, part);
     const float c = dot / static_cast<float>(H) * (r * r);
-    for (int64_t h = threadIdx.x * 8; h < H; h += 512 * 8) {
+    const auto write = [&](int64_t h, int k) {
       const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
-      float g[8], s[8], w[8], o[8];
-      widen_chunk<F>(load_chunk<F>(grad_y + t * H + h, count), g);
-      widen_chunk<F>(load_chunk<F>(stored + t * H + h, count), s);
+      float g[8], s[8], w[8], gs[8], o[8];
+      widen_chunk<F>(cg[k], g);
+      widen_chunk<F>(cs[k], s);
+      widen_chunk<F>(cgs[k], gs);
       load_weight<F>(weight, wide_weight != 0, h, count, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = r * fmaf(-s[e], c, g[e] * w[e]);
       if (grad_stored != nullptr) {
-        widen_chunk<F>(load_chunk<F>(grad_stored + t * H + h, count), g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = o[e] + g[e];
+        for (int e = 0; e < 8; ++e) o[e] = o[e] + gs[e];
       }
       Chunk<F> q;
       narrow_chunk<F>(o, q);
       store_chunk<F>(grad_x + t * H + h, count, q);
+    };
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < ITER; ++k) {
+        const int64_t h = static_cast<int64_t>(k) * kStep + threadIdx.x * 8;
+        if (h < H) write(h, k);
+      }
+    } else {
+      for (int64_t h = threadIdx.x * 8; h < H; h += kStep) {
+        load(h, 0);
+        load_more(h, 0);
+        write(h, 0);
+      }
     }
-    __syncthreads();
+    __syncthreads();  // `part` is written again for the next row
   }
 }
 
-// ... and the weight's gradient, 2048 columns to a block, each column's rows
-// in ascending order.
+// ... and parts of the weight's gradient: 2048 columns and `rows` rows to a
+// block, each column's rows in ascending order, four rows' loads in flight.
 template <int F>
-__global__ __launch_bounds__(256) void rms_norm_bwd_long_weight_kernel(
+__global__ __launch_bounds__(256) void rms_norm_bwd_weight_kernel(
     const typename Store<F>::type* __restrict__ grad_y,
     const typename Store<F>::type* __restrict__ stored, const float* __restrict__ rstd,
-    float* __restrict__ grad_weight, int64_t T, int64_t H) {
+    float* __restrict__ partial, int64_t T, int64_t H, int64_t rows) {
+  constexpr int kAhead = 4;
   const int64_t h = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (h >= H) return;
   const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
+  const int64_t t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
   float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int64_t t = 0; t < T; ++t) {
-    const float r = rstd[t];
-    float g[8], s[8];
-    widen_chunk<F>(load_chunk<F>(grad_y + t * H + h, count), g);
-    widen_chunk<F>(load_chunk<F>(stored + t * H + h, count), s);
+  for (int64_t t = t0; t < t1; t += kAhead) {
+    Chunk<F> cg[kAhead], cs[kAhead];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[e] = fmaf(g[e], s[e] * r, dw[e]);
+    for (int k = 0; k < kAhead; ++k)
+      if (t + k < t1) {
+        cg[k] = load_chunk<F>(grad_y + (t + k) * H + h, count);
+        cs[k] = load_chunk<F>(stored + (t + k) * H + h, count);
+      }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (t + k < t1) {
+        const float r = rstd[t + k];
+        float g[8], s[8];
+        widen_chunk<F>(cg[k], g);
+        widen_chunk<F>(cs[k], s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[e] = fmaf(g[e], s[e] * r, dw[e]);
+      }
   }
   Chunk<kF32> c;
   narrow_chunk<kF32>(dw, c);
-  store_chunk<kF32>(grad_weight + h, count, c);
+  store_chunk<kF32>(partial + blockIdx.y * H + h, count, c);
 }
 
-// grad_weight[h] = sum over the blocks' parts: 64 columns to a block, each of
-// its four waves adds every fourth part in ascending order, then the four
-// results in ascending order. With no parts the sums are +0.0.
-__global__ __launch_bounds__(256) void rms_norm_bwd_reduce_kernel(const float* __restrict__ partial,
-                                                                  float* __restrict__ grad_weight,
-                                                                  int64_t parts, int64_t H) {
-  __shared__ float sums[4][64];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t h = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+// grad_weight[h] = sum over the blocks' parts: 16 columns to a block, each of 64
+// threads of a column adds every 64th part in ascending order, then the 64
+// results are added in ascending order, 8 by 8. With no parts the sums are +0.0.
+__global__ __launch_bounds__(1024) void rms_norm_bwd_reduce_kernel(const float* __restrict__ partial,
+                                                                   float* __restrict__ grad_weight,
+                                                                   int64_t parts, int64_t H) {
+  __shared__ float sums[64][17];
+  __shared__ float groups[8][16];
+  const int column = threadIdx.x % 16, lane = threadIdx.x / 16;
+  const int64_t h = static_cast<int64_t>(blockIdx.x) * 16 + column;
   float s = 0.0f;
   if (h < H) {
 #pragma unroll 8
-    for (int64_t k = wave; k < parts; k += 4) s += partial[k * H + h];
+    for (int64_t k = lane; k < parts; k += 64) s += partial[k * H + h];
   }
-  sums[wave][lane] = s;
+  sums[lane][column] = s;
   __syncthreads();
-  if (wave == 0 && h < H)
-    grad_weight[h] = ((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane];
+  if (lane < 8) {
+    s = sums[8 * lane][column];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += sums[8 * lane + k][column];
+    groups[lane][column] = s;
+  }
+  __syncthreads();
+  if (lane == 0 && h < H) {
+    s = groups[0][column];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += groups[k][column];
+    grad_weight[h] = s;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -566,8 +692,9 @@ hipError_t launch_fwd(const FwdArgs& a) {
 }
 
 // The block by the row's length alone, so that a row's sums have one order:
-// the fewest threads up to 512 that hold it in one chunk each, then 2 and 4
-// chunks a thread, then rows that are read twice.
+// the fewest threads up to 512 that hold it in one chunk each, then 512 and
+// 1024 with two, then rows that are read twice. T = 4096, H = 7168: one chunk in each of 1024 threads
+// is slower (the sum to e4m3 rows 46.9 us, two in each of 512 35.0).
 template <int F, int SRC, int FMT>
 hipError_t launch_fwd_h(const FwdArgs& a) {
   if (a.H <= 64 * 8) return launch_fwd<F, SRC, FMT, 64, 1>(a);
@@ -575,7 +702,7 @@ hipError_t launch_fwd_h(const FwdArgs& a) {
   if (a.H <= 256 * 8) return launch_fwd<F, SRC, FMT, 256, 1>(a);
   if (a.H <= 512 * 8) return launch_fwd<F, SRC, FMT, 512, 1>(a);
   if (a.H <= 512 * 16) return launch_fwd<F, SRC, FMT, 512, 2>(a);
-  if (a.H <= kHeld) return launch_fwd<F, SRC, FMT, 512, 4>(a);
+  if (a.H <= kHeld) return launch_fwd<F, SRC, FMT, 1024, 2>(a);
   return launch_fwd<F, SRC, FMT, 512, 0>(a);
 }
 
@@ -591,13 +718,34 @@ hipError_t launch_fwd_s(const FwdArgs& a, int32_t fmt) {
   return a.residual != nullptr ? launch_fwd_f<F, kAdd>(a, fmt) : launch_fwd_f<F, kPlain>(a, fmt);
 }
 
-// Blocks of the backward: enough to fill 256 CUs twice over, each with its
-// own part of the weight's gradient in the workspace.
-constexpr int64_t kBwdBlocks = 512;
+// Blocks of the backward: enough waves for the 256 CUs, each block with its own
+// part of the weight's gradient in the workspace (8 MiB in all at most). bf16 with
+// grad_stored, blocks against half and twice as many: T = 4096, H = 7168: 256 44.9 us (512 47.8);
+// T = 8192, H = 2048: 512 26.1 (1024 28.8); T = 8192, H = 512: 1024 13.5 (512 15.8, 4096 24.0).
+int64_t bwd_blocks(int64_t T, int64_t H) {
+  const int64_t blocks = H <= 1024 ? 1024 : H <= 4096 ? 512 : 256;
+  return T < blocks ? T : blocks;
+}
 
-int64_t bwd_blocks(int64_t T) { return T < kBwdBlocks ? T : kBwdBlocks; }
+// Rows of up to this many columns have both gradients from one kernel.
+constexpr int64_t kFused = 512 * 2 * 8;
 
-int64_t workspace_need(int64_t T, int64_t H) { return H <= kHeld ? bwd_blocks(T) * H * 4 : 0; }
+// Longer ones: rows of a block of the weight's kernel, about 1024 blocks in all of
+// at least 32 rows.
+int64_t weight_rows(int64_t T, int64_t H) {
+  const int64_t wide = (H + 2047) / 2048;
+  const int64_t parts = wide >= 1024 ? 1 : 1024 / wide;
+  const int64_t rows = (T + parts - 1) / parts;
+  return rows < 32 ? 32 : rows;
+}
+
+int64_t workspace_parts(int64_t T, int64_t H) {
+  if (H <= kFused) return bwd_blocks(T, H);
+  const int64_t rows = weight_rows(T, H);
+  return (T + rows - 1) / rows;
+}
+
+int64_t workspace_need(int64_t T, int64_t H) { return workspace_parts(T, H) * H * 4; }
 
 mhc_status validate_bwd(const void* grad_y, const void* stored, const void* weight,
                         int32_t weight_dtype, const void* rstd, const void* grad_stored,
@@ -634,14 +782,14 @@ struct BwdArgs {
 };
 
 hipError_t launch_reduce(const BwdArgs& a, int64_t parts, hipEvent_t start) {
-  return launch_kernel(rms_norm_bwd_reduce_kernel, dim3(static_cast<uint32_t>((a.H + 63) / 64)),
-                       dim3(256), a.s, start, a.stop, a.partial, a.grad_weight, parts, a.H);
+  return launch_kernel(rms_norm_bwd_reduce_kernel, dim3(static_cast<uint32_t>((a.H + 15) / 16)),
+                       dim3(1024), a.s, start, a.stop, a.partial, a.grad_weight, parts, a.H);
 }
 
 template <int F, int THREADS, int ITER>
 hipError_t launch_bwd(const BwdArgs& a) {
   typedef typename Store<F>::type S;
-  const int64_t blocks = bwd_blocks(a.T);
+  const int64_t blocks = bwd_blocks(a.T, a.H);
   const hipError_t e = launch_kernel(
       rms_norm_bwd_kernel<F, THREADS, ITER>, dim3(static_cast<uint32_t>(blocks)), dim3(THREADS),
       a.s, a.start, nullptr, static_cast<const S*>(a.grad_y), static_cast<const S*>(a.stored),
@@ -650,25 +798,33 @@ hipError_t launch_bwd(const BwdArgs& a) {
   return e != hipSuccess ? e : launch_reduce(a, blocks, nullptr);
 }
 
+template <int F, int THREADS, int ITER>
+hipError_t launch_bwd_row(const BwdArgs& a) {
+  typedef typename Store<F>::type S;
+  const int64_t blocks = a.T < kMaxBlocks ? a.T : kMaxBlocks;
+  hipError_t e = launch_kernel(
+      rms_norm_bwd_row_kernel<F, THREADS, ITER>, dim3(static_cast<uint32_t>(blocks)),
+      dim3(THREADS), a.s, a.start, nullptr, static_cast<const S*>(a.grad_y),
+      static_cast<const S*>(a.stored), a.weight, a.wide, a.rstd,
+      static_cast<const S*>(a.grad_stored), static_cast<S*>(a.grad_x), a.T, a.H);
+  if (e != hipSuccess) return e;
+  const int64_t rows = weight_rows(a.T, a.H), parts = workspace_parts(a.T, a.H);
+  e = launch_kernel(rms_norm_bwd_weight_kernel<F>,
+                    dim3(static_cast<uint32_t>((a.H + 2047) / 2048), static_cast<uint32_t>(parts)),
+                    dim3(256), a.s, nullptr, nullptr, static_cast<const S*>(a.grad_y),
+                    static_cast<const S*>(a.stored), a.rstd, a.partial, a.T, a.H, rows);
+  return e != hipSuccess ? e : launch_reduce(a, parts, nullptr);
+}
+
 template <int F>
 hipError_t launch_bwd_h(const BwdArgs& a) {
-  typedef typename Store<F>::type S;
   if (a.H <= 64 * 8) return launch_bwd<F, 64, 1>(a);
   if (a.H <= 128 * 8) return launch_bwd<F, 128, 1>(a);
   if (a.H <= 256 * 8) return launch_bwd<F, 256, 1>(a);
   if (a.H <= 512 * 8) return launch_bwd<F, 512, 1>(a);
-  if (a.H <= 512 * 16) return launch_bwd<F, 512, 2>(a);
-  if (a.H <= kHeld) return launch_bwd<F, 512, 4>(a);
-  const int64_t blocks = a.T < kMaxBlocks ? a.T : kMaxBlocks;
-  const hipError_t e = launch_kernel(
-      rms_norm_bwd_long_kernel<F>, dim3(static_cast<uint32_t>(blocks)), dim3(512), a.s, a.start,
-      nullptr, static_cast<const S*>(a.grad_y), static_cast<const S*>(a.stored), a.weight, a.wide,
-      a.rstd, static_cast<const S*>(a.grad_stored), static_cast<S*>(a.grad_x), a.T, a.H);
-  if (e != hipSuccess) return e;
-  return launch_kernel(rms_norm_bwd_long_weight_kernel<F>,
-                       dim3(static_cast<uint32_t>((a.H + 2047) / 2048)), dim3(256), a.s, nullptr,
-                       a.stop, static_cast<const S*>(a.grad_y), static_cast<const S*>(a.stored),
-                       a.rstd, a.grad_weight, a.T, a.H);
+  if (a.H <= kFused) return launch_bwd<F, 512, 2>(a);
+  if (a.H <= kHeld) return launch_bwd_row<F, 1024, 2>(a);
+  return launch_bwd_row<F, 512, 0>(a);
 }
 
 }  // namespace

@@ -149,7 +149,7 @@ def test_workspace_bytes(lib):
     f = lib.mhc_rms_norm_bwd_workspace_bytes
     assert f(0, 64) == 0 and f(1, 64) == 256 and f(100, 64) == 25600
     assert f(1 << 20, 64) == f(1 << 21, 64) > 0
-    assert f(10, 20000) == 0 and f(-1, 64) == -1 and f(1, 0) == -1 and f(1, (1 << 26) + 1) == -1
+    assert f(10, 20000) == 80000 and f(33, 20000) == 160000 and f(-1, 64) == -1 and f(1, 0) == -1 and f(1, (1 << 26) + 1) == -1
 
 
 def test_python_refusals(built_library):
