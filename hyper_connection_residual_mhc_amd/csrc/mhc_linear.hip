@@ -220,7 +220,8 @@ struct TileArgs {
   const uint8_t* xs;  // kMX
   const uint8_t* ws;  // kMX
   int64_t M, N;
-  uint32_t kbytes;    // bytes of k that count
+  uint32_t kbytes;    // bytes of k that count, in rows that run along it
+  uint32_t kturned;   // and in operands where k runs down (no more than kbytes: rows may be padded)
   uint32_t tiles_m, tiles_n;
   uint32_t splits, per_split;  // parts of the sum, and tiles of kTileK in each
   float* partial;              // [splits][M][N] where splits > 1
@@ -286,6 +287,7 @@ struct Operand {
   uint32_t row, piece;
   uint32_t ld;
   uint32_t here;    // rows (columns) that exist
+  uint32_t kbytes;  // bytes of k that exist
   i32x4 held[2][DMA ? 1 : Q];  // through registers: two tiles on their way
 
   static __device__ __forceinline__ uint32_t swap(uint32_t row) {
@@ -301,8 +303,9 @@ struct Operand {
     }
   }
 
-  __device__ __forceinline__ void init(const Matrix& m, int64_t first, uint32_t kbytes) {
+  __device__ __forceinline__ void init(const Matrix& m, int64_t first, const TileArgs& a) {
     const int64_t left = m.count - first;
+    kbytes = TURNED ? a.kturned : a.kbytes;
     here = static_cast<uint32_t>(left < SPAN ? left : SPAN);
     ld = static_cast<uint32_t>(m.ld);
     base = static_cast<const uint8_t*>(m.p) + (TURNED ? first * ELEM : first * m.ld);
@@ -314,7 +317,7 @@ struct Operand {
 
   // Starts the loads of round q of the tile kt into `to`, the tile's place in LDS.
   template <int SET = 0>
-  __device__ __forceinline__ void start(uint32_t kt, uint32_t kbytes, uint32_t to, int q) {
+  __device__ __forceinline__ void start(uint32_t kt, uint32_t to, int q) {
     const uint32_t rows = q * kEach;
     if constexpr (DMA) {
       const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -581,8 +584,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
   const uint32_t wm = wave / WN, wn = wave % WN;
   OpX lx;
   OpW lw;
-  lx.init(a.x, place.m0, a.kbytes);
-  lw.init(a.w, place.n0, a.kbytes);
+  lx.init(a.x, place.m0, a);
+  lw.init(a.w, place.n0, a);
   Reader<OpX, TX, false, 1> rx;
   Reader<OpW, TW, true, G> rw;
   rx.init(wm * (TI * 16));
@@ -670,9 +673,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
   const auto start = [&](uint32_t kt, uint32_t stage) {
     const uint32_t to = at0 + stage * kBuffer;
 #pragma unroll
-    for (int q = 0; q < OpX::Q; ++q) lx.start(kt, a.kbytes, to, q);
+    for (int q = 0; q < OpX::Q; ++q) lx.start(kt, to, q);
 #pragma unroll
-    for (int q = 0; q < OpW::Q; ++q) lw.start(kt, a.kbytes, to + BM * kTileK, q);
+    for (int q = 0; q < OpW::Q; ++q) lw.start(kt, to + BM * kTileK, q);
     if constexpr (kScales && DMA)
       load_to_lds<4>(kt < all ? so : kOutside, sr, kt * 4, at1 + stage * (kThreads * 4) + wave * 256);
   };
@@ -693,9 +696,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
       constexpr int S = decltype(set)::value;
       if (kt < last) {
 #pragma unroll
-        for (int q = 0; q < OpX::Q; ++q) lx.template start<S>(kt, a.kbytes, 0, q);
+        for (int q = 0; q < OpX::Q; ++q) lx.template start<S>(kt, 0, q);
 #pragma unroll
-        for (int q = 0; q < OpW::Q; ++q) lw.template start<S>(kt, a.kbytes, 0, q);
+        for (int q = 0; q < OpW::Q; ++q) lw.template start<S>(kt, 0, q);
       }
     };
     const auto pass = [&](uint32_t kt, auto set) {
@@ -767,8 +770,8 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
   static_assert(OpX::Q == TJ && OpW::Q == TJ, "one round of loads for each W tile");
   OpX lx;
   OpW lw;
-  lx.init(a.x, place.m0, a.kbytes);
-  lw.init(a.w, place.n0, a.kbytes);
+  lx.init(a.x, place.m0, a);
+  lw.init(a.w, place.n0, a);
   Reader<OpX, TX, false, 1> rx;
   Reader<OpW, TW, true, 4> rw;
   rx.init(wm * (TI * 16));
@@ -787,8 +790,8 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
   }
   const uint32_t at0 = lds_address(&lds[0][0]), at1 = lds_address(&scales[0][0]);
   const auto start = [&](uint32_t kt, uint32_t b, int q) {
-    lx.start(kt, a.kbytes, at0 + b * kBuffer, q);
-    lw.start(kt, a.kbytes, at0 + b * kBuffer + BM * kTileK, q);
+    lx.start(kt, at0 + b * kBuffer, q);
+    lw.start(kt, at0 + b * kBuffer + BM * kTileK, q);
   };
   // kMX: the scales of four tiles from kt on, 16 bytes of each row.
   const auto start_scales = [&](uint32_t kt, uint32_t b) {
@@ -1053,6 +1056,62 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// Rows that are no whole pieces
+//
+// Operands whose rows are no multiple of 16 bytes cannot be loaded straight into
+// LDS. Where the product is long enough they are copied into the workspace
+// first, rows padded with zeros: one pass over them, against tiles that go
+// through registers (2048 x 2048 x 2047 in bf16: 54 us, backward 105 and 106 us a product;
+// with whole rows 35 and 36).
+// ---------------------------------------------------------------------------
+
+struct PadJob {
+  const uint8_t* in;
+  uint8_t* out;
+  int64_t rows;
+  int64_t bytes;   // of a row of `in`
+  int64_t pieces;  // 16-byte pieces of a row of `out` (of 4 bytes where `narrow`)
+  int32_t narrow;
+};
+
+constexpr int kMostJobs = 4;
+
+struct PadJobs {
+  PadJob job[kMostJobs];
+};
+
+// Job blockIdx.y; a thread moves whole pieces of the padded rows.
+__global__ __launch_bounds__(256) void linear_pad_kernel(PadJobs jobs) {
+  const PadJob& j = jobs.job[blockIdx.y];
+  const int size = j.narrow ? 4 : 16;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < j.rows * j.pieces;
+       id += step) {
+    const int64_t row = id / j.pieces, at = (id - row * j.pieces) * size;
+    const uint8_t* p = j.in + row * j.bytes + at;
+    const int64_t left = j.bytes - at;
+    typedef u32x4 u32x4_at1 __attribute__((aligned(1)));
+    u32x4 v = {0, 0, 0, 0};
+    if (left >= size && size == 16) {
+      v = *reinterpret_cast<const u32x4_at1*>(p);
+    } else {
+      uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < left && i < size) u[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+      v = u32x4{u[0], u[1], u[2], u[3]};
+    }
+    uint8_t* q = j.out + (row * j.pieces) * size + at;
+    if (size == 16) {
+      *reinterpret_cast<u32x4*>(q) = v;
+    } else {
+      const uint32_t w = v[0];
+      *reinterpret_cast<uint32_t*>(q) = w;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Backward
 //
 // gz and the bias's sums come from one pass over grad_out and z; the two
@@ -1067,7 +1126,7 @@ template <int F, int ACT>
 __global__ __launch_bounds__(256) void linear_gz_kernel(
     const typename Store<F>::type* __restrict__ grad_out,
     const typename Store<F>::type* __restrict__ z, typename Store<F>::type* __restrict__ gz,
-    float* __restrict__ partial, int64_t M, int64_t N, int64_t rows) {
+    float* __restrict__ partial, int64_t M, int64_t N, int64_t ldz, int64_t rows) {
   constexpr int kAhead = 4;
   __shared__ float sums[4][512];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -1095,7 +1154,8 @@ __global__ __launch_bounds__(256) void linear_gz_kernel(
             for (int i = 0; i < 8; ++i) v[i] = v[i] * slope<ACT>(s[i]);
             Chunk<F> c;
             narrow_chunk<F>(v, c);
-            store_chunk<F>(gz + (m + 4 * k) * N + n, count, c);
+            // rows of gz are ldz long, zeros past N
+            store_chunk<F>(gz + (m + 4 * k) * ldz + n, static_cast<int>(min(ldz - n, static_cast<int64_t>(8))), c);
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[i] = sum[i] + v[i];
@@ -1206,9 +1266,11 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
   const int64_t all = ceil_div(K * elem(dtype), kTileK);
   int64_t s = parts;
   if (s == 0) {
-    // two blocks for each CU, and at least 4 tiles of the sum in each part
+    // at least 4 tiles of the sum in each part, and at most two blocks for each
+    // CU, of the wide tiles one: 2048^3 in bf16 in one part of 256 blocks 25.8 us, in two
+    // parts 34; 17 x 7168 x 4096 in four parts of 112 small tiles 14.6, in two 21.9
     s = 1;
-    const int64_t slots = k == MHC_LINEAR_LARGE ? 256 : 512;
+    const int64_t slots = k >= MHC_LINEAR_MEDIUM ? 256 : 512;
     while (s < kMaxSplits && M > 0 && tiles(k) * s * 2 <= slots && all / (s * 2) >= 4) s *= 2;
   }
   if (s > all) s = all;
@@ -1218,24 +1280,78 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
   return ok();
 }
 
-int64_t fwd_workspace(int64_t M, int64_t N, const mhc_linear_launch& plan) {
-  return plan.splits > 1 ? mul_bytes(mul_bytes(M, N, 4), plan.splits, 1) : 0;
+int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
+
+// Products of at least this many terms have operands without whole rows copied
+// first. Forward, with at least kPadRows rows of each: 2048 x 2048 x 2047 in bf16 54 us
+// through registers, 38 with copies; 256 x 4096 x 4095 35 and 38. The backward's turned
+// operands lose more: 1024 x 1024 x 1023 25 us a product through registers, 19 with copies,
+// 4096 x 4096 x 2047 316 and 78.
+constexpr int64_t kPadForward = 1LL << 31;
+constexpr int64_t kPadRows = 512;
+constexpr int64_t kPadBackward = 1LL << 29;
+
+// Places in the workspace, in bytes, each from a multiple of 256 on; `total` is
+// -1 where a size does not fit.
+struct Places {
+  int64_t total = 0;
+  int64_t take(int64_t bytes) {
+    const int64_t here = total;
+    if (total < 0 || bytes < 0 || bytes > INT64_MAX - 256 ||
+        __builtin_add_overflow(total, round_up(bytes, 256), &total)) {
+      total = -1;
+      return 0;
+    }
+    return here;
+  }
+};
+
+struct FwdPlan {
+  mhc_linear_launch launch;
+  bool pad;
+  int64_t ld, scale_ld;               // bytes of padded rows
+  int64_t part, x, w, xs, ws, total;  // places
+};
+
+FwdPlan plan_fwd(int64_t M, int64_t N, int64_t K, int32_t dtype, const mhc_linear_launch& launch) {
+  FwdPlan p = {};
+  p.launch = launch;
+  if (M == 0) return p;
+  Places at;
+  p.part = launch.splits > 1 ? at.take(mul_bytes(mul_bytes(M, N, 4), launch.splits, 1)) : 0;
+  const int64_t row = K * elem(dtype), whole = dtype == MHC_LINEAR_E4M3_MX ? kTileK : 16;
+  p.pad = launch.kernel != MHC_LINEAR_ROWS && row % whole != 0 && M >= kPadRows && N >= kPadRows &&
+          (M > INT64_MAX / N / K || M * N * K >= kPadForward);
+  if (p.pad) {
+    p.ld = round_up(row, whole);
+    p.x = at.take(mul_bytes(M, p.ld, 1));
+    p.w = at.take(mul_bytes(N, p.ld, 1));
+    if (dtype == MHC_LINEAR_E4M3_MX) {
+      p.scale_ld = p.ld / 32;
+      p.xs = at.take(mul_bytes(M, p.scale_ld, 1));
+      p.ws = at.take(mul_bytes(N, p.scale_ld, 1));
+    }
+  }
+  p.total = at.total;
+  return p;
 }
 
 mhc_status validate_fwd(const void* x, const void* xs, const void* w, const void* ws,
                         const void* bias, const void* residual, const void* out, const void* z,
                         const void* workspace, int64_t workspace_bytes, int64_t M, int64_t N,
                         int64_t K, int32_t dtype, int32_t act, const mhc_linear_launch* launch,
-                        mhc_linear_launch* plan) {
+                        FwdPlan* plan) {
+  mhc_linear_launch chosen;
   mhc_status st = check_sizes(M, N, K, dtype);
   if (st != MHC_SUCCESS) return st;
   if (act < MHC_ACT_NONE || act > MHC_ACT_GELU)
     return fail(MHC_ERROR_INVALID_VALUE, "unknown activation %d", act);
-  if ((st = make_plan(M, N, K, dtype, launch, plan)) != MHC_SUCCESS) return st;
+  if ((st = make_plan(M, N, K, dtype, launch, &chosen)) != MHC_SUCCESS) return st;
+  *plan = plan_fwd(M, N, K, dtype, chosen);
   if (!is8(dtype) && (xs != nullptr || ws != nullptr))
     return fail(MHC_ERROR_INVALID_VALUE, "16-bit operands have no scales");
   if (M == 0) return ok();
-  const int64_t need = fwd_workspace(M, N, *plan);
+  const int64_t need = plan->total;
   if (need < 0) return fail(MHC_ERROR_INVALID_VALUE, "the workspace's size does not fit 64 bits");
   if (workspace_bytes < need)
     return fail(MHC_ERROR_INVALID_VALUE, "workspace_bytes %lld < %lld needed",
@@ -1252,21 +1368,21 @@ mhc_status validate_fwd(const void* x, const void* xs, const void* w, const void
                        {residual, residual != nullptr ? MN : 0, 2, "residual"}};
   const Tensor outs[] = {{out, MN, 2, "out"},
                          {z, z != nullptr ? MN : 0, 2, "z"},
-                         {workspace, need, 4, "workspace"}};
+                         {workspace, need, 16, "workspace"}};
   return check_tensors(in, outs);
 }
 
 // Whether an operand can be loaded straight into LDS: whole, aligned 16-byte
 // pieces, and where k runs down the rows all of it within a buffer's 31 bits.
 template <bool TURNED>
-bool whole(const Matrix& m, uint32_t kbytes) {
+bool whole(const Matrix& m, const TileArgs& a) {
   if (reinterpret_cast<uintptr_t>(m.p) % 16 != 0 || m.ld % 16 != 0) return false;
-  return TURNED ? static_cast<int64_t>(kbytes / 2) * m.ld <= INT32_MAX : kbytes % 16 == 0;
+  return TURNED ? static_cast<int64_t>(a.kturned / 2) * m.ld <= INT32_MAX : a.kbytes % 16 == 0;
 }
 
 template <int OP, bool TX, bool TW>
 bool straight(const TileArgs& a) {
-  if (!whole<TX>(a.x, a.kbytes) || !whole<TW>(a.w, a.kbytes)) return false;
+  if (!whole<TX>(a.x, a) || !whole<TW>(a.w, a)) return false;
   // block scales come four of a row at a time
   return OP != kOpMX || (a.kbytes % kTileK == 0 && reinterpret_cast<uintptr_t>(a.xs) % 4 == 0 &&
                          reinterpret_cast<uintptr_t>(a.ws) % 4 == 0);
@@ -1337,11 +1453,46 @@ hipError_t launch_rows(const TileArgs& t, hipStream_t s, hipEvent_t start, hipEv
   return launch_kernel(linear_rows_kernel<OP, 8>, grid, dim3(512), s, start, stop, a);
 }
 
+PadJob pad_job(const void* in, void* out, int64_t rows, int64_t bytes, int64_t ld, bool narrow) {
+  return {static_cast<const uint8_t*>(in), static_cast<uint8_t*>(out), rows, bytes,
+          ld / (narrow ? 4 : 16), narrow ? 1 : 0};
+}
+
+hipError_t launch_pad(const PadJobs& jobs, int count, hipStream_t s, hipEvent_t start) {
+  int64_t most = 1;
+  for (int i = 0; i < count; ++i) {
+    const int64_t blocks = ceil_div(jobs.job[i].rows * jobs.job[i].pieces, 256);
+    if (blocks > most) most = blocks;
+  }
+  return launch_kernel(linear_pad_kernel, dim3(static_cast<uint32_t>(most < 4096 ? most : 4096), static_cast<uint32_t>(count)),
+                       dim3(256), s, start, nullptr, jobs);
+}
+
 template <int OP>
-hipError_t launch_fwd(const TileArgs& a, const mhc_linear_launch& plan, hipStream_t s,
+hipError_t launch_fwd(TileArgs a, const FwdPlan& p, uint8_t* workspace, hipStream_t s,
                       hipEvent_t start, hipEvent_t stop) {
-  if (plan.kernel == MHC_LINEAR_ROWS) return launch_rows<OP>(a, s, start, stop);
-  return launch_product<OP, false, false>(a, plan, s, start, stop);
+  if (p.launch.kernel == MHC_LINEAR_ROWS) return launch_rows<OP>(a, s, start, stop);
+  a.partial = reinterpret_cast<float*>(workspace + p.part);
+  if (p.pad) {
+    PadJobs jobs = {};
+    int count = 0;
+    const int64_t blocks = (a.kbytes + 31) / 32;
+    jobs.job[count++] = pad_job(a.x.p, workspace + p.x, a.M, a.kbytes, p.ld, false);
+    jobs.job[count++] = pad_job(a.w.p, workspace + p.w, a.N, a.kbytes, p.ld, false);
+    if (OP == kOpMX) {
+      jobs.job[count++] = pad_job(a.xs, workspace + p.xs, a.M, blocks, p.scale_ld, true);
+      jobs.job[count++] = pad_job(a.ws, workspace + p.ws, a.N, blocks, p.scale_ld, true);
+      a.xs = workspace + p.xs;
+      a.ws = workspace + p.ws;
+    }
+    const hipError_t e = launch_pad(jobs, count, s, start);
+    if (e != hipSuccess) return e;
+    start = nullptr;
+    a.x = {workspace + p.x, a.M, p.ld};
+    a.w = {workspace + p.w, a.N, p.ld};
+    a.kbytes = static_cast<uint32_t>(p.ld);
+  }
+  return launch_product<OP, false, false>(a, p.launch, s, start, stop);
 }
 
 // --- backward ---
@@ -1356,11 +1507,11 @@ int64_t bias_rows(int64_t M, int64_t N) {
 }
 
 struct BwdPlan {
-  int64_t gz, bias, part, total;  // byte offsets in the workspace; part: split sums
-  mhc_linear_launch px, pw;       // the two products
+  bool pad_k, pad_n;               // rows along K (x, W) and along N (gz) are copied whole
+  int64_t ldk, ldn;                // their bytes
+  int64_t gz, bias, x, w, part, total;  // places; part: split sums
+  mhc_linear_launch px, pw;        // the two products
 };
-
-int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 
 // A product of the backward: the tile kernels from 64 x 64 on.
 mhc_status plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, mhc_linear_launch* p) {
@@ -1370,26 +1521,30 @@ mhc_status plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, mhc_line
   return make_plan(M, N, K, dtype, &small, p);
 }
 
-// -1 in total where a size does not fit.
 BwdPlan plan_bwd(int64_t M, int64_t N, int64_t K, int32_t dtype) {
   BwdPlan p = {};
   if (M == 0) return p;
-  int64_t at = 0;
-  bool bad = false;
-  const auto take = [&](int64_t bytes) {
-    const int64_t here = at;
-    if (bytes < 0 || bytes > INT64_MAX - 256 || __builtin_add_overflow(at, round_up(bytes, 256), &at))
-      bad = true;
-    return here;
-  };
-  p.gz = take(mul_bytes(M, N, 2));
-  p.bias = take(mul_bytes(ceil_div(M, bias_rows(M, N)), N, 4));
+  Places at;
+  const bool large = M > INT64_MAX / N / K || M * N * K >= kPadBackward;
+  p.pad_k = large && K % 8 != 0;
+  p.pad_n = large && N % 8 != 0;
+  p.ldk = p.pad_k ? round_up(K * 2, 16) : K * 2;
+  p.ldn = p.pad_n ? round_up(N * 2, 16) : N * 2;
+  p.gz = at.take(mul_bytes(M, p.ldn, 1));
+  p.bias = at.take(mul_bytes(ceil_div(M, bias_rows(M, N)), N, 4));
+  if (p.pad_k) {
+    p.x = at.take(mul_bytes(M, p.ldk, 1));
+    p.w = at.take(mul_bytes(N, p.ldk, 1));
+  }
   if (plan_product(M, K, N, dtype, &p.px) != MHC_SUCCESS ||
       plan_product(N, K, M, dtype, &p.pw) != MHC_SUCCESS)
-    bad = true;
-  const int64_t a = fwd_workspace(M, K, p.px), b = fwd_workspace(N, K, p.pw);
-  p.part = take(a < 0 || b < 0 ? -1 : a > b ? a : b);
-  p.total = bad ? -1 : at;
+    at.total = -1;
+  const auto parts = [](int64_t rows, int64_t columns, const mhc_linear_launch& l) {
+    return l.splits > 1 ? mul_bytes(mul_bytes(rows, columns, 4), l.splits, 1) : 0;
+  };
+  const int64_t a = parts(M, K, p.px), b = parts(N, K, p.pw);
+  p.part = at.take(a < 0 || b < 0 ? -1 : a > b ? a : b);
+  p.total = at.total;
   return p;
 }
 
@@ -1468,6 +1623,23 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
   } else {
     const BwdPlan p = plan_bwd(a.M, a.N, a.K, dtype);
     const S* gz = static_cast<const S*>(a.grad_out);
+    const void *x = a.x, *w = a.w;
+    PadJobs jobs = {};
+    int count = 0;
+    if (p.pad_k && a.gw != nullptr) {
+      jobs.job[count++] = pad_job(a.x, a.ws + p.x, a.M, a.K * 2, p.ldk, false);
+      x = a.ws + p.x;
+    }
+    if (p.pad_k && a.gx != nullptr) {
+      jobs.job[count++] = pad_job(a.w, a.ws + p.w, a.N, a.K * 2, p.ldk, false);
+      w = a.ws + p.w;
+    }
+    const bool products = a.gx != nullptr || a.gw != nullptr;
+    if (p.pad_n && a.act == MHC_ACT_NONE && products) {
+      jobs.job[count++] = pad_job(a.grad_out, a.ws + p.gz, a.M, a.N * 2, p.ldn, false);
+      gz = reinterpret_cast<const S*>(a.ws + p.gz);
+    }
+    if (count > 0 && (e = launch_pad(jobs, count, s, marks.first())) != hipSuccess) return e;
     if (a.act != MHC_ACT_NONE || a.gb != nullptr) {
       const int64_t rows = bias_rows(a.M, a.N), parts = ceil_div(a.M, rows);
       S* made = a.act != MHC_ACT_NONE ? reinterpret_cast<S*>(a.ws + p.gz) : nullptr;
@@ -1475,7 +1647,7 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
       const auto run = [&](auto kernel) {
         return launch_kernel(kernel, dim3(static_cast<uint32_t>(ceil_div(a.N, 512)), static_cast<uint32_t>(parts)),
                              dim3(256), s, marks.first(), nullptr, static_cast<const S*>(a.grad_out),
-                             static_cast<const S*>(a.z), made, sums, a.M, a.N, rows);
+                             static_cast<const S*>(a.z), made, sums, a.M, a.N, p.ldn / 2, rows);
       };
       switch (a.act) {
         case MHC_ACT_RELU: e = run(linear_gz_kernel<F, MHC_ACT_RELU>); break;
@@ -1494,10 +1666,11 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
     if (a.gx != nullptr) {
       // grad_x [M, K]: rows of gz, with W [N, K] turned
       TileArgs t = {};
-      t.x = {gz, a.M, a.N * 2};
-      t.w = {a.w, a.K, a.K * 2};
+      t.x = {gz, a.M, p.ldn};
+      t.w = {w, a.K, p.ldk};
       t.M = a.M; t.N = a.K;
-      t.kbytes = static_cast<uint32_t>(a.N * 2);
+      t.kbytes = static_cast<uint32_t>(p.ldn);  // gz's padding is zeros
+      t.kturned = static_cast<uint32_t>(a.N * 2);
       t.partial = reinterpret_cast<float*>(a.ws + p.part);
       t.e.out = a.gx; t.e.N = a.K;
       e = launch_product<OP, false, true>(t, p.px, s, marks.first(), nullptr);
@@ -1506,10 +1679,10 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
     if (a.gw != nullptr) {
       // grad_weight [N, K]: gz [M, N] and x [M, K], both turned
       TileArgs t = {};
-      t.x = {gz, a.N, a.N * 2};
-      t.w = {a.x, a.K, a.K * 2};
+      t.x = {gz, a.N, p.ldn};
+      t.w = {x, a.K, p.ldk};
       t.M = a.N; t.N = a.K;
-      t.kbytes = static_cast<uint32_t>(a.M * 2);
+      t.kbytes = t.kturned = static_cast<uint32_t>(a.M * 2);
       t.partial = reinterpret_cast<float*>(a.ws + p.part);
       t.e.out = a.gw; t.e.N = a.K;
       e = launch_product<OP, true, true>(t, p.pw, s, marks.first(), nullptr);
@@ -1543,7 +1716,7 @@ int64_t mhc_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t 
   if (check_sizes(M, N, K, dtype) != MHC_SUCCESS ||
       make_plan(M, N, K, dtype, launch, &p) != MHC_SUCCESS)
     return -1;
-  return fwd_workspace(M, N, p);
+  return plan_fwd(M, N, K, dtype, p).total;
 }
 
 int64_t mhc_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
@@ -1557,7 +1730,7 @@ mhc_status mhc_linear_validate_fwd(const void* x, const void* x_scales, const vo
                                    const void* workspace, int64_t workspace_bytes, int64_t M,
                                    int64_t N, int64_t K, int32_t dtype, int32_t act,
                                    const mhc_linear_launch* launch) {
-  mhc_linear_launch plan;
+  FwdPlan plan;
   return validate_fwd(x, x_scales, weight, weight_scales, bias, residual, out, z, workspace,
                       workspace_bytes, M, N, K, dtype, act, launch, &plan);
 }
@@ -1576,7 +1749,7 @@ mhc_status mhc_linear_fwd(const void* x, const void* x_scales, const void* weigh
                           void* out, void* z, void* workspace, int64_t workspace_bytes, int64_t M,
                           int64_t N, int64_t K, int32_t dtype, int32_t act, void* stream,
                           const mhc_linear_launch* launch, void* start_event, void* stop_event) {
-  mhc_linear_launch plan;
+  FwdPlan plan;
   const mhc_status st = validate_fwd(x, x_scales, weight, weight_scales, bias, residual, out, z,
                                      workspace, workspace_bytes, M, N, K, dtype, act, launch, &plan);
   if (st != MHC_SUCCESS) return st;
@@ -1595,7 +1768,6 @@ mhc_status mhc_linear_fwd(const void* x, const void* x_scales, const void* weigh
   a.M = M;
   a.N = N;
   a.kbytes = static_cast<uint32_t>(ld);
-  a.partial = static_cast<float*>(workspace);
   a.e.bias = bias;
   a.e.residual = residual;
   a.e.out = out;
@@ -1604,12 +1776,13 @@ mhc_status mhc_linear_fwd(const void* x, const void* x_scales, const void* weigh
   a.e.act = act;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const hipEvent_t b = static_cast<hipEvent_t>(start_event), f = static_cast<hipEvent_t>(stop_event);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   hipError_t e;
   switch (dtype) {
-    case MHC_LINEAR_BF16: e = launch_fwd<kOpBF16>(a, plan, s, b, f); break;
-    case MHC_LINEAR_F16: e = launch_fwd<kOpF16>(a, plan, s, b, f); break;
-    case MHC_LINEAR_E4M3_ROW: e = launch_fwd<kOpE4M3>(a, plan, s, b, f); break;
-    default: e = launch_fwd<kOpMX>(a, plan, s, b, f); break;
+    case MHC_LINEAR_BF16: e = launch_fwd<kOpBF16>(a, plan, ws, s, b, f); break;
+    case MHC_LINEAR_F16: e = launch_fwd<kOpF16>(a, plan, ws, s, b, f); break;
+    case MHC_LINEAR_E4M3_ROW: e = launch_fwd<kOpE4M3>(a, plan, ws, s, b, f); break;
+    default: e = launch_fwd<kOpMX>(a, plan, ws, s, b, f); break;
   }
   return launch_status(e, "product launch");
 }

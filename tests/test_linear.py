@@ -139,7 +139,8 @@ def test_launches(lib):
         for dtype in (1, 4):
             p = L.mhc_linear_plan(100, 100, 4096, dtype, {"kernel": kernel, "splits": 3})
             assert p == {"kernel": kernel, "splits": 3}
-            assert L.mhc_linear_fwd_workspace_bytes(100, 100, 4096, dtype, p) == 100 * 100 * 4 * 3
+            need = 100 * 100 * 4 * 3                        # each part's sums, from a multiple of 256 bytes on
+            assert L.mhc_linear_fwd_workspace_bytes(100, 100, 4096, dtype, p) == -(-need // 256) * 256
             assert L.mhc_linear_plan(100, 100, 60, dtype, {"kernel": kernel, "splits": 8})["splits"] == 1
             # every part has a tile of the sum: 5 tiles in 4 parts are 3 parts of 2
             assert L.mhc_linear_plan(100, 100, 640 // (1 if dtype == 4 else 2), dtype,
@@ -328,6 +329,31 @@ def test_forward_alignment_and_edges(device, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16", "row", "mx"])
+@pytest.mark.parametrize("M,N,K", [(1100, 1300, 1600 - 7), (2050, 700, 1999), (600, 1801, 2000 + 24)])
+def test_forward_rows_that_are_no_whole_pieces(device, kind, M, N, K):
+    """Products long enough for their operands to be copied into whole rows first; fp64 on the GPU. The workspace
+    is larger than a call without copies needs, and nothing outside it is written."""
+    from hyper_connection_residual_mhc_amd import linear as L
+    say(f"forward {kind} M={M} N={N} K={K}")
+    ops, xv, wv, t = make(kind, M, N, K, seed=M, residual=False)
+    up = {k: None if v is None else v.to(device) for k, v in ops.items()}
+    out = R.Guarded((M, N), t, device)
+    ws = R.Guarded((L.mhc_linear_fwd_workspace_bytes(M, N, K, ABI[kind]),), torch.uint8, device, 0xFF)
+    L.mhc_linear_fwd(up["x"], up["weight"], out.t, bias=up["bias"], x_scales=up["x_scales"],
+                     weight_scales=up["weight_scales"], workspace=ws.t)
+    assert out.untouched() and ws.untouched()
+    x, w, b = (v.to(device) for v in (xv, wv, R.d(ops["bias"])))
+    want, size = x @ w.t() + b, x.abs() @ w.abs().t() + b.abs()
+    tol = size * (additions(K, 128 if kind in ("row", "mx") else 32) + 6) * STEP
+    if kind in ("row", "mx"):
+        tol = tol + size * 7 * 2.0 ** -13                  # at most the largest product of each 8, so at most their sum
+    tol = tol + (want.abs() + tol) * R.HALF_STEP[t] + R.HALF_TINY[t]
+    over = (out.t.double() - want).abs() - tol
+    assert float(over.max()) <= 0, int((over > 0).sum())
+
+
+@pytest.mark.gpu
 def test_rows_do_not_depend_on_the_batch(device):
     """With a named tile kernel and one part a row's bytes are the same whatever M is and where it stands."""
     from hyper_connection_residual_mhc_amd import linear as L
@@ -441,14 +467,20 @@ def test_backward_sizes(device, kind, activation):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(3800, 3704, 3528), (3801, 3704, 3592), (2100, 2050, 1000), (130, 1024, 3000)])
-def test_backward_large_tiles(device, M, N, K):
-    """Sizes at which the products take the large and the middling tiles, with ragged edges; fp64 on the GPU."""
+@pytest.mark.parametrize("M,N,K", [(3800, 3704, 3528), (3801, 3704, 3592), (2100, 2050, 1000), (130, 1024, 3000), (1500, 801, 1001), (900, 1024, 1003), (1031, 1025, 1024),
+                                   (3800, 3701, 3525)])
+@pytest.mark.parametrize("activation", ["none", "relu"])
+def test_backward_large_tiles(device, M, N, K, activation):
+    """Sizes at which the products take the large and the middling tiles, with ragged edges and with rows that are
+    copied first; fp64 on the GPU."""
     from hyper_connection_residual_mhc_amd import linear as L
-    say(f"backward M={M} N={N} K={K}")
+    say(f"backward M={M} N={N} K={K} {activation}")
     gen = torch.Generator(device=device).manual_seed(M)
     g, x, w = (torch.randn(s, device=device, generator=gen).to(BF16) for s in ((M, N), (M, K), (N, K)))
-    gx, gw, gb = L.linear_backward(g, x, w, bias=True)
+    z = torch.randn((M, N), device=device, generator=gen).to(BF16)
+    gx, gw, gb = L.linear_backward(g, x, w, bias=True, activation=activation, z=z)
+    if activation == "relu":
+        g = torch.where(z > 0, g, torch.zeros_like(g))     # exact: the slope is 0 or 1
     for got, want, size, length in ((gx, g.double() @ w.double(), g.double().abs() @ w.double().abs(), N),
                                     (gw, g.double().t() @ x.double(), g.double().abs().t() @ x.double().abs(), M)):
         tol = size * additions(length, 32) * STEP
