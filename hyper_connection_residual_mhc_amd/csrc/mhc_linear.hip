@@ -1082,7 +1082,11 @@ struct PadJobs {
 
 // Job blockIdx.y; a thread moves whole pieces of the padded rows.
 __global__ __launch_bounds__(256) void linear_pad_kernel(PadJobs jobs) {
-  const PadJob& j = jobs.job[blockIdx.y];
+  // (an index into the arguments would put them into scratch memory)
+  PadJob j = jobs.job[0];
+#pragma unroll
+  for (int i = 1; i < kMostJobs; ++i)
+    if (blockIdx.y == i) j = jobs.job[i];
   const int size = j.narrow ? 4 : 16;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
   for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < j.rows * j.pieces;
