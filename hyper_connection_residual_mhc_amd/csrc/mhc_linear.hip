@@ -272,6 +272,19 @@ __device__ __forceinline__ i32x4 buffer_of(const void* p, int64_t bytes) {
                __builtin_amdgcn_readfirstlane(size), kRsrcFormat};
 }
 
+// The first `left` < 16 bytes from p on, zeros after them (a loop over bytes in
+// registers: unrolled over every piece it would be most of a kernel).
+__device__ __forceinline__ i32x4 short_piece(const uint8_t* p, uint32_t left) {
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (uint32_t i = left; i-- > 0;) {
+    hi = (hi << 8) | (lo >> 56);
+    lo = (lo << 8) | p[i];
+  }
+  return i32x4{static_cast<int32_t>(lo), static_cast<int32_t>(lo >> 32), static_cast<int32_t>(hi),
+               static_cast<int32_t>(hi >> 32)};
+}
+
 // The part of an operand that a block loads: SPAN rows (or columns) of it. IS_W
 // and G choose the places.
 template <int SPAN, int THREADS, bool TURNED, bool IS_W, int G, bool DMA, int ELEM>
@@ -351,16 +364,7 @@ struct Operand {
           held[SET][q] = *reinterpret_cast<const i32x4_at1*>(p);
         }
       } else if (left > 0) {
-        uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (uint32_t i = 0; i < 16; i += ELEM) {
-          if (i < left) {
-            const uint32_t b = ELEM == 2 ? *reinterpret_cast<const uint16_t*>(p + i) : p[i];
-            u[i / 4] |= b << (8 * (i % 4));
-          }
-        }
-        held[SET][q] = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
-                        static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
+        held[SET][q] = short_piece(p, left);
       }
     }
   }
@@ -692,8 +696,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
     }
     wait_tiles<0>();  // nothing arrives in LDS any more
   } else {
+    // the 8-bit 128 x 128 tile has registers for one tile on its way, not two,
+    // and for one pass's block scales
+    constexpr int kSets = is8(OP) && TI * TJ >= 16 ? 1 : 2;
     const auto load = [&](uint32_t kt, auto set) {
-      constexpr int S = decltype(set)::value;
+      constexpr int S = decltype(set)::value % kSets;
       if (kt < last) {
 #pragma unroll
         for (int q = 0; q < OpX::Q; ++q) lx.template start<S>(kt, 0, q);
@@ -703,18 +710,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
     };
     const auto pass = [&](uint32_t kt, auto set) {
       constexpr int S = decltype(set)::value;
-      lx.template put<S>(lds[S]);
-      lw.template put<S>(lds[S] + BM * kTileK);
+      lx.template put<S % kSets>(lds[S]);
+      lw.template put<S % kSets>(lds[S] + BM * kTileK);
       take_scales(S);
       __syncthreads();
-      load(kt + 2, set);
-      if (kt + 1 < last) read_scales(kt + 1);
+      load(kt + kSets, set);
+      if (kSets == 2 && kt + 1 < last) read_scales(kt + 1);
       multiply(lds[S]);
+      if (kSets == 1 && kt + 1 < last) read_scales(kt + 1);
     };
     typedef std::integral_constant<int, 0> Even;
     typedef std::integral_constant<int, 1> Odd;
     load(first, Even());
-    load(first + 1, Odd());
+    if constexpr (kSets == 2) load(first + 1, Odd());
     read_scales(first);
     uint32_t kt = first;
     for (; kt + 1 < last; kt += 2) {
@@ -945,18 +953,8 @@ __device__ __forceinline__ void load_unit(const uint8_t* row, uint32_t k, uint32
     if (FULL || at + 16 <= kbytes) {
       if constexpr (is8(OP)) v = *reinterpret_cast<const i32x4_at1*>(row + at);
       else v = *reinterpret_cast<const i32x4_at2*>(row + at);
-    } else {
-      uint32_t u[4] = {0, 0, 0, 0};
-#pragma unroll
-      for (uint32_t i = 0; i < 16; i += is8(OP) ? 1 : 2) {
-        if (at + i < kbytes) {
-          const uint32_t b = is8(OP) ? row[at + i]
-                                     : *reinterpret_cast<const uint16_t*>(row + at + i);
-          u[i / 4] |= b << (8 * (i % 4));
-        }
-      }
-      v = i32x4{static_cast<int32_t>(u[0]), static_cast<int32_t>(u[1]),
-                static_cast<int32_t>(u[2]), static_cast<int32_t>(u[3])};
+    } else if (at < kbytes) {
+      v = short_piece(row + at, kbytes - at);
     }
     if constexpr (is8(OP)) f[0].w[p] = v;
     else f[p].w[0] = v;
@@ -1080,13 +1078,16 @@ struct PadJobs {
   PadJob job[kMostJobs];
 };
 
-// Job blockIdx.y; a thread moves whole pieces of the padded rows.
-__global__ __launch_bounds__(256) void linear_pad_kernel(PadJobs jobs) {
-  // (an index into the arguments would put them into scratch memory)
-  PadJob j = jobs.job[0];
-#pragma unroll
-  for (int i = 1; i < kMostJobs; ++i)
-    if (blockIdx.y == i) j = jobs.job[i];
+// Job blockIdx.y of four (an index into an argument would put it into scratch
+// memory); a thread moves whole pieces of the padded rows.
+__global__ __launch_bounds__(256) void linear_pad_kernel(PadJob a, PadJob b, PadJob c, PadJob d) {
+  const uint32_t y = blockIdx.y;
+  const PadJob j = {y == 0 ? a.in : y == 1 ? b.in : y == 2 ? c.in : d.in,
+                    y == 0 ? a.out : y == 1 ? b.out : y == 2 ? c.out : d.out,
+                    y == 0 ? a.rows : y == 1 ? b.rows : y == 2 ? c.rows : d.rows,
+                    y == 0 ? a.bytes : y == 1 ? b.bytes : y == 2 ? c.bytes : d.bytes,
+                    y == 0 ? a.pieces : y == 1 ? b.pieces : y == 2 ? c.pieces : d.pieces,
+                    y == 0 ? a.narrow : y == 1 ? b.narrow : y == 2 ? c.narrow : d.narrow};
   const int size = j.narrow ? 4 : 16;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
   for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < j.rows * j.pieces;
@@ -1469,7 +1470,7 @@ hipError_t launch_pad(const PadJobs& jobs, int count, hipStream_t s, hipEvent_t 
     if (blocks > most) most = blocks;
   }
   return launch_kernel(linear_pad_kernel, dim3(static_cast<uint32_t>(most < 4096 ? most : 4096), static_cast<uint32_t>(count)),
-                       dim3(256), s, start, nullptr, jobs);
+                       dim3(256), s, start, nullptr, jobs.job[0], jobs.job[1], jobs.job[2], jobs.job[3]);
 }
 
 template <int OP>
