@@ -578,26 +578,28 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_reduce_kernel(const float* 
   __shared__ float sums[64][17];
   __shared__ float groups[8][16];
   const int column = threadIdx.x % 16, lane = threadIdx.x / 16;
-  const int64_t h = static_cast<int64_t>(blockIdx.x) * 16 + column;
-  float s = 0.0f;
-  if (h < H) {
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * 16; first < H; first += gridDim.x * 16) {
+    const int64_t h = first + column;
+    float s = 0.0f;
+    if (h < H) {
 #pragma unroll 8
-    for (int64_t k = lane; k < parts; k += 64) s += partial[k * H + h];
-  }
-  sums[lane][column] = s;
-  __syncthreads();
-  if (lane < 8) {
-    s = sums[8 * lane][column];
+      for (int64_t k = lane; k < parts; k += 64) s += partial[k * H + h];
+    }
+    sums[lane][column] = s;
+    __syncthreads();
+    if (lane < 8) {
+      s = sums[8 * lane][column];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sums[8 * lane + k][column];
-    groups[lane][column] = s;
-  }
-  __syncthreads();
-  if (lane == 0 && h < H) {
-    s = groups[0][column];
+      for (int k = 1; k < 8; ++k) s += sums[8 * lane + k][column];
+      groups[lane][column] = s;
+    }
+    __syncthreads();
+    if (lane == 0 && h < H) {
+      s = groups[0][column];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += groups[k][column];
-    grad_weight[h] = s;
+      for (int k = 1; k < 8; ++k) s += groups[k][column];
+      grad_weight[h] = s;
+    }
   }
 }
 
@@ -782,8 +784,9 @@ struct BwdArgs {
 };
 
 hipError_t launch_reduce(const BwdArgs& a, int64_t parts, hipEvent_t start) {
-  return launch_kernel(rms_norm_bwd_reduce_kernel, dim3(static_cast<uint32_t>((a.H + 15) / 16)),
-                       dim3(1024), a.s, start, a.stop, a.partial, a.grad_weight, parts, a.H);
+  const int64_t blocks = (a.H + 15) / 16;
+  return launch_kernel(rms_norm_bwd_reduce_kernel,
+                       dim3(static_cast<uint32_t>(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(1024), a.s, start, a.stop, a.partial, a.grad_weight, parts, a.H);
 }
 
 template <int F, int THREADS, int ITER>

@@ -395,6 +395,27 @@ def test_backward_batches(device, T):
 
 
 @pytest.mark.gpu
+def test_longest_row(device):
+    from hyper_connection_residual_mhc_amd import norm
+    H = _lib.MHC_MAX_H
+    say(f"norm forward and backward H={H}")
+    gen = torch.Generator().manual_seed(3)
+    s, g = R.normal(gen, 1, H), R.normal(gen, 1, H, scale=0.5)
+    w = torch.ones(H, device=device)
+    out = norm.rms_norm(s.to(device), w, EPS, return_rstd=True)
+    sd = s.to(device).double()
+    want = sd / torch.sqrt((sd ** 2).mean() + EPS)
+    # the sum's order: 512 threads, a chain of chunks each, then trees
+    tol = want.abs() * (H / 512 + 32) * R.U32
+    assert bool(((out.y.double() - want).abs() <= tol + R.rounding(want.abs() + tol, torch.bfloat16)).all())
+    gx, gw = norm.rms_norm_backward(g.to(device), s.to(device), w, out.rstd)
+    exact = g.to(device).double()[0] * sd[0] * out.rstd.double()
+    # a product and a fused step, and zeros added
+    assert bool(((gw.double() - exact).abs() <= exact.abs() * 4 * R.U32 + 2.0 ** -140).all())
+    assert bool(torch.isfinite(gx).all())
+
+
+@pytest.mark.gpu
 def test_backward_alignment_and_edges(device):
     from hyper_connection_residual_mhc_amd import norm
     a = check_backward(device, 6, 1279, torch.float16, True, seed=9)
