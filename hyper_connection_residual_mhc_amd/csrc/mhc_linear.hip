@@ -1240,6 +1240,11 @@ mhc_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
 constexpr int32_t kMaxSplits = 64;
 constexpr int kMediumStages = 2;  // see the tile kernel
 
+// A launch holds fewer than 2^32 threads along its grid. A large tile's operands
+// may send it through four medium ones.
+int64_t most_tiles(int32_t kernel) { return 1LL << (kernel == MHC_LINEAR_LARGE ? 21 : 23); }
+constexpr int64_t kMaxRowsN = 1LL << 26;  // 16 rows of W to each block of 512 threads
+
 mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
                      const mhc_linear_launch* launch, mhc_linear_launch* plan) {
   const int32_t want = launch != nullptr ? launch->kernel : 0;
@@ -1263,11 +1268,15 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
     if (M > 16 || parts > 1)
       return fail(MHC_ERROR_INVALID_VALUE,
                   "launch: the row kernel takes at most 16 rows and one part");
+    if (N > kMaxRowsN)
+      return fail(MHC_ERROR_INVALID_VALUE, "N must be at most %lld where M is at most 16",
+                  static_cast<long long>(kMaxRowsN));
     *plan = {k, 1};
     return ok();
   }
-  if (tiles(k) > INT32_MAX / kMaxSplits)
-    return fail(MHC_ERROR_INVALID_VALUE, "M and N make too many tiles");
+  if (tiles(k) * (parts > 1 ? parts : 1) > most_tiles(k))
+    return fail(MHC_ERROR_INVALID_VALUE, "M, N and splits make more than %lld tiles",
+                static_cast<long long>(most_tiles(k)));
   const int64_t all = ceil_div(K * elem(dtype), kTileK);
   int64_t s = parts;
   if (s == 0) {

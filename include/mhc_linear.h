@@ -37,15 +37,20 @@
  * tensors at any element alignment, nothing allocated, calls only enqueue on
  * `stream`. M == 0 is a successful call (the backward then writes grad_weight
  * and grad_bias = +0.0). M < 0, N < 1, K < 1, K > MHC_LINEAR_MAX_K, M or N
- * over 2^31 - 1, an unknown dtype or act, scales missing or given where the type has none,
- * a NULL or misaligned pointer, a launch that does not exist, a workspace
- * that is too small or a size past 64 bits give MHC_ERROR_INVALID_VALUE; any
- * overlap of an output (the workspace is one) with an input or another output
- * MHC_ERROR_ALIASING; with either nothing is launched. A failed launch gives
- * MHC_ERROR_HIP. The workspace's contents mean nothing before and after a
- * call; calls that share one must not overlap in time. start_event /
- * stop_event (hipEvent_t cast to void*, each may be NULL) take the start of
- * the call's first kernel and the end of its last.
+ * over 2^31 - 1 (in the backward, which sums over them, over
+ * MHC_LINEAR_MAX_K), N over 2^26 with M <= 16, more than 2^23 tiles (of 256 x
+ * 256: 2^21) in one launch, an unknown dtype or act, scales missing or given
+ * where the type has none, a NULL or misaligned pointer, a launch that does not
+ * exist, a workspace that is too small or a size past 64 bits give
+ * MHC_ERROR_INVALID_VALUE; any overlap of an output (the workspace is one) with
+ * an input or another output MHC_ERROR_ALIASING; with either nothing is
+ * launched. A failed launch gives MHC_ERROR_HIP. The workspace is aligned to 16
+ * bytes (the sums of a split call are in it, and copies of long operands whose
+ * rows are not whole pieces of 16 bytes); its contents mean nothing before and
+ * after a call; calls that share one must not overlap in time, and neither must
+ * two captured graphs of such calls. start_event / stop_event (hipEvent_t cast
+ * to void*, each may be NULL) take the start of the call's first kernel and the
+ * end of its last.
  */
 #ifndef MHC_LINEAR_H
 #define MHC_LINEAR_H

@@ -124,6 +124,23 @@ def test_overlapping_forward_arguments(lib, kw):
     assert lib.mhc_linear_validate_fwd(*fwd_args(**kw)) == MHC_ERROR_ALIASING
 
 
+@pytest.mark.parametrize("M, N, launch, fits", [
+    (1, 1 << 26, None, True), (1, (1 << 26) + 1, None, False), (16, (1 << 26) + 1, {"kernel": ROWS}, False),
+    (1 << 29, 32, None, True), ((1 << 29) + 1, 32, None, False),            # tiles of 64 x 32
+    (1 << 28, 32, {"kernel": NARROW, "splits": 2}, True), ((1 << 28) + 1, 32, {"kernel": NARROW, "splits": 2}, False),
+    (1 << 29, 256, None, True), ((1 << 29) + 1, 256, None, False),          # tiles of 256 x 256
+    ((1 << 31) - 1, (1 << 31) - 1, None, False),
+])
+def test_launches_hold_their_tiles(lib, M, N, launch, fits):
+    from hyper_connection_residual_mhc_amd import linear as L
+    if fits:
+        assert L.mhc_linear_plan(M, N, 128, 1, launch)["kernel"]
+        return
+    with pytest.raises(_lib.MhcError):
+        L.mhc_linear_plan(M, N, 128, 1, launch)
+    assert lib.mhc_linear_validate_fwd(*fwd_args(M=M, N=N, K=128, launch=L._launch_arg(launch))) == MHC_ERROR_INVALID_VALUE
+
+
 def test_launches(lib):
     from hyper_connection_residual_mhc_amd import linear as L
     bad = [{"kernel": 6}, {"kernel": -1}, {"splits": -1}, {"splits": 65}, {"kernel": 1, "splits": 2}]
