@@ -2,9 +2,11 @@
 hyper-connection residual stream and its backward, as hand-written HIP
 kernels behind a C ABI (include/mhc_h_aggregate.h).
 
-The torch-facing names live in `hyper_connection_residual_mhc_amd.ops` (and
-`.coeff` for the coefficient backward epilogue); they are re-exported here
-on first access. Calling them loads the shared libraries (ImportError if
+The torch-facing names live in `hyper_connection_residual_mhc_amd.ops`,
+`.coeff` for the coefficient backward epilogue, and `.norm`, `.linear` and
+`.post` for the rest of a hyper-connected sublayer (RMS norm, matrix
+product, write-back into the streams); they are re-exported here on first
+access. Calling them loads the shared libraries (ImportError if
 they have not been built).
 """
 
@@ -24,7 +26,22 @@ _COEFF_NAMES = (
     "mhc_coeff_bwd", "mhc_coeff_bwd_workspace_bytes", "mhc_coeff_bwd_plan",
     "mhc_coeff_bwd_validate", "coeff_columns",
 )
+# `.linear` the module keeps its name here: the call is `linear.linear`.
+_NORM_NAMES = (
+    "mhc_rms_norm_fwd", "mhc_rms_norm_bwd", "mhc_rms_norm_bwd_workspace_bytes",
+    "rms_norm", "rms_norm_backward", "RMSNorm", "rms_norm_autograd",
+)
+_LINEAR_NAMES = (
+    "mhc_linear_fwd", "mhc_linear_bwd", "mhc_linear_plan", "mhc_linear_fwd_workspace_bytes",
+    "mhc_linear_bwd_workspace_bytes", "linear_backward", "Linear", "linear_autograd",
+)
+_POST_NAMES = (
+    "mhc_post_fwd", "mhc_post_bwd", "post_update", "post_update_backward", "PostUpdate",
+    "post_update_autograd",
+)
 
+# What `import *` brings: the path itself. The sublayer's names are reached as
+# attributes.
 __all__ = list(_OPS_NAMES) + list(_COEFF_NAMES)
 
 
@@ -35,4 +52,13 @@ def __getattr__(name: str):
     if name in _COEFF_NAMES:
         from . import coeff
         return getattr(coeff, name)
+    if name in _NORM_NAMES:
+        from . import norm
+        return getattr(norm, name)
+    if name in _LINEAR_NAMES:
+        from . import linear
+        return getattr(linear, name)
+    if name in _POST_NAMES:
+        from . import post
+        return getattr(post, name)
     raise AttributeError(name)

@@ -53,6 +53,14 @@ def plain(p, act="gelu"):
     return R.post(p["streams"], p["comb"], p["gate"], h @ p["w2"].t())
 
 
+def test_package_names():
+    import hyper_connection_residual_mhc_amd as pkg
+    from hyper_connection_residual_mhc_amd import linear, norm, post
+    for module, names in ((norm, pkg._NORM_NAMES), (linear, pkg._LINEAR_NAMES), (post, pkg._POST_NAMES)):
+        for name in names:
+            assert getattr(pkg, name) is getattr(module, name)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,n,H,F", [(1, 4, 256, 512), (37, 2, 264, 520), (200, 4, 1288, 640), (130, 8, 129, 77)])
 def test_training_step(device, T, n, H, F):
