@@ -272,14 +272,36 @@ __device__ __forceinline__ i32x4 buffer_of(const void* p, int64_t bytes) {
                __builtin_amdgcn_readfirstlane(size), kRsrcFormat};
 }
 
-// The first `left` < 16 bytes from p on, zeros after them (a loop over bytes in
-// registers: unrolled over every piece it would be most of a kernel).
-__device__ __forceinline__ i32x4 short_piece(const uint8_t* p, uint32_t left) {
+typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
+typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
+
+// 16 bytes from p on, at an element's alignment.
+template <int ELEM>
+__device__ __forceinline__ i32x4 piece_at(const uint8_t* p) {
+  if constexpr (ELEM == 2) return *reinterpret_cast<const i32x4_at2*>(p);
+  else return *reinterpret_cast<const i32x4_at1*>(p);
+}
+
+// The first 0 < `left` < 16 bytes from p on, zeros after them: the 16 bytes that
+// end there, shifted. Where they would begin before the row (`before`: whether 16
+// bytes of it are in front of p) byte by byte, which only rows shorter than a
+// piece come to: 14 loads one after another are 9 us.
+template <int ELEM>
+__device__ __forceinline__ i32x4 short_piece(const uint8_t* p, uint32_t left, bool before) {
   uint64_t lo = 0, hi = 0;
+  if (before) {
+    const i32x4 v = piece_at<ELEM>(p + left - 16);
+    const uint64_t a = static_cast<uint32_t>(v[0]) | static_cast<uint64_t>(static_cast<uint32_t>(v[1])) << 32;
+    const uint64_t b = static_cast<uint32_t>(v[2]) | static_cast<uint64_t>(static_cast<uint32_t>(v[3])) << 32;
+    const uint32_t bits = (16 - left) * 8;
+    lo = bits >= 64 ? b >> (bits - 64) : (a >> bits) | (b << (64 - bits));
+    hi = bits >= 64 ? 0 : b >> bits;
+  } else {
 #pragma unroll 1
-  for (uint32_t i = left; i-- > 0;) {
-    hi = (hi << 8) | (lo >> 56);
-    lo = (lo << 8) | p[i];
+    for (uint32_t i = left; i-- > 0;) {
+      hi = (hi << 8) | (lo >> 56);
+      lo = (lo << 8) | p[i];
+    }
   }
   return i32x4{static_cast<int32_t>(lo), static_cast<int32_t>(lo >> 32), static_cast<int32_t>(hi),
                static_cast<int32_t>(hi >> 32)};
@@ -301,6 +323,7 @@ struct Operand {
   uint32_t ld;
   uint32_t here;    // rows (columns) that exist
   uint32_t kbytes;  // bytes of k that exist
+  bool inside;      // TURNED: whether columns are in front of the block's first one
   i32x4 held[2][DMA ? 1 : Q];  // through registers: two tiles on their way
 
   static __device__ __forceinline__ uint32_t swap(uint32_t row) {
@@ -321,6 +344,7 @@ struct Operand {
     kbytes = TURNED ? a.kturned : a.kbytes;
     here = static_cast<uint32_t>(left < SPAN ? left : SPAN);
     ld = static_cast<uint32_t>(m.ld);
+    inside = first > 0;
     base = static_cast<const uint8_t*>(m.p) + (TURNED ? first * ELEM : first * m.ld);
     rsrc = buffer_of(base, TURNED ? kbytes / ELEM * m.ld - first * ELEM : here * m.ld);
     row = threadIdx.x / P;
@@ -353,19 +377,12 @@ struct Operand {
       } else {
         const uint32_t k = kt * kTileK + piece;
         left = rows + row < here && k < kbytes ? kbytes - k : 0;
-        p += static_cast<int64_t>(rows + row) * ld + k;
+        p += (rows + row) * ld + k;  // at most 256 rows of 4 MiB
       }
-      if (left >= 16) {
-        if constexpr (ELEM == 2) {
-          typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
-          held[SET][q] = *reinterpret_cast<const i32x4_at2*>(p);
-        } else {
-          typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
-          held[SET][q] = *reinterpret_cast<const i32x4_at1*>(p);
-        }
-      } else if (left > 0) {
-        held[SET][q] = short_piece(p, left);
-      }
+      if (left >= 16)
+        held[SET][q] = piece_at<ELEM>(p);
+      else if (left > 0)
+        held[SET][q] = short_piece<ELEM>(p, left, TURNED ? piece > 0 || inside : p - base >= 16);
     }
   }
 
@@ -943,18 +960,16 @@ struct RowsArgs {
 template <int OP, bool FULL>
 __device__ __forceinline__ void load_unit(const uint8_t* row, uint32_t k, uint32_t kbytes,
                                           uint32_t g, Frag<OP> (&f)[is8(OP) ? 1 : 2]) {
-  typedef i32x4 i32x4_at1 __attribute__((aligned(1)));
-  typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
+  constexpr int ELEM = is8(OP) ? 1 : 2;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     // piece p of the unit: the lane group's 16 bytes
     const uint32_t at = k + p * 64 + g * 16;
     i32x4 v = {0, 0, 0, 0};
     if (FULL || at + 16 <= kbytes) {
-      if constexpr (is8(OP)) v = *reinterpret_cast<const i32x4_at1*>(row + at);
-      else v = *reinterpret_cast<const i32x4_at2*>(row + at);
+      v = piece_at<ELEM>(row + at);
     } else if (at < kbytes) {
-      v = short_piece(row + at, kbytes - at);
+      v = short_piece<ELEM>(row + at, kbytes - at, at > 0);
     }
     if constexpr (is8(OP)) f[0].w[p] = v;
     else f[p].w[0] = v;
