@@ -906,24 +906,37 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
   write_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
 
-// The parts of a split sum, added in ascending order, and the epilogue.
+// The parts of a split sum, added in ascending order, and the epilogue. One wave
+// to a block and eight parts' loads in flight: 2048 x 24 in 16 parts 6.3 us,
+// four waves and a part at a time 9.9.
+constexpr int kJoinThreads = 64;
+
 template <int OP>
-__global__ __launch_bounds__(256) void linear_join_kernel(const float* __restrict__ partial,
-                                                          uint32_t splits, int64_t M, Epilogue e) {
+__global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(const float* __restrict__ partial,
+                                                                   uint32_t splits, int64_t M, Epilogue e) {
   const int64_t chunks = (e.N + 7) / 8;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < M * chunks;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kJoinThreads;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; id < M * chunks;
        id += step) {
     const int64_t m = id / chunks, n = (id - m * chunks) * 8;
     const int count = static_cast<int>(min(e.N - n, static_cast<int64_t>(8)));
     const float* p = partial + m * e.N + n;
     float v[8], b[8];
     widen_chunk<kF32>(load_chunk<kF32>(p, count), v);
-    for (uint32_t s = 1; s < splits; ++s) {
-      p += M * e.N;
-      widen_chunk<kF32>(load_chunk<kF32>(p, count), b);
+    if (count == 8) {
+#pragma unroll 8
+      for (uint32_t s = 1; s < splits; ++s) {
+        widen_chunk<kF32>(load_chunk<kF32>(p + s * M * e.N, 8), b);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
+        for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
+      }
+    } else {
+#pragma unroll 4
+      for (uint32_t s = 1; s < splits; ++s) {
+        widen_chunk<kF32>(load_chunk<kF32>(p + s * M * e.N, count), b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
+      }
     }
     with_act(e.act, [&](auto act) { finish<OP, decltype(act)::value>(e, m, n, count, v); });
   }
@@ -1467,9 +1480,9 @@ hipError_t launch_product(TileArgs a, const mhc_linear_launch& plan, hipStream_t
     default: e = launch_large<OP, TX, TW>(a, s, start, end); break;
   }
   if (e != hipSuccess || !join) return e;
-  const int64_t blocks = ceil_div(a.M * ceil_div(a.N, 8), 256);
-  return launch_kernel(linear_join_kernel<OP>, dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096)),
-                       dim3(256), s, nullptr, stop, a.partial, a.splits, a.M, a.e);
+  const int64_t blocks = ceil_div(a.M * ceil_div(a.N, 8), kJoinThreads);
+  return launch_kernel(linear_join_kernel<OP>, dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
+                       dim3(kJoinThreads), s, nullptr, stop, a.partial, a.splits, a.M, a.e);
 }
 
 template <int OP>
