@@ -253,7 +253,7 @@ hipError_t launch_bwd(int64_t H, A... a) {
   if (H <= 64 * 8) return launch_bwd_t<N, 64>(a...);
   if (H <= 128 * 8) return launch_bwd_t<N, 128>(a...);
   if (H <= 256 * 8 || N == 8) return launch_bwd_t<N, 256>(a...);
-  return launch_bwd_t<N, 512>(a...);  // T = 4096, H = 7168, n = 4: 152.5 us, with 256 158.8
+  return launch_bwd_t<N, 512>(a...);  // T = 4096, H = 7168, n = 4: 4% less time than 256
 }
 
 }  // namespace
