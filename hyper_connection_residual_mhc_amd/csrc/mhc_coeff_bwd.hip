@@ -573,8 +573,8 @@ hipError_t launch_partial(const CoeffArgs& a, hipStream_t s, hipEvent_t start) {
 
 // Waves per block of the one-launch form: 2 up to this many chunks, 4
 // above. Measured per call (cold inputs, n = 4): 2-wave blocks 4.5 / 4.9 /
-// 5.1 / 5.5 / 5.6 us at 512 / 1024 / 2048 / 3072 / 4096 rows against 5.0 /
-// 5.2 / 5.6 / 5.7 / 5.7 us with 4 (more CUs share the first stage); 4-wave
+// 5.1 / 5.6 us at 512 / 1024 / 2048 / 4096 rows against 5.0 /
+// 5.2 / 5.6 / 5.7 us with 4 (more CUs share the first stage); 4-wave
 // blocks 7.1 / 8.8 us at 8192 / 16384 rows against 7.3 / 10.0 us (the last
 // block's waves each sum fewer outputs). At n = 2 the same or better.
 constexpr uint32_t kTwoWaveMaxChunks = 64;
