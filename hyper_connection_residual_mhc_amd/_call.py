@@ -15,7 +15,7 @@ import torch
 
 from .ops import _require
 
-_SAME_DEVICE = contextlib.nullcontext()
+_NOTHING = contextlib.nullcontext()
 
 
 def require(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device
@@ -36,7 +36,7 @@ def stream_handle(device: torch.device, stream: torch.cuda.Stream | None) -> int
 
 def on(device: torch.device):
     """Context in which `device` is the current one."""
-    return _SAME_DEVICE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def address(t: torch.Tensor | None) -> int | None:
@@ -47,13 +47,13 @@ def address(t: torch.Tensor | None) -> int | None:
 def workspace_of(workspace: torch.Tensor | None, need: int, device: torch.device,
                  stream: torch.cuda.Stream | None) -> tuple[int | None, int, torch.Tensor | None]:
     """(address, bytes, owner) of the caller's workspace, or of a fresh one of
-    `need` bytes that stays alive as long as `stream` uses it."""
+    `need` bytes. A fresh one belongs to `stream`: memory of torch's current
+    stream may still be in use there when `stream` starts to write."""
     if workspace is None:
         if need <= 0:
             return None, 0, None
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        with _NOTHING if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty((need,), dtype=torch.uint8, device=device)
     elif not isinstance(workspace, torch.Tensor) or workspace.device != device or \
             not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")

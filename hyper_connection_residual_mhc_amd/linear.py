@@ -14,6 +14,7 @@ import functools
 from typing import Mapping, NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._call import address, on, require, stream_handle, workspace_of
@@ -240,6 +241,7 @@ class Linear(torch.autograd.Function):
         return o.out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         x, weight, z = ctx.saved_tensors
         need_x, need_w, need_b, _, need_r = ctx.needs_input_grad

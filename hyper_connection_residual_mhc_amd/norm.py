@@ -12,6 +12,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._call import address, on, require, stream_handle, workspace_of
@@ -216,6 +217,7 @@ class RMSNorm(torch.autograd.Function):
         return o.y, o.stored
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y, grad_stored):
         stored, weight, rstd, *streams = ctx.saved_tensors
         if grad_y is None:

@@ -8,6 +8,7 @@ gfx950 kernels; a missing library raises ImportError.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._call import on, require, stream_handle
@@ -101,6 +102,7 @@ class PostUpdate(torch.autograd.Function):
         return post_update(residual, comb, post, y)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out):
         grads = post_update_backward(grad_out.contiguous(), *ctx.saved_tensors)
         return tuple(g if need else None for g, need in zip(grads, ctx.needs_input_grad))

@@ -132,3 +132,43 @@ def test_decoding_step_in_a_graph(device):
         graph.replay()
         torch.cuda.synchronize()
         assert R.same_bytes(got, step(new)), k
+
+
+@pytest.mark.gpu
+def test_workspaces_belong_to_the_stream_that_uses_them(device, monkeypatch):
+    from hyper_connection_residual_mhc_amd import linear, norm
+    side = torch.cuda.Stream()
+    x, w = torch.randn(300, 4096, device=device).to(BF16), torch.randn(64, 4096, device=device).to(BF16)
+    out, gw = torch.empty(300, 64, device=device, dtype=BF16), torch.empty_like(w)
+    g, ones, dw = torch.randn_like(x), torch.ones(300, device=device), torch.empty(4096, device=device)
+    gx = torch.empty_like(x)
+    torch.cuda.synchronize()
+    seen, empty = [], torch.empty
+
+    def recording(*a, **kw):
+        seen.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", recording)
+    linear.mhc_linear_fwd(x, w, out, launch={"kernel": 3, "splits": 4}, stream=side)
+    linear.mhc_linear_bwd(out, x, w, grad_weight=gw, stream=side)
+    norm.mhc_rms_norm_bwd(g, x, w[0], ones, gx, dw, stream=side)
+    assert seen == [side] * 3
+    seen.clear()
+    linear.mhc_linear_fwd(x, w, out, launch={"kernel": 3, "splits": 4})
+    assert seen == [torch.cuda.current_stream()]
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_second_derivatives_are_refused(device):
+    from hyper_connection_residual_mhc_amd import linear, norm, post
+    p = make(5, 4, 64, 32, 0, device)
+    x = torch.randn(5, 64, device=device).to(BF16)
+    for call, leaf in ((lambda t: norm.rms_norm_autograd(t, p["norm"])[0], x),
+                       (lambda t: linear.linear_autograd(t, p["w1"], p["b1"], activation="silu"), x),
+                       (lambda t: post.post_update_autograd(p["streams"], p["comb"], p["gate"], t), x)):
+        t = leaf.clone().requires_grad_()
+        first, = torch.autograd.grad(call(t).float().square().sum(), t, create_graph=True)
+        with pytest.raises(RuntimeError):
+            first.float().square().sum().backward()
