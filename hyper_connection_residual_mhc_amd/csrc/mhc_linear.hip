@@ -160,8 +160,8 @@ struct Frag {
 };
 
 // acc[i] of lane l: row 4 (l / 16) + i of `a` against row l % 16 of `b`. sa, sb:
-// the lane's e8m0 bytes (kMX).
-template <int OP>
+// the lane's e8m0 bytes (kMX), in byte BYTE_A and BYTE_B.
+template <int OP, int BYTE_A = 0, int BYTE_B = 0>
 __device__ __forceinline__ f32x4 mma(const Frag<OP>& a, const Frag<OP>& b, f32x4 acc, int sa,
                                      int sb) {
   const i32x4 a0 = a.w[0], b0 = b.w[0];
@@ -175,9 +175,29 @@ __device__ __forceinline__ f32x4 mma(const Frag<OP>& a, const Frag<OP>& b, f32x4
     const i32x8 x = __builtin_shufflevector(a0, a.w[1], 0, 1, 2, 3, 4, 5, 6, 7);
     const i32x8 y = __builtin_shufflevector(b0, b.w[1], 0, 1, 2, 3, 4, 5, 6, 7);
     // 0x7F is the scale 1
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0,
-                                                            OP == kOpMX ? sa : 0x7F, 0,
-                                                            OP == kOpMX ? sb : 0x7F);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        x, y, acc, 0, 0, BYTE_A, OP == kOpMX ? sa : 0x7F, BYTE_B, OP == kOpMX ? sb : 0x7F);
+  }
+}
+
+// The same with the scale bytes named by values that unrolling makes constants.
+template <int OP>
+__device__ __forceinline__ f32x4 mma_bytes(const Frag<OP>& a, const Frag<OP>& b, f32x4 acc, int sa,
+                                           int sb, int byte_a, int byte_b) {
+  const auto at = [&](auto i) {
+    constexpr int A = decltype(i)::value;
+    switch (byte_b) {
+      case 0: return mma<OP, A, 0>(a, b, acc, sa, sb);
+      case 1: return mma<OP, A, 1>(a, b, acc, sa, sb);
+      case 2: return mma<OP, A, 2>(a, b, acc, sa, sb);
+      default: return mma<OP, A, 3>(a, b, acc, sa, sb);
+    }
+  };
+  switch (byte_a) {
+    case 0: return at(std::integral_constant<int, 0>());
+    case 1: return at(std::integral_constant<int, 1>());
+    case 2: return at(std::integral_constant<int, 2>());
+    default: return at(std::integral_constant<int, 3>());
   }
 }
 
@@ -768,10 +788,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs a
 // 1230 (nobody fills a wave's gaps); all loads at the start of the half 1140;
 // reads not ahead of the pass 1280; without the raised priority of the
 // matrix instructions 1346. Matrix units are busy 57-63% of the cycles, at a clock that the
-// load itself brings down to 1.7 GHz (bf16) and 1.95 GHz (e4m3). e4m3: 2550
-// TFLOP/s with row scales, 2060 with block scales (their bytes come 16 of a row
-// at a time, for four passes: a pass's 4 alone cost as many requests as its
-// values, 1880).
+// load itself brings down to 1.7 GHz (bf16) and 1.95 GHz (e4m3). e4m3 at 8192^3 and 8192 x
+// 4096 x 7168: 2670 TFLOP/s with row scales (the library's 2436 and 2675), with block
+// scales 2270 and 2460; with a scale byte read for each row and pass instead of
+// one word for four tiles 2060.
+
 // ---------------------------------------------------------------------------
 
 template <int OP, bool TX, bool TW>
@@ -781,10 +802,11 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
   constexpr int kPieces = is8(OP) ? 1 : 2;  // matrix instructions for one result in a pass
   constexpr int ELEM = is8(OP) ? 1 : 2;
   constexpr uint32_t kBuffer = (BM + BN) * kTileK;
-  // kMX: the e8m0 bytes of four passes, 16 for each row of x and of W
-  constexpr uint32_t kScaleBytes = OP == kOpMX ? (BM + BN) * 16 : 0;
+  constexpr bool kScales = OP == kOpMX;
+  constexpr uint32_t kTurned = 8 * 64 + 16;  // words of a pass in `turned`; 16 more, so that four passes are in four banks
   __shared__ __align__(1024) uint8_t lds[2][kBuffer];
-  __shared__ __align__(1024) uint8_t scales[2][OP == kOpMX ? kScaleBytes : 16];
+  __shared__ __align__(1024) uint8_t scales[kScales ? (BM + BN) * 16 : 16];
+  __shared__ uint32_t turned[2][kScales ? 4 * kTurned : 1];
   const Place place = place_of<BM, BN>(a);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t lane = threadIdx.x % 64, g = lane / 16;
@@ -802,46 +824,74 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
   rx.init(wm * (TI * 16));
   rw.init(wn * (TJ * 16));
 
-  // kMX: each of the first four waves brings the bytes of 64 x rows, the others of 64 W rows.
+  // kMX: block scales come four passes at a time, 16 bytes of each row into
+  // `scales`: the first four waves bring 64 rows of x each, the others of W. A
+  // wave then turns its 64 rows: word [pass][wave][lane] of `turned` holds, for the
+  // lane group's 32 values of the pass, the bytes of the lane's row in each of
+  // four tiles, and the matrix instruction picks the byte of its tile.
   const uint32_t kblocks = a.kbytes / 32;
   uint32_t so = 0;
   i32x4 sr = {0, 0, 0, 0};
-  if constexpr (OP == kOpMX) {
+  if constexpr (kScales) {
     const bool of_x = wave < 4;
     const uint32_t r = threadIdx.x % 256, here = of_x ? lx.here : lw.here;
     sr = buffer_of(of_x ? a.xs + place.m0 * kblocks : a.ws + place.n0 * kblocks,
                    static_cast<int64_t>(here) * kblocks);
     so = r < here ? r * kblocks : kOutside;
   }
-  const uint32_t at0 = lds_address(&lds[0][0]), at1 = lds_address(&scales[0][0]);
+  const uint32_t at0 = lds_address(&lds[0][0]), at1 = lds_address(&scales[0]);
   const auto start = [&](uint32_t kt, uint32_t b, int q) {
     lx.start(kt, at0 + b * kBuffer, q);
     lw.start(kt, at0 + b * kBuffer + BM * kTileK, q);
   };
-  // kMX: the scales of four tiles from kt on, 16 bytes of each row.
-  const auto start_scales = [&](uint32_t kt, uint32_t b) {
-    if constexpr (OP == kOpMX)
-      load_to_lds<16>(kt * 4 < kblocks ? so : kOutside, sr, kt * 4, at1 + b * kScaleBytes + wave * 1024);
+  const auto start_scales = [&](uint32_t kt) {
+    if constexpr (kScales) load_to_lds<16>(kt * 4 < kblocks ? so : kOutside, sr, kt * 4, at1 + wave * 1024);
+  };
+  // Lane (g, low) takes the words of pass g of its four rows.
+  const auto turn_scales = [&](uint32_t b) {
+    if constexpr (kScales) {
+      const uint32_t low = lane % 16;
+      uint32_t d[4], e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t row = wave < 4 ? i * 16 + low : (low / 4) * 16 + i * 4 + low % 4;
+        d[i] = *reinterpret_cast<const uint32_t*>(&scales[(wave * 64 + row) * 16 + g * 4]);
+      }
+      const uint32_t lo01 = __builtin_amdgcn_perm(d[1], d[0], 0x05010400), lo23 = __builtin_amdgcn_perm(d[3], d[2], 0x05010400);
+      const uint32_t hi01 = __builtin_amdgcn_perm(d[1], d[0], 0x07030602), hi23 = __builtin_amdgcn_perm(d[3], d[2], 0x07030602);
+      e[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100);
+      e[1] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302);
+      e[2] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100);
+      e[3] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) turned[b][g * kTurned + wave * 64 + i * 16 + low] = e[i];
+    }
+  };
+  // The scale bytes of a pass: of the W tiles and of each half of the x tiles.
+  struct Scales {
+    int w, x[2];
+  };
+  Scales now = {}, next = {};
+  const auto read_scales = [&](uint32_t step, Scales& s) {
+    if constexpr (kScales) {
+      const uint32_t* p = &turned[step / 4 % 2][step % 4 * kTurned + lane];
+      s.w = p[(4 + wn) * 64];
+      s.x[0] = p[wm * 128];
+      s.x[1] = p[wm * 128 + 64];
+    }
   };
 
-  // Both 16-byte pieces of a pass, and the scale byte.
   struct Row {
-    i32x4 w[2];
-    int s;
+    i32x4 w[2];  // both 16-byte pieces of a pass
   };
   Row w[TJ], xa[HALF], xb[HALF];
-  const auto scale_at = [&](uint32_t step, uint32_t row) {
-    return OP == kOpMX ? scales[step / 4 % 2][row * 16 + step % 4 * 4 + g] : 0;
-  };
-  const auto read_w = [&](uint32_t b, uint32_t step, int j) {
+  const auto read_w = [&](uint32_t b, int j) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) w[j].w[h] = rw.read(lds[b] + BM * kTileK, j, h);
-    w[j].s = scale_at(step, BM + rw.row_of(wn * (TJ * 16), j));
   };
-  const auto read_x = [&](uint32_t b, uint32_t step, int i, Row& r) {
+  const auto read_x = [&](uint32_t b, int i, Row& r) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) r.w[h] = rx.read(lds[b], i, h);
-    r.s = scale_at(step, rx.row_of(wm * (TI * 16), i));
   };
 
   f32x4 acc[TI][TJ];
@@ -857,7 +907,7 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
         f32x4& c = acc[half * HALF + i][j];
         if constexpr (is8(OP)) {
           const Frag<OP> p = {w[j].w[0], w[j].w[1]}, q = {x[i].w[0], x[i].w[1]};
-          c = mma<OP>(p, q, c, w[j].s, x[i].s);
+          c = kScales ? mma_bytes<OP>(p, q, c, now.w, now.x[half], j, i) : mma<OP>(p, q, c, 0, 0);
         } else {
           const Frag<OP> p = {w[j].w[h]}, q = {x[i].w[h]};
           c = mma<OP>(p, q, c, 0, 0);
@@ -870,26 +920,31 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
   const uint32_t last = min(all, first + a.per_split);
 #pragma unroll
   for (int q = 0; q < TJ; ++q) start(first, 0, q);
-  start_scales(first, 0);
+  start_scales(first);
   wait_tiles<0>();
+  turn_scales(0);
 #pragma unroll
   for (int q = 0; q < TJ; ++q) start(first + 1, 1, q);
 #pragma unroll
-  for (int j = 0; j < TJ; ++j) read_w(0, 0, j);
+  for (int j = 0; j < TJ; ++j) read_w(0, j);
 #pragma unroll
-  for (int i = 0; i < HALF; ++i) read_x(0, 0, i, xa[i]);
+  for (int i = 0; i < HALF; ++i) read_x(0, i, xa[i]);
+  if constexpr (kScales) __syncthreads();  // every wave has turned its rows
+  read_scales(0, now);
   for (uint32_t kt = first; kt < last; ++kt) {
     const uint32_t step = kt - first, b = step & 1;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      if (j < HALF) read_x(b, step, HALF + j, xb[j]);
+      if (j < HALF) read_x(b, HALF + j, xb[j]);
       __builtin_amdgcn_s_setprio(1);
       multiply(0, j, xa);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
     wait_tiles<0>();
-    if (step % 4 == 2) start_scales(kt + 2, (step + 2) / 4 % 2);
+    if (kScales && step % 4 == 1) start_scales(kt + 3);
+    if (kScales && step % 4 == 2) turn_scales((step + 2) / 4 % 2);
+    read_scales(step + 1, next);
     // past the last tile: zeros are loaded and old values read, and neither is used
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
@@ -897,10 +952,11 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs a) {
       __builtin_amdgcn_s_setprio(1);
       multiply(1, j, xb);
       __builtin_amdgcn_s_setprio(0);
-      read_w(b ^ 1, step + 1, j);
-      if (j < HALF) read_x(b ^ 1, step + 1, j, xa[j]);
+      read_w(b ^ 1, j);
+      if (j < HALF) read_x(b ^ 1, j, xa[j]);
       __builtin_amdgcn_sched_barrier(0);
     }
+    now = next;
   }
   wait_tiles<0>();  // nothing arrives in LDS any more
   write_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);

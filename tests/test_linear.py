@@ -278,6 +278,27 @@ def test_forward_depths(device, kernel, kind):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kernel", [ROWS, NARROW, SMALL, MEDIUM, LARGE])
+def test_forward_block_scales(device, kernel):
+    """Scales that differ from block to block by up to 2^16, over one to nine passes of the tiles and in parts."""
+    from hyper_connection_residual_mhc_amd import linear as L
+    M, N = (7, 40) if kernel == ROWS else (300, 290)
+    for passes in range(1, 10):
+        for splits in (1,) if kernel == ROWS or passes < 4 else (1, 2):
+            K = 128 * passes
+            say(f"block scales kernel={kernel} K={K} splits={splits}")
+            gen = torch.Generator().manual_seed(passes)
+            x, w = (torch.randn(r, K, generator=gen).to(torch.float8_e4m3fn) for r in (M, N))
+            xs, ws = (torch.randint(119, 136, (r, K // 32), generator=gen, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+                      for r in (M, N))
+            out, z = torch.empty(M, N, dtype=BF16, device=device), torch.empty(M, N, dtype=BF16, device=device)
+            L.mhc_linear_fwd(x.to(device), w.to(device), out, x_scales=xs.to(device), weight_scales=ws.to(device), z=z,
+                             launch={"kernel": kernel, "splits": splits})
+            torch.cuda.synchronize()
+            check_forward(out, z, dict(bias=None, residual=None), R.dequantise(x, xs), R.dequantise(w, ws), BF16, "none", "mx")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "mx"])
 @pytest.mark.parametrize("kernel", [NARROW, SMALL, MEDIUM, LARGE])
 def test_forward_tiles(device, kernel, kind):
