@@ -36,7 +36,7 @@ def stream_handle(device: torch.device, stream: torch.cuda.Stream | None) -> int
 
 def on(device: torch.device):
     """Context in which `device` is the current one."""
-    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _NOTHING if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def address(t: torch.Tensor | None) -> int | None:

@@ -223,7 +223,7 @@ def linear_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     grad_bias; the last None unless bias). The residual's gradient is
     grad_out itself."""
     grad_x, grad_weight = torch.empty_like(x), torch.empty_like(weight)
-    grad_bias = torch.empty((weight.shape[0],), dtype=x.dtype, device=x.device) if bias else None
+    grad_bias = x.new_empty((weight.shape[0],)) if bias else None
     mhc_linear_bwd(grad_out, x, weight, grad_x=grad_x, grad_weight=grad_weight,
                    grad_bias=grad_bias, activation=activation, z=z)
     return grad_x, grad_weight, grad_bias

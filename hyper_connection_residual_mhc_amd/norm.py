@@ -168,20 +168,19 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     """The norm with freshly allocated outputs (no autograd); `stored` is
     returned with a residual or pre."""
     T, n, H = _check_inputs(x, weight, residual, pre, quant)
-    dev = x.device
     scales = stored = rstd = None
     if quant is None:
-        y = x.new_empty((T, H))
+        y = x.new_empty((T, H)) if n else torch.empty_like(x)
     else:
         y = x.new_empty((T, H), dtype=torch.float8_e4m3fn)
         if quant == "row":
-            scales = torch.empty((T,), dtype=torch.float32, device=dev)
+            scales = x.new_empty((T,), dtype=torch.float32)
         else:
-            scales = torch.empty((T, -(-H // 32)), dtype=torch.float8_e8m0fnu, device=dev)
+            scales = x.new_empty((T, -(-H // 32)), dtype=torch.float8_e8m0fnu)
     if n or residual is not None:
-        stored = x.new_empty((T, H))
+        stored = x.new_empty((T, H)) if n else torch.empty_like(x)
     if return_rstd:
-        rstd = torch.empty((T,), dtype=torch.float32, device=dev)
+        rstd = x.new_empty((T,), dtype=torch.float32)
     _launch_fwd(x, weight, y, eps, residual, pre, scales, stored, rstd, quant, T, n, H, None, None,
                 None)
     return RMSNormOut(y, scales, stored, rstd)
@@ -194,7 +193,7 @@ def rms_norm_backward(grad_y: torch.Tensor, stored: torch.Tensor, weight: torch.
     grad_weight in fp32)."""
     T, H = _check_bwd_inputs(grad_y, stored, weight, rstd, grad_stored)
     grad_x = torch.empty_like(stored)
-    grad_weight = torch.empty((H,), dtype=torch.float32, device=stored.device)
+    grad_weight = stored.new_empty((H,), dtype=torch.float32)
     _launch_bwd(grad_y, stored, weight, rstd, grad_stored, grad_x, grad_weight, None, T, H, None,
                 None, None)
     return grad_x, grad_weight
