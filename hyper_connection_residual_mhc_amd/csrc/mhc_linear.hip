@@ -1381,13 +1381,13 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 
 // Products of at least this many terms have operands without whole rows copied
-// first. Forward, with at least kPadRows rows of each: 2048 x 2048 x 2047 in bf16 54 us
-// through registers, 38 with copies; 256 x 4096 x 4095 35 and 38. The backward's turned
-// operands lose more: 1024 x 1024 x 1023 25 us a product through registers, 19 with copies,
-// 4096 x 4096 x 2047 316 and 78.
-constexpr int64_t kPadForward = 1LL << 31;
+// first. Forward in bf16, with at least kPadRows rows of each, through registers and with
+// copies: 512 x 4096 x 2047 31 and 36 us, 2048 x 2048 x 2047 41 and 37, 4096 x 4096 x 2047
+// 110 and 73. A product of the backward, where turned operands lose more: 1024 x 1024 x 1023 17
+// and 18.5 us, 512 x 2048 x 2047 24 and 21, 2048 x 2048 x 2047 81 and 37.
+constexpr int64_t kPadForward = 3LL << 31;
 constexpr int64_t kPadRows = 512;
-constexpr int64_t kPadBackward = 1LL << 29;
+constexpr int64_t kPadBackward = 3LL << 29;
 
 // Places in the workspace, in bytes, each from a multiple of 256 on; `total` is
 // -1 where a size does not fit.

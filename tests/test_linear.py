@@ -368,7 +368,8 @@ def test_forward_alignment_and_edges(device, kind):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "f16", "row", "mx"])
-@pytest.mark.parametrize("M,N,K", [(1100, 1300, 1600 - 7), (2050, 700, 1999), (600, 1801, 2000 + 24)])
+@pytest.mark.parametrize("M,N,K", [(1100, 1300, 1600 - 7), (2050, 700, 1999), (600, 1801, 2000 + 24),
+                                   (2050, 1700, 1999), (1100, 3001, 2024)])
 def test_forward_rows_that_are_no_whole_pieces(device, kind, M, N, K):
     """Products long enough for their operands to be copied into whole rows first; fp64 on the GPU. The workspace
     is larger than a call without copies needs, and nothing outside it is written."""
