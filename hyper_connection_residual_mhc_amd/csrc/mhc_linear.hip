@@ -1366,10 +1366,12 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
   if (s == 0) {
     // at least 4 tiles of the sum in each part, and at most two blocks for each
     // CU, of the wide tiles one: 2048^3 in bf16 in one part of 256 blocks 25.8 us, in two
-    // parts 34; 17 x 7168 x 4096 in four parts of 112 small tiles 14.6, in two 21.9
+    // parts 34; 17 x 7168 x 4096 in four parts of 112 small tiles 14.6, in two 21.9;
+    // 2048 x 24 x 28672 in 16 parts of 32 narrow tiles 29.3, in eight 31. More than 32 parts cost the join
+    // more than they save: 17 x 24 x 28672 in 32 13.7, in 64 15.4
     s = 1;
     const int64_t slots = k >= MHC_LINEAR_MEDIUM ? 256 : 512;
-    while (s < kMaxSplits && M > 0 && tiles(k) * s * 2 <= slots && all / (s * 2) >= 4) s *= 2;
+    while (s < 32 && M > 0 && tiles(k) * s * 2 <= slots && all / (s * 2) >= 4) s *= 2;
   }
   if (s > all) s = all;
   // no empty part
