@@ -69,19 +69,23 @@ __device__ __forceinline__ float activate(float v) {
   return v;
 }
 
-// act'(v), for the backward.
+// act'(v), for the backward; its limit, 0 or 1, at an infinite v (a z past the
+// range of fp16 is stored as one), NaN at NaN alone.
 template <int ACT>
 __device__ __forceinline__ float slope(float v) {
   if constexpr (ACT == MHC_ACT_RELU) return v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v);
   if constexpr (ACT == MHC_ACT_SILU) {
-    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * v));
-    return s * fmaf(v, 1.0f - s, 1.0f);
+    // from 200 on the sigmoid is 0 or 1, which times an infinite v would be a NaN
+    const float c = v < -200.0f ? -200.0f : (v > 200.0f ? 200.0f : v);
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * c));
+    return s * fmaf(c, 1.0f - s, 1.0f);
   }
   if constexpr (ACT == MHC_ACT_GELU) {
     const float a = fminf(fabsf(v), 30.0f);
     const float tail = half_erfc_sqrt2(a);
     const float density = 0.39894228f * __builtin_amdgcn_exp2f(-0.72134752f * a * a);
-    return (v < 0.0f ? tail : 1.0f - tail) + (v < 0.0f ? -a : a) * density + (v - v) * 0.0f;
+    const float r = (v < 0.0f ? tail : 1.0f - tail) + (v < 0.0f ? -a : a) * density;
+    return v != v ? v : r;
   }
   return 1.0f;
 }

@@ -27,7 +27,8 @@
  *     grad_weight = gz^T x                       [N, K]
  *     grad_bias   = sum over m of gz             [N], the sum in fp32
  * in the type of x; each output may be NULL (not wanted). The residual's
- * gradient is grad_out itself.
+ * gradient is grad_out itself. act' of an infinite z is its limit, 0 or 1 (in
+ * fp16 a z past +-65520 is stored as an infinity).
  *
  * The order of a sum over k depends on M, N, K, the type and the launch shape,
  * on nothing else: a call repeated gives the same bytes. With a launch that
