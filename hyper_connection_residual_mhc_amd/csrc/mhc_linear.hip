@@ -1212,9 +1212,9 @@ __global__ __launch_bounds__(256) void linear_pad_kernel(PadJob a, PadJob b, Pad
 // ---------------------------------------------------------------------------
 
 // gz = rnd(grad_out * act'(z)) where gz is given, and this block's rows of the
-// bias's sums where partial is: 512 columns to a block, 8 to a lane; each of
-// the four waves takes every fourth row, four rows' loads in flight, joined in
-// ascending order.
+// bias's sums (of the products before that rounding) where partial is: 512
+// columns to a block, 8 to a lane; each of the four waves takes every fourth
+// row, four rows' loads in flight, joined in ascending order.
 template <int F, int ACT>
 __global__ __launch_bounds__(256) void linear_gz_kernel(
     const typename Store<F>::type* __restrict__ grad_out,

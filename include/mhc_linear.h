@@ -25,7 +25,7 @@
  *     gz          = rnd(grad_out * act'(z))      (rounded: the next products read 16 bits)
  *     grad_x      = gz W                         [M, K]
  *     grad_weight = gz^T x                       [N, K]
- *     grad_bias   = sum over m of gz             [N], the sum in fp32
+ *     grad_bias   = sum over m of grad_out * act'(z), unrounded, in fp32     [N]
  * in the type of x; each output may be NULL (not wanted). The residual's
  * gradient is grad_out itself. act' of an infinite z is its limit, 0 or 1 (in
  * fp16 a z past +-65520 is stored as an infinity).

@@ -1,7 +1,8 @@
-"""The product's backward where z passed its type's range (include/mhc_linear.h):
+"""The product's backward at the limits of 16 bits (include/mhc_linear.h). Where z passed its range:
 a pre-activation beyond +-65520 is stored as an infinity in fp16 while the
 forward's output, made from the fp32 value, may be finite, so the slope at an
-infinite z is the activation's limit."""
+infinite z is the activation's limit. And where its products are rounded: grad_bias sums them
+before that."""
 
 from __future__ import annotations
 
@@ -76,3 +77,24 @@ def test_gradients_where_fp16_z_overflows(device, activation):
     R.assert_within(gx, wx, tol + R.rounding(wx.abs() + tol, torch.float16), "grad_x")
     tol = dz.t() @ xv.abs() + gz.abs().t() @ xv.abs() * 2.0 ** -18
     R.assert_within(gw, ww, tol + R.rounding(ww.abs() + tol, torch.float16), "grad_weight")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("activation", ["silu", "gelu"])
+def test_bias_gradient_sums_before_the_rounding(device, activation):
+    """grad_bias adds grad_out * act'(z) before its rounding to 16 bits: over equal rows it is within half a step of
+    the exact sum, which the sum of the rounded products is not."""
+    from hyper_connection_residual_mhc_amd import linear as L
+    gen = torch.Generator().manual_seed(5)
+    M, N, t = 1000, 200, torch.float16
+    g, z = (R.normal(gen, 1, N, dtype=t, scale=s).expand(M, N).contiguous() for s in (0.01, 1.0))
+    gb = L.linear_backward(g.to(device), torch.ones(M, 8, dtype=t, device=device), torch.ones(N, 8, dtype=t, device=device),
+                           activation=activation, z=z.to(device), bias=True)[2]
+    each = (R.d(g) * R.act_slope(R.d(z), activation))[0]
+    want = each * M
+    # the slope (1e-5 fitted tail, 2^-20 of its parts), the product, and additions of at most 1000 / 4 + 4 + 256 equal
+    # terms, each off by at most half a step of fp32
+    tol = R.d(g)[0].abs() * M * (1e-5 + 8 * 2.0 ** -20) + want.abs() * (2 + 510) * R.U32
+    rounded = (each.to(t).double() * M).to(t).double()
+    assert bool(((rounded - want).abs() > tol + R.rounding(want.abs() + tol, t)).any())
+    R.assert_within(gb, want, tol + R.rounding(want.abs() + tol, t), "grad_bias")
