@@ -270,8 +270,10 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 
 // Starts a load of BYTES for each lane from `offset` + `at` of the buffer to the
 // wave's consecutive places in LDS from `to` on; a lane past the buffer's end
-// brings zeros (the check counts `at` too). No register is written; the loads
-// are waited for by wait_tiles().
+// brings zeros (the check counts `at` too). No vector register is written; the
+// loads are waited for by wait_tiles(). m0 is a reserved register, which a list
+// of clobbers cannot name: nothing else in this library may use it (a test
+// reads the machine code for that).
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(uint32_t offset, i32x4 rsrc, uint32_t at, uint32_t to) {
   if constexpr (BYTES == 16)
