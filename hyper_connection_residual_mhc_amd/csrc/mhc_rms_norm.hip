@@ -187,7 +187,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
   constexpr int kStep = THREADS * 8;
   constexpr bool kKeep = ITER > 0;
   constexpr int kUnroll = kKeep ? ITER : 1;
-  __shared__ float part[3][THREADS / 64];
+  __shared__ float part[2][THREADS / 64];
   const int64_t iters = kKeep ? ITER : (H + kStep - 1) / kStep;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     float p[SRC >= 2 ? SRC : 1];
