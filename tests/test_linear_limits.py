@@ -98,3 +98,23 @@ def test_bias_gradient_sums_before_the_rounding(device, activation):
     rounded = (each.to(t).double() * M).to(t).double()
     assert bool(((rounded - want).abs() > tol + R.rounding(want.abs() + tol, t)).any())
     R.assert_within(gb, want, tol + R.rounding(want.abs() + tol, t), "grad_bias")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [3, 70])
+def test_forward_of_infinite_z(device, M):
+    """A bias of -inf or +inf, as a mask of columns: relu and gelu give 0 and inf, silu NaN and inf, and the other
+    columns are what they are without it."""
+    from hyper_connection_residual_mhc_amd import linear as L
+    gen = torch.Generator().manual_seed(M)
+    x, w = R.normal(gen, M, 96).to(device), R.normal(gen, 40, 96).to(device)
+    bias = R.normal(gen, 40)
+    masked = bias.clone()
+    masked[5], masked[11] = -INF, INF
+    rest = [n for n in range(40) if n not in (5, 11)]
+    for activation in ("relu", "gelu", "silu"):
+        plain = L.linear(x, w, bias.to(device), activation=activation).out.cpu()
+        out = L.linear(x, w, masked.to(device), activation=activation).out.cpu()
+        assert R.same_bytes(out[:, rest], plain[:, rest])
+        assert (out[:, 11] == INF).all()
+        assert torch.isnan(out[:, 5]).all() if activation == "silu" else (out[:, 5] == 0).all()
