@@ -600,8 +600,10 @@ __device__ __forceinline__ void write_tile(const TileArgs& a, const Place& at, u
 // row's come by the four) go the same way. Through registers there are two
 // stages, and block scales are read for each tile by the lanes that use them.
 //
-// 64 x 64 tiles in three stages (three blocks to a CU): 512 x 4096 x 4096 in
-// bf16 27.3 us, two stages 33.6, four 27.7. 128 x 128 in two stages (two blocks
+// 64 x 64 tiles in three stages (three blocks to a CU): 256 x 4096 x 4096 in
+// bf16, in the two parts that the policy gives it, 19.8 us, two stages 23.2,
+// four 19.9; 512 x 4096 x 4096 by name and in one part 26.1, 32.1 and 27.0.
+// 128 x 128 in two stages (two blocks
 // to a CU, which fill each other's waits): 1024 x 4096 x 4096 44 us, three or
 // four stages and one block 50. Block scales through LDS: 128 x 4096 x 7168 18.3
 // us, by each lane 23.9. At least two waves to a SIMD are asked for: with more
@@ -1149,8 +1151,8 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs a) {
 // Operands whose rows are no multiple of 16 bytes cannot be loaded straight into
 // LDS. Where the product is long enough they are copied into the workspace
 // first, rows padded with zeros: one pass over them, against tiles that go
-// through registers (2048 x 2048 x 2047 in bf16: 54 us, backward 105 and 106 us a product;
-// with whole rows 35 and 36).
+// through registers (2048 x 2048 x 2047 in bf16: 41 us, a product of the backward 81; with
+// copies 37 and 36; 2048 x 2048 x 2048 takes 25 and 26). Where they pay: kPadForward.
 // ---------------------------------------------------------------------------
 
 struct PadJob {
@@ -1348,6 +1350,10 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
   };
   int32_t k = want;
   if (k == 0) {
+    // The row kernel does not split its sum: 1, 4 and 16 rows x 24 columns take it 4.8, 5.3 and 7.0
+    // us at K = 4096, the narrow tiles in parts 8.1, 8.4 and 8.7; x 1024 columns 5.5, 6.1 and 8.0 against
+    // 10. Over a long sum with few columns the tiles would be ahead, at K = 28672 11.0, 12.1 and
+    // 12.6 against 15.5, 19.3 and 32.9 (1024 columns 20 against 24 to 39).
     if (M <= 16) k = MHC_LINEAR_ROWS;
     else if (N <= 32) k = MHC_LINEAR_NARROW;
     else if (tiles(MHC_LINEAR_LARGE) >= 192) k = MHC_LINEAR_LARGE;
@@ -1391,8 +1397,10 @@ int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 // Products of at least this many terms have operands without whole rows copied
 // first. Forward in bf16, with at least kPadRows rows of each, through registers and with
 // copies: 512 x 4096 x 2047 31 and 36 us, 2048 x 2048 x 2047 41 and 37, 4096 x 4096 x 2047
-// 110 and 73. A product of the backward, where turned operands lose more: 1024 x 1024 x 1023 17
-// and 18.5 us, 512 x 2048 x 2047 24 and 21, 2048 x 2048 x 2047 81 and 37.
+// 109 and 76. A product of the backward, where turned operands lose more: 1024 x 1024 x 1023 17.5
+// and 19 us, 512 x 2048 x 2047 27 and 26 (x's gradient), 20 and 17 (the weight's), 2048 x 2048 x
+// 2047 81 and 36. Rows alone decide: operands of whole rows at addresses that are no
+// multiples of 16 are not copied (4096 x 7168 x 4096 197 us, so 455).
 constexpr int64_t kPadForward = 3LL << 31;
 constexpr int64_t kPadRows = 512;
 constexpr int64_t kPadBackward = 3LL << 29;

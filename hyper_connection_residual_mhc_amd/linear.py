@@ -206,7 +206,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
            return_z: bool = False) -> LinearOut:
     """The product with freshly allocated outputs (no autograd). return_z:
     also the value before the activation, which the backward needs unless
-    the activation is "none"."""
+    the activation is "none". The launch is the policy's; where a row's bytes
+    must not depend on the batch, `mhc_linear_fwd` takes a launch by name."""
     sizes = _check_fwd_inputs(x, weight, bias, residual, x_scales, weight_scales)
     M, N, _, _, kind = sizes
     out = x.new_empty((M, N), dtype=kind)

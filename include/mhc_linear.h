@@ -7,6 +7,7 @@
  *     out = act(z) + residual          residual, out, z [M, N]
  *     act: MHC_ACT_NONE v, _RELU max(v, 0), _SILU v / (1 + exp(-v)),
  *          _GELU v * (1 + erf(v / sqrt 2)) / 2
+ *          (at v = -inf RELU and GELU give their limit 0, SILU its formula's NaN)
  *
  * dtype says what x and W are:
  *     MHC_LINEAR_BF16, MHC_LINEAR_F16   16-bit values; bias, residual, out and z in the same type
@@ -32,10 +33,13 @@
  *
  * The order of a sum over k depends on M, N, K, the type and the launch shape,
  * on nothing else: a call repeated gives the same bytes. With a launch that
- * names a tile kernel and splits = 1, a row's bytes do not depend on M either.
+ * names a tile kernel and splits = 1, a row's bytes do not depend on M either;
+ * with the policy's launch they do (from 16 to 17 rows, for one), and the
+ * backward always takes the policy's.
  *
  * Rules: as in mhc_h_aggregate.h - device pointers, contiguous row-major
- * tensors at any element alignment, nothing allocated, calls only enqueue on
+ * tensors at any element alignment (the same bytes, but about twice the time
+ * where x or W does not start at a multiple of 16), nothing allocated, calls only enqueue on
  * `stream`. M == 0 is a successful call (the backward then writes grad_weight
  * and grad_bias = +0.0). M < 0, N < 1, K < 1, K > MHC_LINEAR_MAX_K, M or N
  * over 2^31 - 1 (in the backward, which sums over them, over
@@ -47,7 +51,8 @@
  * an input or another output MHC_ERROR_ALIASING; with either nothing is
  * launched. A failed launch gives MHC_ERROR_HIP. The workspace is aligned to 16
  * bytes (the sums of a split call are in it, and copies of long operands whose
- * rows are not whole pieces of 16 bytes); its contents mean nothing before and
+ * rows are not whole pieces of 16 bytes; the backward's is sized for any act
+ * and all three gradients, with M x N values of gz in it); its contents mean nothing before and
  * after a call; calls that share one must not overlap in time, and neither must
  * two captured graphs of such calls. start_event / stop_event (hipEvent_t cast
  * to void*, each may be NULL) take the start of the call's first kernel and the

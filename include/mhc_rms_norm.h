@@ -34,7 +34,10 @@
  * grad_x is the gradient of x and of r alike, or of the collapsed row, which
  * mhc_h_aggregate_bwd takes further.
  *
- * Values are fp32 in registers and sums are held in fp32. The sums over h
+ * Values are fp32 in registers and sums are held in fp32: a row whose sum of
+ * squares passes the range of fp32 (values from about 1.8e19 / sqrt(H) on) has
+ * rstd 0, and squares below 2^-149 count as 0 (with eps 0 a row of nothing else
+ * has rstd inf). The sums over h
  * follow an order that depends only on H, so a row's bytes never depend on T or
  * on other rows; grad_weight sums rows in an order that depends only on T and H.
  *
@@ -92,7 +95,8 @@ mhc_status mhc_rms_norm_fwd(const void* x, const void* residual, const float* pr
 
 /* Bytes of device memory the backward needs as its workspace (contents before
  * and after a call mean nothing; calls that share one must not overlap in
- * time), or -1 for a T or H that is out of range. */
+ * time, and neither must two captured graphs of such calls), or -1 for a T or H
+ * that is out of range. */
 int64_t mhc_rms_norm_bwd_workspace_bytes(int64_t T, int64_t H);
 
 mhc_status mhc_rms_norm_bwd(const void* grad_y, const void* stored, const void* weight,
