@@ -1399,7 +1399,7 @@ int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
 // copies: 512 x 4096 x 2047 31 and 36 us, 2048 x 2048 x 2047 41 and 37, 4096 x 4096 x 2047
 // 109 and 76. A product of the backward, where turned operands lose more: 1024 x 1024 x 1023 17.5
 // and 19 us, 512 x 2048 x 2047 27 and 26 (x's gradient), 20 and 17 (the weight's), 2048 x 2048 x
-// 2047 81 and 36. Rows alone decide: operands of whole rows at addresses that are no
+// 2047 81 and 36. The rows' length alone decides: operands of whole rows at addresses that are no
 // multiples of 16 are not copied (4096 x 7168 x 4096 197 us, so 455).
 constexpr int64_t kPadForward = 3LL << 31;
 constexpr int64_t kPadRows = 512;

@@ -38,9 +38,9 @@
  * backward always takes the policy's.
  *
  * Rules: as in mhc_h_aggregate.h - device pointers, contiguous row-major
- * tensors at any element alignment (the same bytes, but about twice the time
- * where x or W does not start at a multiple of 16), nothing allocated, calls only enqueue on
- * `stream`. M == 0 is a successful call (the backward then writes grad_weight
+ * tensors at any element alignment (the same bytes, in two to three times
+ * the time where x or W does not start at a multiple of 16), nothing allocated,
+ * calls only enqueue on `stream`. M == 0 is a successful call (the backward then writes grad_weight
  * and grad_bias = +0.0). M < 0, N < 1, K < 1, K > MHC_LINEAR_MAX_K, M or N
  * over 2^31 - 1 (in the backward, which sums over them, over
  * MHC_LINEAR_MAX_K), N over 2^26 with M <= 16, more than 2^23 tiles (of 256 x
