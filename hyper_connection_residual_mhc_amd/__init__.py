@@ -35,6 +35,11 @@ _LINEAR_NAMES = (
     "mhc_linear_fwd", "mhc_linear_bwd", "mhc_linear_plan", "mhc_linear_fwd_workspace_bytes",
     "mhc_linear_bwd_workspace_bytes", "linear_backward", "Linear", "linear_autograd",
 )
+# `.gated` the module keeps its name here: the call is `gated.gated`.
+_GATED_NAMES = (
+    "mhc_gated_fwd", "mhc_gated_bwd", "mhc_gated_plan", "mhc_gated_fwd_workspace_bytes",
+    "mhc_gated_bwd_workspace_bytes", "gated_backward", "Gated", "gated_autograd",
+)
 _POST_NAMES = (
     "mhc_post_fwd", "mhc_post_bwd", "post_update", "post_update_backward", "PostUpdate",
     "post_update_autograd",
@@ -58,6 +63,9 @@ def __getattr__(name: str):
     if name in _LINEAR_NAMES:
         from . import linear
         return getattr(linear, name)
+    if name in _GATED_NAMES:
+        from . import gated
+        return getattr(gated, name)
     if name in _POST_NAMES:
         from . import post
         return getattr(post, name)

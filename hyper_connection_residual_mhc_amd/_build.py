@@ -8,6 +8,8 @@ the measurement library the tests and the benchmark use:
 * libmhc_coeff_bwd.so    (csrc/mhc_coeff_bwd.hip,   include/mhc_coeff_bwd.h)
 * libmhc_rms_norm.so     (csrc/mhc_rms_norm.hip,    include/mhc_rms_norm.h)
 * libmhc_linear.so       (csrc/mhc_linear.hip,      include/mhc_linear.h)
+* libmhc_gated.so        (csrc/mhc_gated.hip,       include/mhc_gated.h)
+* libmhc_cross_entropy.so (csrc/mhc_cross_entropy.hip, include/mhc_cross_entropy.h)
 * libmhc_post.so         (csrc/mhc_post.hip,        include/mhc_post.h)
 * libmhc_probes.so       (csrc/mhc_probes.hip,      csrc/mhc_probes.h;
                           not part of the operation)
@@ -61,6 +63,8 @@ SRC = PKG_DIR / "csrc" / "mhc_h_aggregate.hip"
 COEFF_SRC = PKG_DIR / "csrc" / "mhc_coeff_bwd.hip"
 NORM_SRC = PKG_DIR / "csrc" / "mhc_rms_norm.hip"
 LINEAR_SRC = PKG_DIR / "csrc" / "mhc_linear.hip"
+GATED_SRC = PKG_DIR / "csrc" / "mhc_gated.hip"
+CROSS_ENTROPY_SRC = PKG_DIR / "csrc" / "mhc_cross_entropy.hip"
 POST_SRC = PKG_DIR / "csrc" / "mhc_post.hip"
 PROBE_SRC = PKG_DIR / "csrc" / "mhc_probes.hip"
 INCLUDE_DIR = REPO_DIR / "include"
@@ -68,12 +72,16 @@ HEADER = INCLUDE_DIR / "mhc_h_aggregate.h"
 COEFF_HEADER = INCLUDE_DIR / "mhc_coeff_bwd.h"
 NORM_HEADER = INCLUDE_DIR / "mhc_rms_norm.h"
 LINEAR_HEADER = INCLUDE_DIR / "mhc_linear.h"
+GATED_HEADER = INCLUDE_DIR / "mhc_gated.h"
+CROSS_ENTROPY_HEADER = INCLUDE_DIR / "mhc_cross_entropy.h"
 POST_HEADER = INCLUDE_DIR / "mhc_post.h"
 LIB_DIR = PKG_DIR / "lib"
 LIB_PATH = LIB_DIR / "libmhc_h_aggregate.so"
 COEFF_LIB_PATH = LIB_DIR / "libmhc_coeff_bwd.so"
 NORM_LIB_PATH = LIB_DIR / "libmhc_rms_norm.so"
 LINEAR_LIB_PATH = LIB_DIR / "libmhc_linear.so"
+GATED_LIB_PATH = LIB_DIR / "libmhc_gated.so"
+CROSS_ENTROPY_LIB_PATH = LIB_DIR / "libmhc_cross_entropy.so"
 POST_LIB_PATH = LIB_DIR / "libmhc_post.so"
 PROBE_LIB_PATH = LIB_DIR / "libmhc_probes.so"
 BUILD_DIR = REPO_DIR / "_build"
@@ -81,11 +89,12 @@ BUILD_DIR = REPO_DIR / "_build"
 # source -> library, header
 LIBRARIES = {SRC: (LIB_PATH, HEADER), COEFF_SRC: (COEFF_LIB_PATH, COEFF_HEADER),
              NORM_SRC: (NORM_LIB_PATH, NORM_HEADER),
-             LINEAR_SRC: (LINEAR_LIB_PATH, LINEAR_HEADER), POST_SRC: (POST_LIB_PATH, POST_HEADER),
+             LINEAR_SRC: (LINEAR_LIB_PATH, LINEAR_HEADER), GATED_SRC: (GATED_LIB_PATH, GATED_HEADER),
+             POST_SRC: (POST_LIB_PATH, POST_HEADER),
              PROBE_SRC: (PROBE_LIB_PATH, PKG_DIR / "csrc" / "mhc_probes.h")}
 # source -> its own flags (see the module docstring)
 SOURCE_FLAGS = {SRC: ["-mllvm", "-amdgpu-kernarg-preload-count=16"], COEFF_SRC: [],
-                NORM_SRC: [], LINEAR_SRC: [], POST_SRC: [], PROBE_SRC: []}
+                NORM_SRC: [], LINEAR_SRC: [], GATED_SRC: [], POST_SRC: [], PROBE_SRC: []}
 
 ARCH = "gfx950"
 

@@ -1,5 +1,5 @@
 """ctypes view of the C ABIs in include/ (mhc_h_aggregate.h, mhc_coeff_bwd.h,
-mhc_rms_norm.h, mhc_linear.h, mhc_post.h), and of the measurement library
+mhc_rms_norm.h, mhc_linear.h, mhc_gated.h, mhc_post.h), and of the measurement library
 (csrc/mhc_probes.h) that the tests and the benchmark use.
 
 Loading fails loudly (ImportError) when a shared library has not been built,
@@ -14,9 +14,9 @@ import ctypes
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_uint32, c_void_p
 
 from . import _build
-from ._build import (COEFF_LIB_PATH, COEFF_SRC, LIB_PATH, LINEAR_LIB_PATH, LINEAR_SRC,
-                     NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH, POST_SRC, PROBE_LIB_PATH, PROBE_SRC,
-                     SRC)
+from ._build import (COEFF_LIB_PATH, COEFF_SRC, GATED_LIB_PATH, GATED_SRC, LIB_PATH,
+                     LINEAR_LIB_PATH, LINEAR_SRC, NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH, POST_SRC,
+                     PROBE_LIB_PATH, PROBE_SRC, SRC)
 
 MHC_SUCCESS = 0
 MHC_ERROR_INVALID_VALUE = 1
@@ -119,7 +119,7 @@ MHC_COEFF_SCRATCH_BYTES = 2 << 20
 
 MHC_NORM_ABI_VERSION = 1
 MHC_NORM_F32, MHC_NORM_BF16, MHC_NORM_F16 = 0, 1, 2
-MHC_NORM_SAME, MHC_NORM_E4M3_ROW, MHC_NORM_E4M3_MX = 0, 1, 2
+MHC_NORM_SAME, MHC_NORM_E4M3_ROW, MHC_NORM_E4M3_MX, MHC_NORM_I8_ROW = 0, 1, 2, 4
 
 # Every symbol include/mhc_rms_norm.h declares.
 _NORM_FWD = [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_float, c_void_p, c_void_p,
@@ -138,8 +138,10 @@ NORM_SIGNATURES = {
 
 MHC_LINEAR_ABI_VERSION = 1
 MHC_LINEAR_BF16, MHC_LINEAR_F16, MHC_LINEAR_E4M3_ROW, MHC_LINEAR_E4M3_MX = 1, 2, 3, 4
+MHC_LINEAR_I8_ROW = 6
 MHC_ACT_NONE, MHC_ACT_RELU, MHC_ACT_SILU, MHC_ACT_GELU = 0, 1, 2, 3
 MHC_LINEAR_MAX_K = 1 << 21
+MHC_LINEAR_MAX_K_I8 = 131071
 MHC_LINEAR_ROWS, MHC_LINEAR_NARROW, MHC_LINEAR_SMALL, MHC_LINEAR_MEDIUM, MHC_LINEAR_LARGE = \
     1, 2, 3, 4, 5
 
@@ -169,6 +171,27 @@ LINEAR_SIGNATURES = {
     "mhc_linear_bwd": (c_int, _LINEAR_BWD + [c_void_p] * 3),
     "mhc_linear_validate_fwd": (c_int, _LINEAR_FWD + [POINTER(mhc_linear_launch)]),
     "mhc_linear_validate_bwd": (c_int, _LINEAR_BWD),
+}
+
+MHC_GATED_ABI_VERSION = 1
+MHC_GATED_MAX_BWD_N = 1 << 20
+
+# Every symbol include/mhc_gated.h declares.
+_GATED_FWD = [c_void_p] * 12 + [c_int64] * 4 + [c_int32, c_int32]
+_GATED_BWD = [c_void_p] * 12 + [c_int64] * 4 + [c_int32, c_int32]
+GATED_SIGNATURES = {
+    "mhc_gated_abi_version": (c_int, []),
+    "mhc_gated_last_error_message": (c_char_p, []),
+    "mhc_gated_plan": (c_int, [c_int64, c_int64, c_int64, c_int32, POINTER(mhc_linear_launch),
+                               POINTER(mhc_linear_launch)]),
+    "mhc_gated_fwd_workspace_bytes": (c_int64, [c_int64, c_int64, c_int64, c_int32,
+                                                POINTER(mhc_linear_launch)]),
+    "mhc_gated_bwd_workspace_bytes": (c_int64, [c_int64, c_int64, c_int64, c_int32]),
+    "mhc_gated_fwd": (c_int, _GATED_FWD + [c_void_p, POINTER(mhc_linear_launch), c_void_p,
+                                           c_void_p]),
+    "mhc_gated_bwd": (c_int, _GATED_BWD + [c_void_p] * 3),
+    "mhc_gated_validate_fwd": (c_int, _GATED_FWD + [POINTER(mhc_linear_launch)]),
+    "mhc_gated_validate_bwd": (c_int, _GATED_BWD),
 }
 
 MHC_POST_ABI_VERSION = 1
@@ -256,6 +279,13 @@ def linear_lib() -> ctypes.CDLL:
                 "mhc_linear_abi_version", MHC_LINEAR_ABI_VERSION)
 
 
+def gated_lib() -> ctypes.CDLL:
+    """The gated feed-forward library (loaded once). ImportError if missing or
+    stale."""
+    return _get("gated", GATED_LIB_PATH, GATED_SRC, GATED_SIGNATURES, "mhc_gated_abi_version",
+                MHC_GATED_ABI_VERSION)
+
+
 def post_lib() -> ctypes.CDLL:
     """The write-back library (loaded once). ImportError if missing or stale."""
     return _get("post", POST_LIB_PATH, POST_SRC, POST_SIGNATURES, "mhc_post_abi_version",
@@ -295,6 +325,11 @@ def check_norm(status: int) -> None:
 def check_linear(status: int) -> None:
     if status != MHC_SUCCESS:
         raise MhcError(status, linear_lib().mhc_linear_last_error_message().decode())
+
+
+def check_gated(status: int) -> None:
+    if status != MHC_SUCCESS:
+        raise MhcError(status, gated_lib().mhc_gated_last_error_message().decode())
 
 
 def check_post(status: int) -> None:

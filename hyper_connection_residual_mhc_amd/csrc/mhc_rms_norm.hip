@@ -19,6 +19,7 @@
 namespace {
 
 constexpr float kE4M3Max = 448.0f;
+constexpr float kI8Max = 127.0f;
 
 // Blocks of a launch at most; a block takes every gridDim.x-th row.
 constexpr int64_t kMaxBlocks = 1 << 20;
@@ -137,7 +138,21 @@ __device__ __forceinline__ u32x2 pack_e4m3(const float (&v)[8]) {
   return r;
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* p, int count, u32x2 c) {
+// Eight fp32 values of at most 127 as 8-bit integers, nearest even.
+__device__ __forceinline__ u32x2 pack_i8(const float (&v)[8]) {
+  u32x2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w |= (static_cast<uint32_t>(static_cast<int>(rintf(v[4 * i + e]))) & 0xFFu) << (8 * e);
+    r[i] = w;
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_codes(uint8_t* p, int count, u32x2 c) {
   if (count >= 8) {
     __builtin_nontemporal_store(c, reinterpret_cast<u32x2_at1*>(p));
     return;
@@ -275,7 +290,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
           store_chunk<F>(static_cast<typename Store<F>::type*>(out) + t * H + h, count, c);
         }
       }
-    } else if constexpr (FMT == MHC_NORM_E4M3_ROW) {
+    } else if constexpr (FMT == MHC_NORM_E4M3_ROW || FMT == MHC_NORM_I8_ROW) {
       // The normed row in registers where it fits them, else computed twice.
       float kept[kKeep ? ITER : 1][8];
       float amax = 0.0f;
@@ -286,10 +301,15 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
         if (h < H) {
           value(k, h, static_cast<int>(min(H - h, static_cast<int64_t>(8))), v);
           amax = fmaxf(amax, amax8(v));
+          if constexpr (FMT == MHC_NORM_I8_ROW) {
+            // integers have no NaN: the row's scale says that there is one
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = v[e] != v[e] ? INFINITY : amax;
+          }
         }
       }
       amax = block_max<THREADS>(amax, part[1]);
-      const float scale = fmaxf(amax / kE4M3Max, 0x1p-126f);
+      const float scale = fmaxf(amax / (FMT == MHC_NORM_I8_ROW ? kI8Max : kE4M3Max), 0x1p-126f);
       const float inverse = 1.0f / scale;
       if (threadIdx.x == 0) static_cast<float*>(scales)[t] = scale;
 #pragma unroll kUnroll
@@ -299,9 +319,15 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
           const int count = static_cast<int>(min(H - h, static_cast<int64_t>(8)));
           float(&v)[8] = kept[kKeep ? k : 0];
           if constexpr (!kKeep) value(k, h, count, v);
+          if constexpr (FMT == MHC_NORM_I8_ROW) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = v[e] * inverse;
-          store_e4m3(static_cast<uint8_t*>(out) + t * H + h, count, pack_e4m3(v));
+            for (int e = 0; e < 8; ++e) v[e] = scale == INFINITY ? 0.0f : v[e] * inverse;
+            store_codes(static_cast<uint8_t*>(out) + t * H + h, count, pack_i8(v));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = v[e] * inverse;
+            store_codes(static_cast<uint8_t*>(out) + t * H + h, count, pack_e4m3(v));
+          }
         }
       }
     } else {
@@ -322,7 +348,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_fwd_kernel(
         if (in) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = v[e] * inverse;
-          store_e4m3(static_cast<uint8_t*>(out) + t * H + h, count, pack_e4m3(v));
+          store_codes(static_cast<uint8_t*>(out) + t * H + h, count, pack_e4m3(v));
           if (threadIdx.x % 4 == 0)
             static_cast<uint8_t*>(scales)[t * blocks + h / 32] =
                 static_cast<uint8_t>(a == INFINITY ? 255 : power + 127);
@@ -634,9 +660,9 @@ mhc_status validate_fwd(const void* x, const void* residual, const void* pre, in
   const mhc_status st = check_sizes(T, H, dtype, weight_dtype);
   if (st != MHC_SUCCESS) return st;
   if (out_format != MHC_NORM_SAME && out_format != MHC_NORM_E4M3_ROW &&
-      out_format != MHC_NORM_E4M3_MX)
+      out_format != MHC_NORM_E4M3_MX && out_format != MHC_NORM_I8_ROW)
     return fail(MHC_ERROR_INVALID_VALUE,
-                "out_format must be MHC_NORM_SAME, _E4M3_ROW or _E4M3_MX (got %d)", out_format);
+                "out_format must be MHC_NORM_SAME, _E4M3_ROW, _E4M3_MX or _I8_ROW (got %d)", out_format);
   if (!(eps >= 0.0f) || !isfinite(eps))
     return fail(MHC_ERROR_INVALID_VALUE, "eps must be finite and not negative (got %g)",
                 static_cast<double>(eps));
@@ -655,7 +681,8 @@ mhc_status validate_fwd(const void* x, const void* residual, const void* pre, in
   const int64_t E = size_of(dtype);
   const bool e8 = out_format != MHC_NORM_SAME;
   const int64_t row = mul_bytes(T, H, E);
-  const int64_t scale_bytes = out_format == MHC_NORM_E4M3_ROW  ? mul_bytes(T, 4, 1)
+  const bool rows = out_format == MHC_NORM_E4M3_ROW || out_format == MHC_NORM_I8_ROW;
+  const int64_t scale_bytes = rows                             ? mul_bytes(T, 4, 1)
                               : out_format == MHC_NORM_E4M3_MX ? mul_bytes(T, (H + 31) / 32, 1)
                                                                : 0;
   const Tensor in[] = {{x, mul_bytes(T, H, pre != nullptr ? E * n : E), E, "x"},
@@ -663,7 +690,7 @@ mhc_status validate_fwd(const void* x, const void* residual, const void* pre, in
                        {pre, pre != nullptr ? mul_bytes(T, n, 4) : 0, 4, "pre"},
                        {weight, H * size_of(weight_dtype), size_of(weight_dtype), "weight"}};
   const Tensor outs[] = {{out, e8 ? mul_bytes(T, H, 1) : row, e8 ? 1 : E, "out"},
-                         {scales, scale_bytes, out_format == MHC_NORM_E4M3_ROW ? 4 : 1, "scales"},
+                         {scales, scale_bytes, rows ? 4 : 1, "scales"},
                          {stored, stored != nullptr ? row : 0, E, "stored"},
                          {rstd, rstd != nullptr ? mul_bytes(T, 4, 1) : 0, 4, "rstd"}};
   return check_tensors(in, outs);
@@ -712,6 +739,7 @@ template <int F, int SRC>
 hipError_t launch_fwd_f(const FwdArgs& a, int32_t fmt) {
   if (fmt == MHC_NORM_SAME) return launch_fwd_h<F, SRC, MHC_NORM_SAME>(a);
   if (fmt == MHC_NORM_E4M3_ROW) return launch_fwd_h<F, SRC, MHC_NORM_E4M3_ROW>(a);
+  if (fmt == MHC_NORM_I8_ROW) return launch_fwd_h<F, SRC, MHC_NORM_I8_ROW>(a);
   return launch_fwd_h<F, SRC, MHC_NORM_E4M3_MX>(a);
 }
 

@@ -1,8 +1,8 @@
 """Python binding of the matrix product with bias, activation and residual in
 its epilogue: argument marshalling only.
 
-16-bit operands, or e4m3 operands with the scales that `norm.rms_norm` writes
-("row": fp32, one a row; "mx": e8m0, one for 32 columns). Formulas, types and
+16-bit operands, or 8-bit operands with the scales that `norm.rms_norm` writes
+(e4m3 "row" and "int8": fp32, one a row; e4m3 "mx": e8m0, one for 32 columns). Formulas, types and
 rules: include/mhc_linear.h. All arithmetic runs in the gfx950 kernels; a
 missing library raises ImportError.
 """
@@ -59,20 +59,21 @@ def _operands(x: torch.Tensor, weight: torch.Tensor, x_scales, weight_scales
     dev = x.device
     if x.dtype in _DTYPES:
         if x_scales is not None or weight_scales is not None:
-            raise ValueError("scales need float8_e4m3fn operands")
+            raise ValueError("scales need float8_e4m3fn or int8 operands")
         require(x, "x", x.dtype, (M, K), dev)
         require(weight, "weight", x.dtype, (N, K), dev)
         return M, N, K, _DTYPES[x.dtype], x.dtype
-    if x.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"x must be bfloat16, float16 or float8_e4m3fn (got {x.dtype})")
-    require(x, "x", torch.float8_e4m3fn, (M, K), dev)
-    require(weight, "weight", torch.float8_e4m3fn, (N, K), dev)
+    if x.dtype not in (torch.float8_e4m3fn, torch.int8):
+        raise TypeError(f"x must be bfloat16, float16, float8_e4m3fn or int8 (got {x.dtype})")
+    require(x, "x", x.dtype, (M, K), dev)
+    require(weight, "weight", x.dtype, (N, K), dev)
     if not isinstance(x_scales, torch.Tensor) or not isinstance(weight_scales, torch.Tensor):
-        raise ValueError("float8_e4m3fn operands need x_scales and weight_scales")
-    if x_scales.dtype == torch.float32:
+        raise ValueError("float8_e4m3fn and int8 operands need x_scales and weight_scales")
+    if x.dtype == torch.int8 or x_scales.dtype == torch.float32:
         require(x_scales, "x_scales", torch.float32, (M,), dev)
         require(weight_scales, "weight_scales", torch.float32, (N,), dev)
-        return M, N, K, _lib.MHC_LINEAR_E4M3_ROW, torch.bfloat16
+        abi = _lib.MHC_LINEAR_I8_ROW if x.dtype == torch.int8 else _lib.MHC_LINEAR_E4M3_ROW
+        return M, N, K, abi, torch.bfloat16
     blocks = -(-K // 32)
     require(x_scales, "x_scales", torch.float8_e8m0fnu, (M, blocks), dev)
     require(weight_scales, "weight_scales", torch.float8_e8m0fnu, (N, blocks), dev)

@@ -2,7 +2,7 @@
 
 One pass over a row adds the residual or collapses the residual streams (the
 bits of `ops.h_aggregate`), norms it, and writes it in the input's type or in
-8 bits (e4m3) with scales that `linear.linear` takes. Formulas, types and
+8 bits (e4m3 or integers) with scales that `linear.linear` takes. Formulas, types and
 rules: include/mhc_rms_norm.h. All arithmetic runs in the gfx950 kernels; a
 missing library raises ImportError.
 """
@@ -20,14 +20,16 @@ from ._lib import check_norm
 
 _DTYPES = {torch.float32: _lib.MHC_NORM_F32, torch.bfloat16: _lib.MHC_NORM_BF16,
            torch.float16: _lib.MHC_NORM_F16}
-_FORMATS = {None: _lib.MHC_NORM_SAME, "row": _lib.MHC_NORM_E4M3_ROW, "mx": _lib.MHC_NORM_E4M3_MX}
+_FORMATS = {None: _lib.MHC_NORM_SAME, "row": _lib.MHC_NORM_E4M3_ROW, "mx": _lib.MHC_NORM_E4M3_MX,
+            "int8": _lib.MHC_NORM_I8_ROW}
+_CODES = {"row": torch.float8_e4m3fn, "mx": torch.float8_e4m3fn, "int8": torch.int8}
 SUPPORTED_HC = (2, 4, 8)
 
 
 class RMSNormOut(NamedTuple):
     """What `rms_norm` returns; a field that was not asked for is None."""
-    y: torch.Tensor                 # [T, H] in x's type, or float8_e4m3fn
-    scales: torch.Tensor | None     # "row": [T] fp32; "mx": [T, ceil(H / 32)] float8_e8m0fnu
+    y: torch.Tensor                 # [T, H] in x's type, or float8_e4m3fn, or int8
+    scales: torch.Tensor | None     # "row", "int8": [T] fp32; "mx": [T, ceil(H / 32)] float8_e8m0fnu
     stored: torch.Tensor | None     # [T, H]: x + residual, or the collapsed streams
     rstd: torch.Tensor | None       # [T] fp32
 
@@ -49,7 +51,7 @@ def _check_inputs(x, weight, residual, pre, quant) -> tuple[int, int, int]:
     """(T, n, H) of a forward call whose inputs are sound."""
     T, n, H = _shapes(x, pre)
     if quant not in _FORMATS:
-        raise ValueError(f'quant must be None, "row" or "mx" (got {quant!r})')
+        raise ValueError(f'quant must be None, "row", "mx" or "int8" (got {quant!r})')
     dev, dt = x.device, x.dtype
     require(x, "x", dt, (T, n, H) if n else (T, H), dev)
     _check_weight(weight, dt, H, dev)
@@ -86,15 +88,15 @@ def mhc_rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, out: torch.Tensor, *
                      ) -> torch.Tensor:
     """out <- norm of x [T, H], of x + residual, or of streams x [T, n, H]
     collapsed with pre [T, n]; writes scales, stored and rstd where given.
-    quant: None, "row" or "mx". Asynchronous."""
+    quant: None, "row", "mx" or "int8". Asynchronous."""
     T, n, H = _check_inputs(x, weight, residual, pre, quant)
     dev, dt = x.device, x.dtype
-    require(out, "out", dt if quant is None else torch.float8_e4m3fn, (T, H), dev)
+    require(out, "out", dt if quant is None else _CODES[quant], (T, H), dev)
     if stored is not None:
         require(stored, "stored", dt, (T, H), dev)
     if rstd is not None:
         require(rstd, "rstd", torch.float32, (T,), dev)
-    if quant == "row":
+    if quant in ("row", "int8"):
         require(scales, "scales", torch.float32, (T,), dev)
     elif quant == "mx":
         require(scales, "scales", torch.float8_e8m0fnu, (T, -(-H // 32)), dev)
@@ -172,8 +174,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *,
     if quant is None:
         y = x.new_empty((T, H)) if n else torch.empty_like(x)
     else:
-        y = x.new_empty((T, H), dtype=torch.float8_e4m3fn)
-        if quant == "row":
+        y = x.new_empty((T, H), dtype=_CODES[quant])
+        if quant != "mx":
             scales = x.new_empty((T,), dtype=torch.float32)
         else:
             scales = x.new_empty((T, -(-H // 32)), dtype=torch.float8_e8m0fnu)

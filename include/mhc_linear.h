@@ -14,9 +14,11 @@
  *     MHC_LINEAR_E4M3_ROW               e4m3 codes with fp32 scales x_scales [M], weight_scales [N]
  *     MHC_LINEAR_E4M3_MX                e4m3 codes with e8m0 scales x_scales [M, ceil(K/32)],
  *                                       weight_scales [N, ceil(K/32)], one for 32 consecutive k
+ *     MHC_LINEAR_I8_ROW                 8-bit integers with fp32 scales x_scales [M], weight_scales [N]
  * and the 8-bit forms (the outputs of mhc_rms_norm_fwd) take and give bf16
  * otherwise. Sums over k and the epilogue are fp32, and out and z are each
- * rounded once. 16-bit products enter the sum exactly; of 8-bit products the
+ * rounded once. 16-bit products enter the sum exactly; the sum of 8-bit integers
+ * is an exact 32-bit integer, rounded to fp32 once; of e4m3 products the
  * matrix instruction drops, in each group of 8 consecutive k, the bits below
  * 2^-13 of the largest product's power of two (so a group is off by at most
  * 7 * 2^-13 of its largest product). bias, residual and z may be NULL (absent).
@@ -35,13 +37,15 @@
  * on nothing else: a call repeated gives the same bytes. With a launch that
  * names a tile kernel and splits = 1, a row's bytes do not depend on M either;
  * with the policy's launch they do (from 16 to 17 rows, for one), and the
- * backward always takes the policy's.
+ * backward always takes the policy's. With 8-bit integers no launch and no M
+ * changes a row's bytes.
  *
  * Rules: as in mhc_h_aggregate.h - device pointers, contiguous row-major
  * tensors at any element alignment (the same bytes, in two to three times
  * the time where x or W does not start at a multiple of 16), nothing allocated,
  * calls only enqueue on `stream`. M == 0 is a successful call (the backward then writes grad_weight
- * and grad_bias = +0.0). M < 0, N < 1, K < 1, K > MHC_LINEAR_MAX_K, M or N
+ * and grad_bias = +0.0). M < 0, N < 1, K < 1, K > MHC_LINEAR_MAX_K (with 8-bit
+ * integers over MHC_LINEAR_MAX_K_I8), M or N
  * over 2^31 - 1 (in the backward, which sums over them, over
  * MHC_LINEAR_MAX_K), N over 2^26 with M <= 16, more than 2^23 tiles (of 256 x
  * 256: 2^21) in one launch, an unknown dtype or act, scales missing or given
@@ -75,6 +79,7 @@ extern "C" {
 #define MHC_LINEAR_F16 2
 #define MHC_LINEAR_E4M3_ROW 3
 #define MHC_LINEAR_E4M3_MX 4
+#define MHC_LINEAR_I8_ROW 6 /* 5 is no type */
 
 #define MHC_ACT_NONE 0
 #define MHC_ACT_RELU 1
@@ -83,6 +88,8 @@ extern "C" {
 
 /* Longest sum accepted. */
 #define MHC_LINEAR_MAX_K (1LL << 21)
+/* And of 8-bit integers, whose sums are held in 32 bits: 131071 (-128)^2 < 2^31. */
+#define MHC_LINEAR_MAX_K_I8 131071
 
 /* Kernels of the forward (mhc_linear_launch.kernel). */
 #define MHC_LINEAR_ROWS 1    /* up to 16 rows of x: the weight is streamed once */

@@ -15,6 +15,10 @@
  *     MHC_NORM_SAME      out[t,h] = rnd(v[t,h])
  *     MHC_NORM_E4M3_ROW  scales[t] = max(amax / 448, 2^-126), amax over the row of |v|   (fp32 [T])
  *                        out[t,h] = e4m3(v[t,h] * (1 / scales[t]))
+ *     MHC_NORM_I8_ROW    scales[t] = max(amax / 127, 2^-126), amax over the row of |v|   (fp32 [T])
+ *                        out[t,h] = the integer nearest to v[t,h] * (1 / scales[t]), ties to even;
+ *                        a row with an infinity or a NaN has scale infinity and codes 0
+ *                        (a product with it is NaN)
  *     MHC_NORM_E4M3_MX   for each block of 32 consecutive columns (the last may be
  *                        short) p = the smallest integer in [-127, 127] with
  *                        amax over the block of |v| <= 448 * 2^p;
@@ -22,7 +26,7 @@
  *                        ([T, ceil(H / 32)] bytes; 255, a NaN, where amax is infinite);
  *                        out[t,h] = e4m3(v[t,h] * 2^-p)
  * e4m3 is the OCP format (4 exponent and 3 mantissa bits, largest 448), rounded
- * to nearest even; by the choice of scale nothing saturates. A NaN stays a NaN.
+ * to nearest even; by the choice of scale nothing saturates. A NaN stays a NaN in e4m3.
  * s and rstd are written where `stored` and `rstd` are given (stored only where
  * s is new, i.e. with a residual or pre).
  *
@@ -80,6 +84,7 @@ extern "C" {
 #define MHC_NORM_SAME 0
 #define MHC_NORM_E4M3_ROW 1
 #define MHC_NORM_E4M3_MX 2
+#define MHC_NORM_I8_ROW 4 /* 3 is no format */
 
 int mhc_rms_norm_abi_version(void);
 
