@@ -6,7 +6,8 @@ The torch-facing names live in `hyper_connection_residual_mhc_amd.ops`,
 `.coeff` for the coefficient backward epilogue, and `.norm`, `.linear` and
 `.post` for the rest of a hyper-connected sublayer (RMS norm, matrix
 product, write-back into the streams); they are re-exported here on first
-access. Calling them loads the shared libraries (ImportError if
+access, and so are those of `.gated` (the gated feed-forward block) and
+`.loss` (the cross entropy of a large vocabulary). Calling them loads the shared libraries (ImportError if
 they have not been built).
 """
 
@@ -40,6 +41,11 @@ _GATED_NAMES = (
     "mhc_gated_fwd", "mhc_gated_bwd", "mhc_gated_plan", "mhc_gated_fwd_workspace_bytes",
     "mhc_gated_bwd_workspace_bytes", "gated_backward", "Gated", "gated_autograd",
 )
+_LOSS_NAMES = (
+    "mhc_cross_entropy_fwd", "mhc_cross_entropy_bwd", "mhc_cross_entropy_grads",
+    "mhc_cross_entropy_workspace_bytes", "linear_cross_entropy", "linear_cross_entropy_backward",
+    "linear_cross_entropy_grads", "LinearCrossEntropy", "linear_cross_entropy_autograd",
+)
 _POST_NAMES = (
     "mhc_post_fwd", "mhc_post_bwd", "post_update", "post_update_backward", "PostUpdate",
     "post_update_autograd",
@@ -66,6 +72,9 @@ def __getattr__(name: str):
     if name in _GATED_NAMES:
         from . import gated
         return getattr(gated, name)
+    if name in _LOSS_NAMES:
+        from . import loss
+        return getattr(loss, name)
     if name in _POST_NAMES:
         from . import post
         return getattr(post, name)

@@ -90,11 +90,13 @@ BUILD_DIR = REPO_DIR / "_build"
 LIBRARIES = {SRC: (LIB_PATH, HEADER), COEFF_SRC: (COEFF_LIB_PATH, COEFF_HEADER),
              NORM_SRC: (NORM_LIB_PATH, NORM_HEADER),
              LINEAR_SRC: (LINEAR_LIB_PATH, LINEAR_HEADER), GATED_SRC: (GATED_LIB_PATH, GATED_HEADER),
+             CROSS_ENTROPY_SRC: (CROSS_ENTROPY_LIB_PATH, CROSS_ENTROPY_HEADER),
              POST_SRC: (POST_LIB_PATH, POST_HEADER),
              PROBE_SRC: (PROBE_LIB_PATH, PKG_DIR / "csrc" / "mhc_probes.h")}
 # source -> its own flags (see the module docstring)
 SOURCE_FLAGS = {SRC: ["-mllvm", "-amdgpu-kernarg-preload-count=16"], COEFF_SRC: [],
-                NORM_SRC: [], LINEAR_SRC: [], GATED_SRC: [], POST_SRC: [], PROBE_SRC: []}
+                NORM_SRC: [], LINEAR_SRC: [], GATED_SRC: [], CROSS_ENTROPY_SRC: [],
+                POST_SRC: [], PROBE_SRC: []}
 
 ARCH = "gfx950"
 

@@ -1,5 +1,5 @@
 """ctypes view of the C ABIs in include/ (mhc_h_aggregate.h, mhc_coeff_bwd.h,
-mhc_rms_norm.h, mhc_linear.h, mhc_gated.h, mhc_post.h), and of the measurement library
+mhc_rms_norm.h, mhc_linear.h, mhc_gated.h, mhc_cross_entropy.h, mhc_post.h), and of the measurement library
 (csrc/mhc_probes.h) that the tests and the benchmark use.
 
 Loading fails loudly (ImportError) when a shared library has not been built,
@@ -14,9 +14,10 @@ import ctypes
 from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_uint32, c_void_p
 
 from . import _build
-from ._build import (COEFF_LIB_PATH, COEFF_SRC, GATED_LIB_PATH, GATED_SRC, LIB_PATH,
-                     LINEAR_LIB_PATH, LINEAR_SRC, NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH, POST_SRC,
-                     PROBE_LIB_PATH, PROBE_SRC, SRC)
+from ._build import (COEFF_LIB_PATH, COEFF_SRC, CROSS_ENTROPY_LIB_PATH, CROSS_ENTROPY_SRC,
+                     GATED_LIB_PATH, GATED_SRC, LIB_PATH, LINEAR_LIB_PATH, LINEAR_SRC,
+                     NORM_LIB_PATH, NORM_SRC, POST_LIB_PATH, POST_SRC, PROBE_LIB_PATH, PROBE_SRC,
+                     SRC)
 
 MHC_SUCCESS = 0
 MHC_ERROR_INVALID_VALUE = 1
@@ -194,6 +195,30 @@ GATED_SIGNATURES = {
     "mhc_gated_validate_bwd": (c_int, _GATED_BWD),
 }
 
+MHC_CROSS_ENTROPY_ABI_VERSION = 1
+MHC_REDUCTION_NONE, MHC_REDUCTION_SUM, MHC_REDUCTION_MEAN = 0, 1, 2
+MHC_CROSS_ENTROPY_MAX_V = 1 << 21
+MHC_CROSS_ENTROPY_CHUNK_BYTES = 1 << 30
+
+# Every symbol include/mhc_cross_entropy.h declares.
+_CE_SIZES = [c_int64] * 3 + [c_int32, POINTER(mhc_linear_launch)]
+_CE_FWD = [c_void_p] * 6 + [c_int64] * 4 + [c_int32, c_int32]
+_CE_BWD = [c_void_p] * 9 + [c_int64] * 4 + [c_int32, c_int32]
+_CE_CALL = [c_int64, c_void_p, POINTER(mhc_linear_launch), c_void_p, c_void_p]
+CROSS_ENTROPY_SIGNATURES = {
+    "mhc_cross_entropy_abi_version": (c_int, []),
+    "mhc_cross_entropy_last_error_message": (c_char_p, []),
+    "mhc_cross_entropy_fwd_workspace_bytes": (c_int64, _CE_SIZES),
+    "mhc_cross_entropy_bwd_workspace_bytes": (c_int64, _CE_SIZES),
+    "mhc_cross_entropy_grads_workspace_bytes": (c_int64, _CE_SIZES),
+    "mhc_cross_entropy_fwd": (c_int, _CE_FWD + _CE_CALL),
+    "mhc_cross_entropy_bwd": (c_int, _CE_BWD + _CE_CALL),
+    "mhc_cross_entropy_grads": (c_int, _CE_BWD + _CE_CALL),
+    "mhc_cross_entropy_validate_fwd": (c_int, _CE_FWD + [POINTER(mhc_linear_launch)]),
+    "mhc_cross_entropy_validate_bwd": (c_int, _CE_BWD + [POINTER(mhc_linear_launch)]),
+    "mhc_cross_entropy_validate_grads": (c_int, _CE_BWD + [POINTER(mhc_linear_launch)]),
+}
+
 MHC_POST_ABI_VERSION = 1
 
 # Every symbol include/mhc_post.h declares.
@@ -286,6 +311,14 @@ def gated_lib() -> ctypes.CDLL:
                 MHC_GATED_ABI_VERSION)
 
 
+def cross_entropy_lib() -> ctypes.CDLL:
+    """The cross entropy library (loaded once). ImportError if missing or
+    stale."""
+    return _get("cross_entropy", CROSS_ENTROPY_LIB_PATH, CROSS_ENTROPY_SRC,
+                CROSS_ENTROPY_SIGNATURES, "mhc_cross_entropy_abi_version",
+                MHC_CROSS_ENTROPY_ABI_VERSION)
+
+
 def post_lib() -> ctypes.CDLL:
     """The write-back library (loaded once). ImportError if missing or stale."""
     return _get("post", POST_LIB_PATH, POST_SRC, POST_SIGNATURES, "mhc_post_abi_version",
@@ -330,6 +363,11 @@ def check_linear(status: int) -> None:
 def check_gated(status: int) -> None:
     if status != MHC_SUCCESS:
         raise MhcError(status, gated_lib().mhc_gated_last_error_message().decode())
+
+
+def check_cross_entropy(status: int) -> None:
+    if status != MHC_SUCCESS:
+        raise MhcError(status, cross_entropy_lib().mhc_cross_entropy_last_error_message().decode())
 
 
 def check_post(status: int) -> None:

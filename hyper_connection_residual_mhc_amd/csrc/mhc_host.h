@@ -94,7 +94,7 @@ mhc_status launch_status(hipError_t e, const char* what) {
 }
 
 // A call with no work: both events, where given, with nothing between them.
-mhc_status record_empty(void* stream, void* start, void* stop) {
+[[maybe_unused]] mhc_status record_empty(void* stream, void* start, void* stop) {
   hipError_t e = hipSuccess;
   if (start != nullptr)
     e = hipEventRecord(static_cast<hipEvent_t>(start), static_cast<hipStream_t>(stream));

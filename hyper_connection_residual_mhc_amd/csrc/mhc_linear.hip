@@ -19,7 +19,7 @@ namespace {
 // Epilogue: scales, bias, activation and residual.
 struct Epilogue {
   static constexpr int kW = kOne, kSums = 1;
-  static constexpr bool kHalves = false, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
   const void* bias;
   const void* residual;
   void* out;

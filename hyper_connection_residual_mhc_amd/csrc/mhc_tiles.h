@@ -235,6 +235,7 @@ struct TileShape {
 
 // E, the epilogue, says
 //   kW       what W is (kOne, kBoth, kChain), kSums how many sums an output has;
+//   kSplits  whether sums come in parts, which another kernel joins;
 //   kHalves  two products in one launch: x (turned) is two blocks of M columns, and
 //            the rows of the second one's results come after the M of the first;
 //   kTakes   e.take() has the sums in their registers first;
@@ -597,7 +598,7 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
         }
       }
     };
-    if (a.splits > 1) {
+    if (E::kSplits && a.splits > 1) {
       const int64_t rows = E::kHalves ? 2 * a.M : a.M;
       float* partial = a.partial + static_cast<int64_t>(at.part) * kSums * rows * a.N;
       each([&](int64_t m, int64_t n, int count, float(&v)[8 * kSums]) {
@@ -622,8 +623,8 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
 template <int OP, int BM, int BN, int WM, int WN, int SIZE, class E>
 __device__ __forceinline__ void end_tile(const TileArgs<E>& a, const Place& at, uint8_t* lds,
                                          f32x4 (&acc)[BM / WM / 16][BN / WN / 16]) {
-  if constexpr (E::kTakes)
-    if (a.splits == 1) a.e.template take<OP, BM / WM / 16, BN / WN / 16, WN>(a, at, acc);
+  static_assert(!E::kTakes || !E::kSplits, "whole sums");
+  if constexpr (E::kTakes) a.e.template take<OP, BM / WM / 16, BN / WN / 16, WN>(a, at, acc);
   if constexpr (E::kWrites) write_tile<OP, BM, BN, WM, WN, SIZE>(a, at, lds, acc);
 }
 
@@ -1216,7 +1217,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs<E> a) 
 template <int W, bool HALVES>
 struct StoreEpilogue {
   static constexpr int kW = W, kSums = 1;
-  static constexpr bool kHalves = HALVES, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = true, kHalves = HALVES, kTakes = false, kWrites = true;
   void* out;
   void* out2;
   int64_t M, N;

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void linear_pad_kernel(PadJob a, PadJob b, Pad
 // Host side: sizes and the choice of a launch
 // ---------------------------------------------------------------------------
 
-bool known_dtype(int32_t d) {
+[[maybe_unused]] bool known_dtype(int32_t d) {
   return (d >= MHC_LINEAR_BF16 && d <= MHC_LINEAR_E4M3_MX) || d == MHC_LINEAR_I8_ROW;
 }
 int64_t elem(int32_t dtype) { return is8(dtype) ? 1 : 2; }
@@ -239,8 +239,8 @@ hipError_t launch_large(TileArgs<E> a, hipStream_t s, hipEvent_t start, hipEvent
   return launch_kernel(linear_large_kernel<OP, TX, TW, E>, grid, dim3(512), s, start, stop, a);
 }
 
-// One product and its epilogue, as planned. The backward's products (TW) and
-// those of two weights have no narrow form.
+// One product and its epilogue, as planned. The backward's products (TW), those
+// of two weights and those that are never split have no narrow form.
 template <int OP, bool TX, bool TW, class E>
 hipError_t launch_product(TileArgs<E> a, const mhc_linear_launch& plan, hipStream_t s,
                           hipEvent_t start, hipEvent_t stop) {
@@ -252,7 +252,7 @@ hipError_t launch_product(TileArgs<E> a, const mhc_linear_launch& plan, hipStrea
   hipError_t e;
   switch (plan.kernel) {
     case MHC_LINEAR_NARROW:
-      if constexpr (!TW && E::kW == kOne) {
+      if constexpr (!TW && E::kW == kOne && E::kSplits) {
         e = launch_tile<OP, 64, 32, 4, 1, 3, TX, TW>(a, s, start, end);
         break;
       }
@@ -260,11 +260,14 @@ hipError_t launch_product(TileArgs<E> a, const mhc_linear_launch& plan, hipStrea
     case MHC_LINEAR_MEDIUM: e = launch_medium<OP, TX, TW>(a, s, start, end); break;
     default: e = launch_large<OP, TX, TW>(a, s, start, end); break;
   }
-  if (e != hipSuccess || !join) return e;
-  const int64_t rows = E::kHalves ? 2 * a.M : a.M;
-  const int64_t blocks = ceil_div(rows * ceil_div(a.N, 8), kJoinThreads);
-  return launch_kernel(linear_join_kernel<OP, E>, dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
-                       dim3(kJoinThreads), s, nullptr, stop, a.partial, a.splits, rows, a.N, a.e);
+  if constexpr (E::kSplits) {
+    if (e != hipSuccess || !join) return e;
+    const int64_t rows = E::kHalves ? 2 * a.M : a.M;
+    const int64_t blocks = ceil_div(rows * ceil_div(a.N, 8), kJoinThreads);
+    return launch_kernel(linear_join_kernel<OP, E>, dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
+                         dim3(kJoinThreads), s, nullptr, stop, a.partial, a.splits, rows, a.N, a.e);
+  }
+  return e;
 }
 
 template <int OP, class E>
