@@ -145,6 +145,7 @@ MHC_LINEAR_MAX_K = 1 << 21
 MHC_LINEAR_MAX_K_I8 = 131071
 MHC_LINEAR_ROWS, MHC_LINEAR_NARROW, MHC_LINEAR_SMALL, MHC_LINEAR_MEDIUM, MHC_LINEAR_LARGE = \
     1, 2, 3, 4, 5
+MHC_LINEAR_SHORT = 7
 
 
 class mhc_linear_launch(ctypes.Structure):

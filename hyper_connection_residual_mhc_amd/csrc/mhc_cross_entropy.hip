@@ -26,12 +26,20 @@ __device__ __forceinline__ float exp_of(float a, float b) {
   return __builtin_amdgcn_exp2f(d * kLog2E);
 }
 
-// The 16-bit values that the workspace holds of a probability (at most 1) are
-// scaled by this, so that fp16 holds what is 2^-29 of the largest as a normal
-// number; bf16 has fp32's range.
-template <int F>
-constexpr float held_scale() {
-  return F == kF16 ? 32768.0f : 1.0f;
+// The exponentials that the workspace holds between the logits and G are fp16, of
+// either type of x: they are at most 1, and fp16's rounding is an eighth of bf16's,
+// which G then adds (in bf16 the gradients at 4096 x 131072 x 4096 were 0.0027 off by
+// the norm, so REPLACE; the output's own rounding is 0.0017). Scaled by this,
+// what is 2^-29 of a group's largest is a normal number, and what is below 2^-40 of
+// it counts as 0.
+constexpr float kHeld = 32768.0f;
+
+__device__ __forceinline__ void hold(uint16_t* held, int64_t ld, int64_t m, int64_t n, int count, float (&v)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * kHeld;
+  Chunk<kF16> c;
+  narrow_chunk<kF16>(v, c);
+  store_chunk<kF16>(held + m * ld + n, count, c);
 }
 
 // Sum s of exp(z - m) over some columns, m the largest z: what the next wave's,
@@ -39,6 +47,18 @@ constexpr float held_scale() {
 struct Stat {
   float m, s;
 };
+
+// Several at once: one exponential each, and one for what was there.
+template <int K>
+__device__ __forceinline__ Stat join_all(const Stat& a, const Stat (&b)[K]) {
+  float m = a.m;
+#pragma unroll
+  for (int k = 0; k < K; ++k) m = fmaxf(m, b[k].m);
+  float s = a.s * exp_of(a.m, m);
+#pragma unroll
+  for (int k = 0; k < K; ++k) s = s + b[k].s * exp_of(b[k].m, m);
+  return {m, s};
+}
 
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
@@ -60,15 +80,16 @@ struct Share {
 // written in 16 bits: a later pass only has to scale them.
 // ---------------------------------------------------------------------------
 
-// Epilogue of the tile kernels. Groups of columns are a wave's.
+// Epilogue of the tile kernels. Groups of columns are a wave's; their statistics
+// lie [groups][rows], since a wave writes those of 16 rows.
 template <bool HOLD>
 struct StatEpilogue {
   static constexpr int kW = kOne, kSums = 1;
   static constexpr bool kSplits = false, kHalves = false, kTakes = true, kWrites = HOLD;
-  Stat* stats;             // [groups][rows]
+  Stat* stats;
   float* target_logit;     // [rows]: written where a target is among the columns
   const int64_t* targets;  // [rows]
-  void* held;              // [rows][ld], 16 bits
+  uint16_t* held;          // [rows][ld]
   int64_t ld;
 
   // Lane l holds in acc[i][0..TJ) 4 TJ consecutive columns of row 16 i + l % 16 of
@@ -145,19 +166,11 @@ struct StatEpilogue {
   // The held exponentials, from take().
   template <int OP, class Fn>
   __device__ __forceinline__ void with(const Fn& fn) const {
-    constexpr int F = out_format(OP);
-    typedef typename Store<F>::type S;
-    fn([&](int64_t m, int64_t n, int count, float(&v)[8]) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * held_scale<F>();
-      Chunk<F> c;
-      narrow_chunk<F>(v, c);
-      store_chunk<F>(static_cast<S*>(held) + m * ld + n, count, c);
-    });
+    fn([&](int64_t m, int64_t n, int count, float(&v)[8]) { hold(held, ld, m, n, count, v); });
   }
 };
 
-// The same of the row kernel: groups are a thread's 8 columns.
+// The same of the row kernel: groups are a thread's 8 columns, [rows][groups].
 template <bool HOLD>
 struct RowStatEpilogue {
   static constexpr int kW = kOne, kSums = 1;
@@ -165,13 +178,11 @@ struct RowStatEpilogue {
   Stat* stats;
   float* target_logit;
   const int64_t* targets;
-  void* held;
-  int64_t ld, M;
+  uint16_t* held;
+  int64_t ld, groups;
 
   template <int OP, class Fn>
   __device__ __forceinline__ void with(const Fn& fn) const {
-    constexpr int F = out_format(OP);
-    typedef typename Store<F>::type S;
     fn([&](int64_t m, int64_t n, int count, float(&v)[8]) {
       const int64_t t = targets[m] - n;
 #pragma unroll
@@ -189,14 +200,8 @@ struct RowStatEpilogue {
         v[e] = exp_of(v[e], top);
         s = s + v[e];
       }
-      stats[n / 8 * M + m] = {top, s};
-      if constexpr (HOLD) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = v[e] * held_scale<F>();
-        Chunk<F> c;
-        narrow_chunk<F>(v, c);
-        store_chunk<F>(static_cast<S*>(held) + m * ld + n, count, c);
-      }
+      stats[m * groups + n / 8] = {top, s};
+      if constexpr (HOLD) hold(held, ld, m, n, count, v);
     });
   }
 };
@@ -239,23 +244,32 @@ struct GradEpilogue {
 
 // lse and the loss of each row from its groups: R rows to a block of 1024 threads,
 // 1024 / R of them to a row, each over every (1024 / R)-th group in ascending
-// order, joined by halving. R is 16 (a group's 16 rows are one 128-byte line), or
-// less for fewer rows.
+// order, eight at a time, joined by halving. R is 16 where there are rows for all
+// CUs (a group's 16 rows are one 128-byte line), and less for fewer rows, which
+// need their groups' latency spread over more threads: 8 rows x 8192 groups 14.6 us
+// with 8 rows to a block, REPLACE with one.
 template <int R>
 __global__ __launch_bounds__(1024) void ce_lse_kernel(const Stat* __restrict__ stats,
                                                       const float* __restrict__ target_logit,
                                                       const int64_t* __restrict__ targets,
                                                       float* __restrict__ lse, float* __restrict__ loss,
-                                                      int64_t M, int64_t V, int64_t groups,
-                                                      int64_t ignore_index) {
+                                                      int64_t M, int64_t V, int64_t groups, int64_t up,
+                                                      int64_t along, int64_t ignore_index) {
   constexpr int kEach = 1024 / R;
   __shared__ Stat part[1024];
   const int64_t row = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x % R;
   const int k = threadIdx.x / R;
   Stat all = {-INFINITY, 0.0f};
   if (row < M) {
-#pragma unroll 8
-    for (int64_t p = k; p < groups; p += kEach) all = join(all, stats[p * M + row]);
+    for (int64_t p = k; p < groups; p += 8 * kEach) {
+      Stat some[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t at = p + i * kEach;
+        some[i] = at < groups ? stats[at * along + row * up] : Stat{-INFINITY, 0.0f};
+      }
+      all = join_all(all, some);
+    }
   }
   part[threadIdx.x] = all;
   __syncthreads();
@@ -346,11 +360,11 @@ template <int F>
 __global__ __launch_bounds__(256) void ce_grad_kernel(
     const Stat* __restrict__ stats, const float* __restrict__ lse, const Share* __restrict__ shares,
     const int64_t* __restrict__ targets, typename Store<F>::type* __restrict__ held, int64_t M,
-    int64_t V, int64_t ld, int64_t segment, int group_bits) {
+    int64_t V, int64_t ld, int64_t segment, int group_bits, int64_t up, int64_t along) {
   const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + threadIdx.x / 16;
   if (row >= M) return;
   const Share w = shares[row];
-  const float l = lse[row], a = w.a * (1.0f / held_scale<F>());
+  const float l = lse[row], a = w.a * (1.0f / kHeld);
   const int64_t t = targets[row];
   const bool none = w.a == 0.0f && w.b == 0.0f;
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * segment + threadIdx.x % 16 * 8;
@@ -359,8 +373,8 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(
   for (int64_t n = begin; n < end; n += 128) {
     typename Store<F>::type* const p = held + row * ld + n;
     float v[8];
-    widen_chunk<F>(load_chunk<F>(p, 8), v);
-    const float f = exp_of(stats[(n >> group_bits) * M + row].m, l) * a;
+    widen_chunk<kF16>(load_chunk<kF16>(p, 8), v);
+    const float f = exp_of(stats[(n >> group_bits) * along + row * up].m, l) * a;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = v[e] * f;
@@ -452,7 +466,7 @@ struct Plan {
 int64_t chunk_rows(int64_t M, int64_t ld) {
   int64_t most = MHC_CROSS_ENTROPY_CHUNK_BYTES / (ld * 2) / 256 * 256;
   if (most < 256) most = 256;
-  if (most > (1 << 20)) most = 1 << 20;  // a sum's length
+  if (most > (1 << 19)) most = 1 << 19;  // a sum's length, and 16 times a grid's height
   if (M <= most) return M;
   return round_up(ceil_div(M, ceil_div(M, most)), 256);
 }
@@ -465,11 +479,8 @@ mhc_status plan_logits(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
   if (mode == kBwd && launch != nullptr && launch->kernel == MHC_LINEAR_ROWS)
     return fail(MHC_ERROR_INVALID_VALUE, "launch: the backward has no row kernel");
   mhc_linear_launch want = {launch != nullptr ? launch->kernel : 0, 1};
-  const mhc_status st = make_plan(M, V, K, dtype, &want, p);
-  if (st != MHC_SUCCESS) return st;
-  if (p->kernel != MHC_LINEAR_NARROW && (mode != kBwd || p->kernel != MHC_LINEAR_ROWS)) return st;
-  want.kernel = MHC_LINEAR_SMALL;
-  return make_plan(M, V, K, dtype, &want, p);
+  if (mode == kBwd && M <= 16 && want.kernel == 0) want.kernel = MHC_LINEAR_SHORT;
+  return best_plan(M, V, K, dtype, false, 1, &want, p);
 }
 
 mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
@@ -482,7 +493,9 @@ mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
   p.chunk = chunk_rows(M, p.ld);
   if ((st = plan_logits(p.chunk, V, K, dtype, mode, launch, &p.logits)) != MHC_SUCCESS) return st;
   if (M == 0) return ok();
-  p.group_bits = p.logits.kernel == MHC_LINEAR_ROWS ? 3 : p.logits.kernel == MHC_LINEAR_SMALL ? 5 : 6;
+  p.group_bits = p.logits.kernel == MHC_LINEAR_ROWS                                            ? 3
+                 : p.logits.kernel == MHC_LINEAR_SMALL || p.logits.kernel == MHC_LINEAR_SHORT ? 5
+                                                                                              : 6;
   p.groups = ceil_div(V, 1 << p.group_bits);
   p.pad = K % 8 != 0 && (M > INT64_MAX / V / K || M * V * K >= kPadBackward);
   p.ldk = p.pad ? round_up(K * 2, 16) : K * 2;
@@ -505,8 +518,8 @@ mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
     p.piece = INT32_MAX / p.ldk / 256 * 256;
     if (p.piece < 256) p.piece = 256;
     if (p.piece > V) p.piece = V;
-    if (plan_product(p.chunk, K, round_up(p.piece, 8), dtype, &p.px) != MHC_SUCCESS ||
-        plan_product(V, K, p.chunk, dtype, &p.pw) != MHC_SUCCESS)
+    if (best_plan(p.chunk, K, round_up(p.piece, 8), dtype, true, 32, nullptr, &p.px) != MHC_SUCCESS ||
+        best_plan(V, K, p.chunk, dtype, true, 32, nullptr, &p.pw) != MHC_SUCCESS)
       at.total = -1;
     const auto parts = [](int64_t rows, int64_t columns, const mhc_linear_launch& l) {
       return l.splits > 1 ? mul_bytes(mul_bytes(rows, columns, 4), l.splits, 1) : 0;
@@ -631,6 +644,10 @@ hipError_t launch_row_logits(const TileArgs<E>& t, hipStream_t s, hipEvent_t sta
                        dim3(512), s, start, nullptr, a);
 }
 
+// Where the statistics of the next row and of the next group are.
+int64_t up_of(const Plan& p) { return p.logits.kernel == MHC_LINEAR_ROWS ? p.groups : 1; }
+int64_t along_of(const Plan& p, int64_t rows) { return p.logits.kernel == MHC_LINEAR_ROWS ? 1 : rows; }
+
 // The statistics of a chunk's logits, lse and the rows' losses.
 template <int OP, bool HOLD>
 hipError_t launch_stats(const Call& c, const Plan& p, const void* x, const void* w, int64_t row0,
@@ -638,10 +655,10 @@ hipError_t launch_stats(const Call& c, const Plan& p, const void* x, const void*
   Stat* const stats = reinterpret_cast<Stat*>(c.ws + p.stats);
   float* const target = reinterpret_cast<float*>(c.ws + p.target);
   const int64_t* const targets = c.targets + row0;
-  void* const held = HOLD ? c.ws + p.held : nullptr;
+  uint16_t* const held = HOLD ? reinterpret_cast<uint16_t*>(c.ws + p.held) : nullptr;
   hipError_t e;
   if (p.logits.kernel == MHC_LINEAR_ROWS) {
-    const RowStatEpilogue<HOLD> ep = {stats, target, targets, held, p.ld, rows};
+    const RowStatEpilogue<HOLD> ep = {stats, target, targets, held, p.ld, p.groups};
     e = launch_row_logits<OP>(logits_of(c, p, x, w, rows, ep), s, marks->first());
   } else {
     const StatEpilogue<HOLD> ep = {stats, target, targets, held, p.ld};
@@ -652,10 +669,10 @@ hipError_t launch_stats(const Call& c, const Plan& p, const void* x, const void*
   const auto run = [&](auto kernel, int64_t r) {
     return launch_kernel(kernel, dim3(static_cast<uint32_t>(ceil_div(rows, r))), dim3(1024), s, nullptr,
                          nullptr, stats, target, targets, c.lse + row0, loss + row0, rows, c.V,
-                         p.groups, c.ignore_index);
+                         p.groups, up_of(p), along_of(p, rows), c.ignore_index);
   };
-  return rows > 8 ? run(ce_lse_kernel<16>, 16) : rows > 4 ? run(ce_lse_kernel<8>, 8)
-       : rows > 2 ? run(ce_lse_kernel<4>, 4) : rows > 1 ? run(ce_lse_kernel<2>, 2) : run(ce_lse_kernel<1>, 1);
+  return rows >= 4096 ? run(ce_lse_kernel<16>, 16) : rows >= 1024 ? run(ce_lse_kernel<4>, 4)
+                                                   : run(ce_lse_kernel<1>, 1);
 }
 
 template <int OP>
@@ -753,11 +770,13 @@ hipError_t launch_all(const Call& c, const Plan& p, hipStream_t s, hipEvent_t st
       } else {
         e = launch_stats<OP, true>(c, p, xc, w, row0, rows, s, &marks);
         if (e != hipSuccess) return e;
-        constexpr int64_t kSegment = 2048;
-        e = launch_kernel(ce_grad_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(c.V, kSegment)), static_cast<uint32_t>(ceil_div(rows, 16))),
+        // 1 to 16 pieces of 128 columns to a block, by what leaves some 2048 blocks
+        const int64_t high = ceil_div(rows, 16), pieces = ceil_div(c.V, 128) * high / 2048;
+        const int64_t segment = 128 * (pieces < 1 ? 1 : pieces > 16 ? 16 : pieces);
+        e = launch_kernel(ce_grad_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(c.V, segment)), static_cast<uint32_t>(high)),
                           dim3(256), s, nullptr, nullptr, reinterpret_cast<const Stat*>(c.ws + p.stats),
                           c.lse + row0, shares + row0, c.targets + row0, reinterpret_cast<S*>(c.ws + p.held),
-                          rows, c.V, p.ld, kSegment, p.group_bits);
+                          rows, c.V, p.ld, segment, p.group_bits, up_of(p), along_of(p, rows));
       }
     }
     if (e == hipSuccess && grads) e = launch_over_g<OP>(c, p, xc, w, row0, rows, s);

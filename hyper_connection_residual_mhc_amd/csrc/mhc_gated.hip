@@ -170,6 +170,16 @@ __global__ __launch_bounds__(256) void gated_gz_kernel(
   }
 }
 
+// The biases' gradients, of the gate in blockIdx.y 0: the parts' sums, rounded once
+// (see linear_bias_kernel).
+template <int F>
+__global__ __launch_bounds__(256) void gated_bias_kernel(const float* __restrict__ partial,
+                                                         typename Store<F>::type* gate,
+                                                         typename Store<F>::type* up, int64_t parts, int64_t N) {
+  typename Store<F>::type* const out = blockIdx.y == 0 ? gate : up;
+  if (out != nullptr) sum_parts<F>(partial + blockIdx.y * parts * N, out, parts, N);
+}
+
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
@@ -197,10 +207,7 @@ mhc_status plan_gated(int64_t M, int64_t N, int64_t K, int32_t dtype,
                       const mhc_linear_launch* launch, mhc_linear_launch* p) {
   if (launch != nullptr && launch->kernel == MHC_LINEAR_NARROW)
     return fail(MHC_ERROR_INVALID_VALUE, "launch: there is no narrow kernel of two weights");
-  const mhc_status st = make_plan(M, 2 * N, K, dtype, launch, p);
-  if (st != MHC_SUCCESS || p->kernel != MHC_LINEAR_NARROW) return st;
-  const mhc_linear_launch small = {MHC_LINEAR_SMALL, launch != nullptr ? launch->splits : 0};
-  return make_plan(M, 2 * N, K, dtype, &small, p);
+  return best_plan(M, 2 * N, K, dtype, false, 32, launch, p);
 }
 
 struct FwdPlan {
@@ -345,8 +352,8 @@ BwdPlan plan_bwd(int64_t M, int64_t N, int64_t K, int32_t dtype) {
     p.wg = at.take(mul_bytes(N, p.ldk, 1));
     p.wu = at.take(mul_bytes(N, p.ldk, 1));
   }
-  if (plan_product(M, K, 2 * p.half, dtype, &p.px) != MHC_SUCCESS ||
-      plan_product(2 * N, K, M, dtype, &p.pw) != MHC_SUCCESS)
+  if (best_plan(M, K, 2 * p.half, dtype, true, 32, nullptr, &p.px) != MHC_SUCCESS ||
+      best_plan(2 * N, K, M, dtype, true, 32, nullptr, &p.pw) != MHC_SUCCESS)
     at.total = -1;
   const auto parts = [](int64_t rows, int64_t columns, const mhc_linear_launch& l) {
     return l.splits > 1 ? mul_bytes(mul_bytes(rows, columns, 4), l.splits, 1) : 0;
@@ -453,13 +460,11 @@ hipError_t launch_bwd(const BwdArgs& a, int32_t dtype, hipStream_t s, hipEvent_t
       default: e = run(gated_gz_kernel<F, MHC_ACT_NONE>); break;
     }
     if (e != hipSuccess) return e;
-    void* const to[] = {a.ggb, a.gub};
-    for (int k = 0; k < 2; ++k)
-      if (to[k] != nullptr) {
-        e = launch_kernel(linear_bias_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(a.N, 64))), dim3(256),
-                          s, nullptr, nullptr, sums + k * p.parts * a.N, static_cast<S*>(to[k]), p.parts, a.N);
-        if (e != hipSuccess) return e;
-      }
+    if (bias) {
+      e = launch_kernel(gated_bias_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(a.N, 64)), 2), dim3(256),
+                        s, nullptr, nullptr, sums, static_cast<S*>(a.ggb), static_cast<S*>(a.gub), p.parts, a.N);
+      if (e != hipSuccess) return e;
+    }
   }
   if (a.gx != nullptr) {
     // grad_x [M, K]: rows of (dg | du), with Wg and then Wu turned

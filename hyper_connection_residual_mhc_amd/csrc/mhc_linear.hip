@@ -157,6 +157,14 @@ mhc_status check_sizes(int64_t M, int64_t N, int64_t K, int32_t dtype) {
 }
 
 
+// The forward's launch. Sums of 8-bit integers are the same in every launch, so
+// theirs may be the fastest; the narrow kernel has no rival at few columns.
+mhc_status plan_launch(int64_t M, int64_t N, int64_t K, int32_t dtype, const mhc_linear_launch* launch,
+                       mhc_linear_launch* p) {
+  return dtype == MHC_LINEAR_I8_ROW && N > 32 ? best_plan(M, N, K, dtype, false, 32, launch, p)
+                                              : make_plan(M, N, K, dtype, launch, p);
+}
+
 struct FwdPlan {
   mhc_linear_launch launch;
   bool pad;
@@ -197,7 +205,7 @@ mhc_status validate_fwd(const void* x, const void* xs, const void* w, const void
   if (st != MHC_SUCCESS) return st;
   if (act < MHC_ACT_NONE || act > MHC_ACT_GELU)
     return fail(MHC_ERROR_INVALID_VALUE, "unknown activation %d", act);
-  if ((st = make_plan(M, N, K, dtype, launch, &chosen)) != MHC_SUCCESS) return st;
+  if ((st = plan_launch(M, N, K, dtype, launch, &chosen)) != MHC_SUCCESS) return st;
   *plan = plan_fwd(M, N, K, dtype, chosen);
   if (!is8(dtype) && (xs != nullptr || ws != nullptr))
     return fail(MHC_ERROR_INVALID_VALUE, "16-bit operands have no scales");
@@ -433,7 +441,7 @@ mhc_status mhc_linear_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
                            const mhc_linear_launch* launch, mhc_linear_launch* plan) {
   mhc_linear_launch p;
   mhc_status st = check_sizes(M, N, K, dtype);
-  if (st == MHC_SUCCESS) st = make_plan(M, N, K, dtype, launch, &p);
+  if (st == MHC_SUCCESS) st = plan_launch(M, N, K, dtype, launch, &p);
   if (st == MHC_SUCCESS && plan != nullptr) *plan = p;
   return st;
 }
@@ -442,7 +450,7 @@ int64_t mhc_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t 
                                        const mhc_linear_launch* launch) {
   mhc_linear_launch p;
   if (check_sizes(M, N, K, dtype) != MHC_SUCCESS ||
-      make_plan(M, N, K, dtype, launch, &p) != MHC_SUCCESS)
+      plan_launch(M, N, K, dtype, launch, &p) != MHC_SUCCESS)
     return -1;
   return plan_fwd(M, N, K, dtype, p).total;
 }

@@ -20,6 +20,8 @@ namespace {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef f32x8 f32x8_at4 __attribute__((aligned(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -112,6 +114,12 @@ __device__ __forceinline__ float sum_value(float v) {
 template <int OP>
 __device__ __forceinline__ float sum_add(float a, float b) {
   if constexpr (OP == kOpI8) return __int_as_float(__float_as_int(a) + __float_as_int(b));
+  else return a + b;
+}
+
+template <int OP>
+__device__ __forceinline__ f32x8 sums_added(const f32x8& a, const f32x8& b) {
+  if constexpr (OP == kOpI8) return __builtin_bit_cast(f32x8, __builtin_bit_cast(i32x8, a) + __builtin_bit_cast(i32x8, b));
   else return a + b;
 }
 
@@ -660,10 +668,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
   constexpr bool kScales = OP == kOpMX;
   typedef Operand<BM, kThreads, TX, false, 1, DMA, ELEM> OpX;
   typedef Operand<BN, kThreads, TW, true, G, DMA, ELEM, W> OpW;
-  constexpr int kLoads = OpX::Q + OpW::Q + (kScales ? 1 : 0);  // of a wave, for a tile
-  static_assert(!kScales || BM + BN <= kThreads, "a scale load for each row");
+  constexpr int kLoads = OpX::Q + OpW::Q;  // of a wave, for a tile
+  constexpr uint32_t kWavesX = (BM + 63) / 64;  // that bring the scales of x
+  static_assert(!kScales || kWavesX * 64 + BN <= kThreads, "a scale load for each row");
   __shared__ __align__(1024) uint8_t lds[kStages][kBuffer];
-  __shared__ __align__(1024) uint8_t scales[kStages][kScales && DMA ? kThreads * 4 : 16];
+  // kMX, DMA: the scales of four passes, of x's rows and then of W's, twice
+  constexpr uint32_t kScaleRows = kWavesX * 64 + (W == kBoth ? 2 * 64 : (BN + 63) / 64 * 64);
+  __shared__ __align__(1024) uint8_t scales[2][kScales && DMA ? kScaleRows * 16 : 16];
 
   const Place place = place_of<BM, BN / E::kSums, E::kHalves>(a);
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -680,7 +691,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
   rx.init(wm * (TI * 16));
   rw.init(wn * kWaveW);
 
-  // Block scales. DMA: thread r brings the 4 bytes of row r, x's then W's.
+  // Block scales. DMA: thread r brings 16 bytes of row r, x's then W's, which are
+  // those of four passes: a load of 4 bytes for each pass asks the L2 for as many
+  // lines as two thirds of the operands (two weights of 14336 x 7168 and 24 rows REPLACE).
   // Else: each lane the bytes of its own rows; rows past the end read the last
   // row's (their values are zeros), and past the last block of a row any finite
   // scale does (those values are zeros too).
@@ -695,9 +708,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
   sx[0] = sw[0] = 0;
   if constexpr (kScales && DMA) {
     // kBoth: one wave brings a weight's rows
-    const bool of_x = wave < BM / 64, of_2 = W == kBoth && wave == BM / 64 + 1;
+    const bool of_x = wave < kWavesX, of_2 = W == kBoth && wave == kWavesX + 1;
     static_assert(W != kBoth || OpW::kRows <= 64, "a weight's scales are one wave's");
-    const uint32_t r = threadIdx.x - (of_x ? 0 : of_2 ? BM + 64 : BM);
+    const uint32_t r = threadIdx.x - (of_x ? 0 : of_2 ? (kWavesX + 1) * 64 : kWavesX * 64);
     sr = buffer_of(of_x ? xs : of_2 ? ws2 : ws, static_cast<int64_t>(of_x ? lx.here : lw.here) * kblocks);
     if (r < (of_x ? lx.here : lw.here)) so = r * kblocks;
   } else if constexpr (kScales) {
@@ -716,14 +729,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
       for (int j = 0; j < TJ; ++j) nw[j] = in ? (W == kBoth && j >= G ? ws2 : ws)[ow[j] + kt * 4] : 0;
     }
   };
-  const auto take_scales = [&](uint32_t stage) {
+  const auto take_scales = [&](uint32_t kt) {
     if constexpr (kScales && DMA) {
+      const uint8_t* const from = scales[kt / 4 % 2] + kt % 4 * 4 + g;
 #pragma unroll
-      for (int i = 0; i < TI; ++i) sx[i] = scales[stage][rx.row_of(wm * (TI * 16), i) * 4 + g];
+      for (int i = 0; i < TI; ++i) sx[i] = from[rx.row_of(wm * (TI * 16), i) * 16];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
         const uint32_t r = W == kBoth ? rw.row_of(wn * kWaveW, j % G) + (j / G) * 64 : rw.row_of(wn * kWaveW, j);
-        sw[j] = scales[stage][(BM + r) * 4 + g];
+        sw[j] = from[(kWavesX * 64 + r) * 16];
       }
     } else if constexpr (kScales) {
 #pragma unroll
@@ -772,8 +786,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
     for (int q = 0; q < OpX::Q; ++q) lx.start(kt, to, q);
 #pragma unroll
     for (int q = 0; q < OpW::Q; ++q) lw.start(kt, to + BM * kTileK, q);
+    // (a wait for the tile waits for these too: they are one load more, and before it)
     if constexpr (kScales && DMA)
-      load_to_lds<4>(kt < all ? so : kOutside, sr, kt * 4, at1 + stage * (kThreads * 4) + wave * 256);
+      if ((kt % 4 == 0 || kt == first) && wave < kScaleRows / 64)
+        load_to_lds<16>(kt < all ? so : kOutside, sr, kt / 4 * 16, at1 + kt / 4 % 2 * (kScaleRows * 16) + wave * 1024);
   };
   if constexpr (DMA) {
 #pragma unroll
@@ -782,7 +798,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
     for (uint32_t kt = first; kt < last; ++kt) {
       wait_tiles<(kStages - 2) * kLoads>();
       start(kt + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-      take_scales(stage);
+      take_scales(kt);
       multiply(lds[stage]);
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -1024,45 +1040,65 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
 }
 
 // The parts of a split sum, added in ascending order, and the epilogue. One wave
-// to a block and eight parts' loads in flight: 2048 x 24 in 16 parts 6.3 us,
-// four waves and a part at a time 9.9.
+// to a block and AHEAD parts' loads in flight, past the last part the last one's
+// again: a load in a branch of its own waits for the one before it. 2048 x 24 in 16
+// parts 6.3 us, four waves and a part at a time 9.9. WIDE: rows of at least 8
+// columns, whose short last chunk comes from the 8 values that end there, shifted
+// once they are summed (129 x 1279 in four parts 13 -> 4.4 us: element by element
+// it holds up its wave for every part).
 constexpr int kJoinThreads = 64;
 
-template <int OP, class E>
+template <int OP, class E, uint32_t AHEAD, bool WIDE>
 __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(const float* __restrict__ partial,
                                                                    uint32_t splits, int64_t M, int64_t N, E e) {
   constexpr int kSums = E::kSums;
-  const int64_t chunks = (N + 7) / 8;
+  const int64_t chunks = (N + 7) / 8, all = M * chunks;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kJoinThreads;
-  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; id < M * chunks;
-       id += step) {
-    const int64_t m = id / chunks, n = (id - m * chunks) * 8;
+  const int64_t part = kSums * M * N;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x; id < all; id += step) {
+    // a division of 64 bits takes as long as a part's load
+    const int64_t m = all <= 0xFFFFFFFFLL ? static_cast<uint32_t>(id) / static_cast<uint32_t>(chunks) : id / chunks;
+    const int64_t n = (id - m * chunks) * 8;
     const int count = static_cast<int>(min(N - n, static_cast<int64_t>(8)));
-    float all[8 * kSums];
+    const int back = WIDE ? 8 - count : 0;
+    const float* const p = partial + m * N + n - back;
+    f32x8 t[kSums];
+#pragma unroll
+    for (int sum = 0; sum < kSums; ++sum) t[sum] = f32x8{0, 0, 0, 0, 0, 0, 0, 0};
+    for (uint32_t s0 = 0; s0 < splits; s0 += AHEAD) {
+      f32x8 b[AHEAD][kSums];
+#pragma unroll
+      for (uint32_t k = 0; k < AHEAD; ++k)
+#pragma unroll
+        for (int sum = 0; sum < kSums; ++sum) {
+          const float* const q = p + min(s0 + k, splits - 1) * part + sum * M * N;
+          if constexpr (WIDE) {
+            b[k][sum] = *reinterpret_cast<const f32x8_at4*>(q);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[k][sum][i] = q[min(i, count - 1)];
+          }
+        }
+#pragma unroll
+      for (uint32_t k = 0; k < AHEAD; ++k)
+        if (s0 + k < splits) {
+#pragma unroll
+          for (int sum = 0; sum < kSums; ++sum) t[sum] = s0 + k == 0 ? b[k][sum] : sums_added<OP>(t[sum], b[k][sum]);
+        }
+    }
+    float v[8 * kSums];
 #pragma unroll
     for (int sum = 0; sum < kSums; ++sum) {
-      const float* p = partial + (sum * M + m) * N + n;
-      float v[8], b[8];
-      widen_chunk<kF32>(load_chunk<kF32>(p, count), v);
-      if (count == 8) {
-#pragma unroll 8
-        for (uint32_t s = 1; s < splits; ++s) {
-          widen_chunk<kF32>(load_chunk<kF32>(p + s * kSums * M * N, 8), b);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = sum_add<OP>(v[i], b[i]);
-        }
-      } else {
-#pragma unroll 4
-        for (uint32_t s = 1; s < splits; ++s) {
-          widen_chunk<kF32>(load_chunk<kF32>(p + s * kSums * M * N, count), b);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = sum_add<OP>(v[i], b[i]);
-        }
+      f32x8 u = t[sum];
+      if constexpr (WIDE) {
+        u = (back & 4) != 0 ? __builtin_shufflevector(u, u, 4, 5, 6, 7, 4, 5, 6, 7) : u;
+        u = (back & 2) != 0 ? __builtin_shufflevector(u, u, 2, 3, 4, 5, 6, 7, 6, 7) : u;
+        u = (back & 1) != 0 ? __builtin_shufflevector(u, u, 1, 2, 3, 4, 5, 6, 7, 7) : u;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) all[8 * sum + i] = v[i];
+      for (int i = 0; i < 8; ++i) v[8 * sum + i] = u[i];
     }
-    e.template with<OP>([&](const auto& finish) { finish(m, n, count, all); });
+    e.template with<OP>([&](const auto& finish) { finish(m, n, count, v); });
   }
 }
 
@@ -1236,12 +1272,11 @@ struct StoreEpilogue {
   }
 };
 
-// grad_bias[n] = the parts' sum, rounded once (+0.0 of none): 64 columns to a
-// block, each of four waves every fourth part, joined in ascending order.
+// out[n] = the parts' sum, rounded once (+0.0 of none): 64 columns to a block,
+// each of four waves every fourth part, joined in ascending order.
 template <int F>
-__global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ partial,
-                                                          typename Store<F>::type* __restrict__ out,
-                                                          int64_t parts, int64_t N) {
+__device__ __forceinline__ void sum_parts(const float* __restrict__ partial,
+                                          typename Store<F>::type* __restrict__ out, int64_t parts, int64_t N) {
   __shared__ float sums[4][64];
   const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 64 + lane;
@@ -1254,6 +1289,13 @@ __global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restric
   __syncthreads();
   if (wave == 0 && n < N)
     out[n] = narrow<F>(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane]);
+}
+
+template <int F>
+__global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ partial,
+                                                          typename Store<F>::type* __restrict__ out,
+                                                          int64_t parts, int64_t N) {
+  sum_parts<F>(partial, out, parts, N);
 }
 
 __global__ __launch_bounds__(256) void linear_zero_kernel(uint16_t* __restrict__ p, int64_t count) {

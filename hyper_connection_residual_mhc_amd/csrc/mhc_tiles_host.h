@@ -3,6 +3,8 @@
 
 #pragma once
 
+#include <math.h>
+
 #include "mhc_host.h"
 #include "mhc_launch.h"
 #include "mhc_tiles.h"
@@ -88,6 +90,7 @@ struct Shape {
 
 Shape shape_of(int32_t kernel) {
   switch (kernel) {
+    case MHC_LINEAR_SHORT: return {32, 64};
     case MHC_LINEAR_NARROW: return {64, 32};
     case MHC_LINEAR_SMALL: return {64, 64};
     case MHC_LINEAR_MEDIUM: return {128, 128};
@@ -107,7 +110,7 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
                      const mhc_linear_launch* launch, mhc_linear_launch* plan) {
   const int32_t want = launch != nullptr ? launch->kernel : 0;
   const int32_t parts = launch != nullptr ? launch->splits : 0;
-  if (want < 0 || want > MHC_LINEAR_LARGE || parts < 0 || parts > kMaxSplits)
+  if (want < 0 || (want > MHC_LINEAR_LARGE && want != MHC_LINEAR_SHORT) || parts < 0 || parts > kMaxSplits)
     return fail(MHC_ERROR_INVALID_VALUE, "launch: kernel %d with %d splits does not exist", want,
                 parts);
   const auto tiles = [&](int32_t k) {
@@ -148,7 +151,7 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
     // 2048 x 24 x 28672 in 16 parts of 32 narrow tiles 29.3, in eight 31. More than 32 parts cost the join
     // more than they save: 17 x 24 x 28672 in 32 13.7, in 64 15.4
     s = 1;
-    const int64_t slots = k >= MHC_LINEAR_MEDIUM ? 256 : 512;
+    const int64_t slots = k == MHC_LINEAR_MEDIUM || k == MHC_LINEAR_LARGE ? 256 : 512;
     while (s < 32 && M > 0 && tiles(k) * s * 2 <= slots && all / (s * 2) >= 4) s *= 2;
   }
   if (s > all) s = all;
@@ -156,6 +159,57 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
   s = ceil_div(all, ceil_div(all, s));
   *plan = {k, static_cast<int32_t>(s)};
   return ok();
+}
+
+// The launch that takes the least time by a model, for the calls whose sums have no
+// older order to keep: products of two weights, those of 8-bit integers (exact in
+// any order) and those around a softmax. In us, a kernel takes `pass` for each pass
+// of kTileK bytes while every CU has at most one block of it, and a CU with more
+// works one off in `busy`; a tile's end takes `end`, a launch 3, and joining s parts 3.5
+// and their bytes' way to memory and back. The constants are fitted to 8-bit and bf16
+// products of 17 to 4096 rows x 1024 to 28672 x 512 to 28672; of 110 of them this takes
+// the fastest launch or one within REPLACE of it. 8-bit integers, the rule above
+// and this one: 32 x 7168 x 4096 12.5 -> 9.8 us (small tiles in 4 parts, short ones in
+// one), 256 x 4096 x 7168 21.9 -> 18.2, 1024 x 1024 x 4096 16.4 -> 11.9; two weights of
+// 14336 x 7168 in bf16 and 24 rows 117 -> 74 (medium tiles, short ones).
+struct Cost {
+  int32_t kernel;
+  double pass, busy, end;
+};
+constexpr Cost kCosts[] = {{MHC_LINEAR_SHORT, 0.21, 0.143, 0.4},
+                           {MHC_LINEAR_SMALL, 0.30, 0.197, 0.65},
+                           {MHC_LINEAR_MEDIUM, 0.75, 0.54, 2.7},
+                           {MHC_LINEAR_LARGE, 1.5, 1.5, 12.0}};
+
+// turned: operands with k down the rows, which have no short form. most: parts.
+mhc_status best_plan(int64_t M, int64_t N, int64_t K, int32_t dtype, bool turned, int32_t most,
+                     const mhc_linear_launch* launch, mhc_linear_launch* plan) {
+  mhc_linear_launch want = {0, most == 1 ? 1 : launch != nullptr ? launch->splits : 0};
+  if (launch != nullptr && launch->kernel != 0) want.kernel = launch->kernel;
+  if (want.kernel != 0 || M == 0 || (M <= 16 && !turned)) return make_plan(M, N, K, dtype, &want, plan);
+  const int64_t all = ceil_div(K * elem(dtype), kTileK);
+  double least = INFINITY;
+  mhc_linear_launch best = {MHC_LINEAR_SMALL, 1};
+  for (const Cost& c : kCosts) {
+    if (turned && c.kernel == MHC_LINEAR_SHORT) continue;
+    const Shape shape = shape_of(c.kernel);
+    const double tiles = static_cast<double>(ceil_div(M, shape.bm)) * static_cast<double>(ceil_div(N, shape.bn));
+    for (int32_t s = 1; s <= 32; s *= 2) {
+      if (want.splits != 0 ? s != 1 : s > 1 && (s > most || all / s < 4 || tiles * s > 1024)) break;
+      const double parts = want.splits != 0 ? want.splits : s;
+      double each = tiles * parts / 256;  // blocks of a CU
+      if (c.kernel == MHC_LINEAR_LARGE) each = ceil(each);
+      if (each < 1) each = 1;
+      const double passes = ceil(static_cast<double>(all) / parts);
+      double t = 3 + passes * fmax(c.pass, each * c.busy) + each * c.end;
+      if (parts > 1) t += 3.5 + parts * static_cast<double>(M) * static_cast<double>(N) * 8 / 4e6;
+      if (t < least) {
+        least = t;
+        best = {c.kernel, static_cast<int32_t>(parts)};
+      }
+    }
+  }
+  return make_plan(M, N, K, dtype, &best, plan);
 }
 
 int64_t round_up(int64_t v, int64_t to) { return ceil_div(v, to) * to; }
@@ -256,6 +310,11 @@ hipError_t launch_product(TileArgs<E> a, const mhc_linear_launch& plan, hipStrea
         e = launch_tile<OP, 64, 32, 4, 1, 3, TX, TW>(a, s, start, end);
         break;
       }
+    case MHC_LINEAR_SHORT:
+      if constexpr (!TW) {
+        e = launch_tile<OP, 32, 64, 2, 2, 4, TX, TW>(a, s, start, end);
+        break;
+      }
     case MHC_LINEAR_SMALL: e = launch_tile<OP, 64, 64, 2, 2, 3, TX, TW>(a, s, start, end); break;
     case MHC_LINEAR_MEDIUM: e = launch_medium<OP, TX, TW>(a, s, start, end); break;
     default: e = launch_large<OP, TX, TW>(a, s, start, end); break;
@@ -264,8 +323,12 @@ hipError_t launch_product(TileArgs<E> a, const mhc_linear_launch& plan, hipStrea
     if (e != hipSuccess || !join) return e;
     const int64_t rows = E::kHalves ? 2 * a.M : a.M;
     const int64_t blocks = ceil_div(rows * ceil_div(a.N, 8), kJoinThreads);
-    return launch_kernel(linear_join_kernel<OP, E>, dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
-                         dim3(kJoinThreads), s, nullptr, stop, a.partial, a.splits, rows, a.N, a.e);
+    const auto run = [&](auto kernel) {
+      return launch_kernel(kernel, dim3(static_cast<uint32_t>(blocks < 16384 ? blocks : 16384)),
+                           dim3(kJoinThreads), s, nullptr, stop, a.partial, a.splits, rows, a.N, a.e);
+    };
+    if (a.N < 8) return run(linear_join_kernel<OP, E, 4, false>);
+    return a.splits <= 4 ? run(linear_join_kernel<OP, E, 4, true>) : run(linear_join_kernel<OP, E, 8 / E::kSums, true>);
   }
   return e;
 }
@@ -298,7 +361,7 @@ hipError_t launch_pad(const PadJobs& jobs, int count, hipStream_t s, hipEvent_t 
 }
 
 // A product of the backward: the tile kernels from 64 x 64 on.
-mhc_status plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, mhc_linear_launch* p) {
+[[maybe_unused]] mhc_status plan_product(int64_t M, int64_t N, int64_t K, int32_t dtype, mhc_linear_launch* p) {
   const mhc_status st = make_plan(M, N, K, dtype, nullptr, p);
   if (st != MHC_SUCCESS || p->kernel >= MHC_LINEAR_SMALL) return st;
   const mhc_linear_launch small = {MHC_LINEAR_SMALL, 0};

@@ -33,7 +33,8 @@
  * G += grad_lse[m] exp(z - lse), for ignored rows too. mhc_cross_entropy_grads gives loss, lse and
  * gradients in one call, for callers that know grad_loss beforehand, and makes
  * the logits once: of a chunk of rows at a time it keeps exp(z - the largest of
- * 64 neighbours), rounded to 16 bits, in the workspace. Chunks of rows hold at
+ * 64 neighbours), rounded to fp16, in the workspace (what is below 2^-40 of that
+ * largest counts as 0). Chunks of rows hold at
  * most MHC_CROSS_ENTROPY_CHUNK_BYTES of such values (256 rows at least).
  *
  * The order of a sum depends on M, V, K, the type and the launch shape, on

@@ -97,6 +97,7 @@ extern "C" {
 #define MHC_LINEAR_SMALL 3   /* tiles of 64 x 64 */
 #define MHC_LINEAR_MEDIUM 4  /* tiles of 128 x 128 */
 #define MHC_LINEAR_LARGE 5   /* tiles of 256 x 256 */
+#define MHC_LINEAR_SHORT 7   /* tiles of 32 x 64; 6 is no kernel */
 
 /* Launch shape: kernel and the number of parts that the sum over k is split
  * into (tile kernels: 1..64; parts are joined in ascending order by a second

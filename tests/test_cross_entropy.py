@@ -10,9 +10,9 @@ the joins of the groups of a thread, in the halving over at most 1024 threads)
 costs at most 8 u of the sum, which is what lse sees. The logarithm and the
 additions cost 4 u of their values.
 A probability p made again from z and lse is off by dz + dlse + (|z - lse| + 2) 4 u
-of itself; one that was held in 16 bits under its group's maximum also by half a
-step, or next to zero by half of the smallest number of the type (in fp16 over
-2^15); what is below 2^-126 may count as 0. G is rounded (in fp16 after scaling its
+of itself; one that was held in fp16 under its group's maximum also by half a step
+of fp16, or next to zero by half of fp16's smallest number over 2^15; what is below
+2^-126 may count as 0. G is rounded (in fp16 after scaling its
 largest share to 2^14 at least), and the products over it see that in full.
 """
 
@@ -250,14 +250,13 @@ def check_grads(gx, gw, x, w, targets, s, z, lse, dz, dlse, t, held, group=64, g
     a = (s if grad_lse is None else s + grad_lse).abs()
     rel = dz + dlse[:, None] + ((z - lse[:, None]).abs() + 2) * 4 * U
     dp = p * rel + 2.0 ** -126
-    narrow = 2.0 ** -14 if t == F16 else 1.0
     if held:
         top = torch.nn.functional.pad(p, (0, -V % group)).view(len(p), -1, group).amax(2).repeat_interleave(group, 1)[:, :V]
-        dp = dp + p * (1 + rel) * R.HALF_STEP[t] + top * R.HALF_TINY[t] * narrow
+        dp = dp + p * (1 + rel) * R.HALF_STEP[F16] + top * R.HALF_TINY[F16] * 2.0 ** -14
         dp = dp + p * ((top.clamp_min(1e-300).log()).abs() + 2) * 4 * U
     largest = torch.maximum(a, s.abs()).max()
     dg = a[:, None] * dp + (g.abs() + a[:, None] * p) * 4 * U
-    dg = dg + (g.abs() + dg) * R.HALF_STEP[t] + R.HALF_TINY[t] * (largest * narrow if t == F16 else 1.0)
+    dg = dg + (g.abs() + dg) * R.HALF_STEP[t] + R.HALF_TINY[t] * (largest * 2.0 ** -14 if t == F16 else 1.0)
     dg = torch.where((a == 0)[:, None] & (s == 0)[:, None], torch.zeros_like(dg), dg)
     ag = g.abs() + dg
     for got, want, tol, long, name in (

@@ -143,7 +143,7 @@ def test_launches(lib):
     with pytest.raises(_lib.MhcError):
         G.mhc_gated_plan(17, 64, 64, 1, {"kernel": ROWS})
     assert G.mhc_gated_plan(16, 4096, 4096, 1) == {"kernel": ROWS, "splits": 1}
-    assert G.mhc_gated_plan(100, 8, 64, 1)["kernel"] == SMALL            # there is no narrow form
+    assert G.mhc_gated_plan(100, 8, 64, 1)["kernel"] not in (NARROW, ROWS)  # there is no narrow form
     assert G.mhc_gated_plan(4096, 8192, 4096, 1) == {"kernel": LARGE, "splits": 1}
     for kernel in (SMALL, MEDIUM, LARGE):
         p = G.mhc_gated_plan(100, 50, 4096, 1, {"kernel": kernel, "splits": 3})
