@@ -16,7 +16,7 @@
 
 namespace {
 
-constexpr float kLog2E = 1.44269504f;
+constexpr float kLog2E = 1.44269504f, kLn2 = 0.69314718f;
 
 // exp(a - b), 1 where they are the same infinity. The difference comes before
 // the product with log2(e): rounding a log2(e) and b log2(e) apart would put an
@@ -26,43 +26,41 @@ __device__ __forceinline__ float exp_of(float a, float b) {
   return __builtin_amdgcn_exp2f(d * kLog2E);
 }
 
-// The exponentials that the workspace holds between the logits and G are fp16, of
-// either type of x: they are at most 1, and fp16's rounding is an eighth of bf16's,
-// which G then adds (in bf16 the gradients at 4096 x 131072 x 4096 were 0.0027 off by
-// the norm, so REPLACE; the output's own rounding is 0.0017). Scaled by this,
-// what is 2^-29 of a group's largest is a normal number, and what is below 2^-40 of
-// it counts as 0.
-constexpr float kHeld = 32768.0f;
-
-__device__ __forceinline__ void hold(uint16_t* held, int64_t ld, int64_t m, int64_t n, int count, float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = v[e] * kHeld;
-  Chunk<kF16> c;
-  narrow_chunk<kF16>(v, c);
-  store_chunk<kF16>(held + m * ld + n, count, c);
+// 2^(a - b), 1 where they are the same infinity.
+__device__ __forceinline__ float exp2_of(float a, float b) {
+  return __builtin_amdgcn_exp2f(a == b ? 0.0f : a - b);
 }
 
-// Sum s of exp(z - m) over some columns, m the largest z: what the next wave's,
-// tile's or group's are joined to.
+// A group of columns: s is the sum of 2^(z log2(e) - m), with m 15 below the
+// largest z log2(e). Everything up to lse stays in powers of two, where a term is one
+// fused multiply-add and one exponential whatever m was rounded to; log2(e)'s own
+// rounding scales all logits alike and moves lse by 2^-25 of the row's entropy.
 struct Stat {
   float m, s;
 };
 
-// Several at once: one exponential each, and one for what was there.
+// The exponentials that the workspace holds between the logits and G are those
+// terms, at most 2^15, in fp16, of either type of x: fp16's rounding is an eighth of
+// bf16's, which G then adds (held in bf16 the gradients at 4096 x 131072 x 4096 were
+// 0.0027 off by the norm, so 0.0024; the output's own rounding is 0.0017). What is 2^-29
+// of a group's largest is a normal number, and what is below 2^-40 of it counts as 0.
+constexpr float kHeld = 15.0f;
+
+// Several groups at once: one exponential each, and one for what was there.
 template <int K>
 __device__ __forceinline__ Stat join_all(const Stat& a, const Stat (&b)[K]) {
   float m = a.m;
 #pragma unroll
   for (int k = 0; k < K; ++k) m = fmaxf(m, b[k].m);
-  float s = a.s * exp_of(a.m, m);
+  float s = a.s * exp2_of(a.m, m);
 #pragma unroll
-  for (int k = 0; k < K; ++k) s = s + b[k].s * exp_of(b[k].m, m);
+  for (int k = 0; k < K; ++k) s = s + b[k].s * exp2_of(b[k].m, m);
   return {m, s};
 }
 
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
-  return {m, a.s * exp_of(a.m, m) + b.s * exp_of(b.m, m)};
+  return {m, a.s * exp2_of(a.m, m) + b.s * exp2_of(b.m, m)};
 }
 
 // What of its row's gradient a probability (a) and the target's place (b) get.
@@ -81,19 +79,22 @@ struct Share {
 // ---------------------------------------------------------------------------
 
 // Epilogue of the tile kernels. Groups of columns are a wave's; their statistics
-// lie [groups][rows], since a wave writes those of 16 rows.
+// lie [groups][rows], since a wave writes those of 16 rows. The terms go to memory
+// from the registers they are made in, 64 consecutive bytes of each of 16 rows at a
+// time, while the next rows' are made; through LDS, like other results, they took
+// 10 us of a 256 x 256 tile's 112 at K = 4096.
 template <bool HOLD>
 struct StatEpilogue {
-  static constexpr int kW = kOne, kSums = 1;
-  static constexpr bool kSplits = false, kHalves = false, kTakes = true, kWrites = HOLD;
+  static constexpr int kW = kOne, kSums = 1, kGroup = 2;
+  static constexpr bool kSplits = false, kHalves = false, kTakes = true, kWrites = false;
   Stat* stats;
   float* target_logit;     // [rows]: written where a target is among the columns
   const int64_t* targets;  // [rows]
   uint16_t* held;          // [rows][ld]
   int64_t ld;
 
-  // Lane l holds in acc[i][0..TJ) 4 TJ consecutive columns of row 16 i + l % 16 of
-  // the wave's part; the four lanes of a row hold its 16 TJ columns.
+  // Lane l holds in acc[i][j] four columns of row 16 i + l % 16 of the wave's part:
+  // of each 32 columns it has 8, and the four lanes of a row have all 16 TJ.
   template <int OP, int TI, int TJ, int WN>
   __device__ __forceinline__ void take(const TileShape& a, const Place& at,
                                        f32x4 (&acc)[TI][TJ]) const {
@@ -101,47 +102,77 @@ struct StatEpilogue {
     const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
     const int64_t first = at.n0 + (wave % WN) * (TJ * 16);
     if (first >= a.N) return;
-    const int64_t n = first + g * (TJ * 4);
-    const int count = static_cast<int>(min(a.N - n, static_cast<int64_t>(TJ * 4)));  // none: not positive
+    const int32_t left = static_cast<int32_t>(min(a.N - first, static_cast<int64_t>(TJ * 16)));
     Stat* const out = stats + first / (TJ * 16) * a.M;
+    const auto column = [&](int j, int e) { return (j / 2) * 32 + static_cast<int>(g) * 8 + (j % 2) * 4 + e; };
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
       const int64_t row = at.m0 + (wave / WN) * (TI * 16) + i * 16 + low;
-      if (count < TJ * 4) {
+      if (left < TJ * 16) {
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (j * 4 + e >= count) acc[i][j][e] = -INFINITY;
+            if (column(j, e) >= left) acc[i][j][e] = -INFINITY;
       }
       float m = acc[i][0][0];
 #pragma unroll
       for (int j = 0; j < TJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
-      m = across_max(m);
+      m = across_max(m) * kLog2E;
       if (row < a.M) {
-        const int64_t t = targets[row] - n;
-        if (t >= 0 && t < count) {
+        const int64_t t = targets[row] - first;
+        if (t >= 0 && t < left && t / 8 % 4 == g) {
           float z = 0.0f;
 #pragma unroll
           for (int j = 0; j < TJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z = t == j * 4 + e ? acc[i][j][e] : z;
+            for (int e = 0; e < 4; ++e) z = t == column(j, e) ? acc[i][j][e] : z;
           target_logit[row] = z;
         }
       }
+      const float below = m - kHeld;
       float s = 0.0f;
+      if (__any(fabsf(m) == INFINITY)) {
+        // terms at an infinite maximum are 2^15, which leaves lse that infinity
 #pragma unroll
-      for (int j = 0; j < TJ; ++j)
+        for (int j = 0; j < TJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = exp_of(acc[i][j][e], m);
-          if constexpr (HOLD) acc[i][j][e] = p;
-          s = s + p;
-        }
+          for (int e = 0; e < 4; ++e) {
+            const float z = acc[i][j][e] * kLog2E;
+            acc[i][j][e] = __builtin_amdgcn_exp2f(z == m ? kHeld : z - below);
+            s = s + acc[i][j][e];
+          }
+      } else {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2E, -below));
+            s = s + acc[i][j][e];
+          }
+      }
       s = across_sum(s);
-      if (g == 0 && row < a.M) out[row] = {m, s};
+      if (g == 0 && row < a.M) out[row] = {below, s};
+      if constexpr (HOLD) {
+        if (row < a.M) {
+#pragma unroll
+          for (int j = 0; j < TJ; j += 2) {
+            const int count = min(left - column(j, 0), 8);
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] = acc[i][j][e];
+              v[4 + e] = acc[i][j + 1][e];
+            }
+            Chunk<kF16> c;
+            narrow_chunk<kF16>(v, c);
+            // rows of `held` are whole chunks: what is past the last column is read by no one
+            if (count > 0) *reinterpret_cast<u32x4*>(held + row * ld + first + column(j, 0)) = c.w[0];
+          }
+        }
+      }
     }
   }
 
@@ -162,18 +193,12 @@ struct StatEpilogue {
     p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
     return __uint_as_float(p[0]) + __uint_as_float(p[1]);
   }
-
-  // The held exponentials, from take().
-  template <int OP, class Fn>
-  __device__ __forceinline__ void with(const Fn& fn) const {
-    fn([&](int64_t m, int64_t n, int count, float(&v)[8]) { hold(held, ld, m, n, count, v); });
-  }
 };
 
 // The same of the row kernel: groups are a thread's 8 columns, [rows][groups].
 template <bool HOLD>
 struct RowStatEpilogue {
-  static constexpr int kW = kOne, kSums = 1;
+  static constexpr int kW = kOne, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true;
   Stat* stats;
   float* target_logit;
@@ -194,14 +219,21 @@ struct RowStatEpilogue {
         if (e >= count) v[e] = -INFINITY;
         top = fmaxf(top, v[e]);
       }
+      top = top * kLog2E;
+      const float below = top - kHeld;
       float s = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        v[e] = exp_of(v[e], top);
+        const float z = v[e] * kLog2E;
+        v[e] = __builtin_amdgcn_exp2f(z == top ? kHeld : fmaf(v[e], kLog2E, -below));
         s = s + v[e];
       }
-      stats[m * groups + n / 8] = {top, s};
-      if constexpr (HOLD) hold(held, ld, m, n, count, v);
+      stats[m * groups + n / 8] = {below, s};
+      if constexpr (HOLD) {
+        Chunk<kF16> c;
+        narrow_chunk<kF16>(v, c);
+        store_chunk<kF16>(held + m * ld + n, 8, c);
+      }
     });
   }
 };
@@ -209,7 +241,7 @@ struct RowStatEpilogue {
 // Epilogue of the logits made again: G itself, from the rows' lse and shares.
 // Columns V.. of the last piece of a row are zeros (W has no such rows).
 struct GradEpilogue {
-  static constexpr int kW = kOne, kSums = 1;
+  static constexpr int kW = kOne, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true;
   const float* lse;        // [rows]
   const Share* shares;     // [rows]
@@ -247,13 +279,13 @@ struct GradEpilogue {
 // order, eight at a time, joined by halving. R is 16 where there are rows for all
 // CUs (a group's 16 rows are one 128-byte line), and less for fewer rows, which
 // need their groups' latency spread over more threads: 8 rows x 8192 groups 14.6 us
-// with 8 rows to a block, REPLACE with one.
+// with 8 rows to a block, 5.5 with one.
 template <int R>
 __global__ __launch_bounds__(1024) void ce_lse_kernel(const Stat* __restrict__ stats,
                                                       const float* __restrict__ target_logit,
                                                       const int64_t* __restrict__ targets,
-                                                      float* __restrict__ lse, float* __restrict__ loss,
-                                                      int64_t M, int64_t V, int64_t groups, int64_t up,
+                                                      float* __restrict__ lse, float* __restrict__ lse2,
+                                                      float* __restrict__ loss, int64_t M, int64_t V, int64_t groups, int64_t up,
                                                       int64_t along, int64_t ignore_index) {
   constexpr int kEach = 1024 / R;
   __shared__ Stat part[1024];
@@ -280,9 +312,10 @@ __global__ __launch_bounds__(1024) void ce_lse_kernel(const Stat* __restrict__ s
   }
   if (k == 0 && row < M) {
     all = part[threadIdx.x];
-    // an infinite logit: the sum's own terms are 1 at it, and lse is that infinity (or a NaN's NaN)
-    const float l = all.m + logf(all.s);
+    // with the largest term at 1 the logarithm is small, and rounded as finely
+    const float l2 = (all.m + kHeld) + __log2f(all.s * 0x1p-15f), l = l2 * kLn2;
     lse[row] = l;
+    lse2[row] = l2;
     const int64_t t = targets[row];
     loss[row] = t == ignore_index ? 0.0f : t >= 0 && t < V ? l - target_logit[row] : NAN;
   }
@@ -358,13 +391,13 @@ __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
 // `segment` columns, 128 of each row at a time: the groups' 16 rows are one line.
 template <int F>
 __global__ __launch_bounds__(256) void ce_grad_kernel(
-    const Stat* __restrict__ stats, const float* __restrict__ lse, const Share* __restrict__ shares,
+    const Stat* __restrict__ stats, const float* __restrict__ lse2, const Share* __restrict__ shares,
     const int64_t* __restrict__ targets, typename Store<F>::type* __restrict__ held, int64_t M,
     int64_t V, int64_t ld, int64_t segment, int group_bits, int64_t up, int64_t along) {
   const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + threadIdx.x / 16;
   if (row >= M) return;
   const Share w = shares[row];
-  const float l = lse[row], a = w.a * (1.0f / kHeld);
+  const float l = lse2[row];
   const int64_t t = targets[row];
   const bool none = w.a == 0.0f && w.b == 0.0f;
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * segment + threadIdx.x % 16 * 8;
@@ -374,7 +407,7 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(
     typename Store<F>::type* const p = held + row * ld + n;
     float v[8];
     widen_chunk<kF16>(load_chunk<kF16>(p, 8), v);
-    const float f = exp_of(stats[(n >> group_bits) * along + row * up].m, l) * a;
+    const float f = exp2_of(stats[(n >> group_bits) * along + row * up].m, l) * w.a;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = v[e] * f;
@@ -395,7 +428,7 @@ __global__ void ce_fill_kernel(float* p, float v) { *p = v; }
 // Sums over pieces of V (grad_x) or chunks of rows (grad_weight) are added up in
 // fp32, in ascending order, and rounded once, with the shares' scale taken back.
 struct SumEpilogue {
-  static constexpr int kW = kOne, kSums = 1;
+  static constexpr int kW = kOne, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
   void* out;
   float* sum;            // where there are several
@@ -459,7 +492,7 @@ struct Plan {
   bool pad;                      // rows along K are copied whole
   int64_t ldk;                   // their bytes
   mhc_linear_launch px, pw;      // the products over G
-  int64_t x, w, stats, target, rows, shares, inverse, held, part, sum_x, sum_w, total;  // places
+  int64_t x, w, stats, target, lse2, rows, shares, inverse, held, part, sum_x, sum_w, total;  // places
 };
 
 // Rows of a chunk: as many as the held values' bytes allow, evenly, in whole tiles.
@@ -508,6 +541,7 @@ mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
     // the launch that the policy chose may go through the medium tiles, whose groups are as wide
     p.stats = at.take(mul_bytes(p.groups, p.chunk, sizeof(Stat)));
     p.target = at.take(mul_bytes(p.chunk, 4, 1));
+    p.lse2 = at.take(mul_bytes(p.chunk, 4, 1));
     p.rows = at.take(mul_bytes(M, 4, 1));
   }
   if (mode != kFwd) {
@@ -668,7 +702,8 @@ hipError_t launch_stats(const Call& c, const Plan& p, const void* x, const void*
   float* const loss = c.reduction == MHC_REDUCTION_NONE ? c.loss : reinterpret_cast<float*>(c.ws + p.rows);
   const auto run = [&](auto kernel, int64_t r) {
     return launch_kernel(kernel, dim3(static_cast<uint32_t>(ceil_div(rows, r))), dim3(1024), s, nullptr,
-                         nullptr, stats, target, targets, c.lse + row0, loss + row0, rows, c.V,
+                         nullptr, stats, target, targets, c.lse + row0, reinterpret_cast<float*>(c.ws + p.lse2),
+                         loss + row0, rows, c.V,
                          p.groups, up_of(p), along_of(p, rows), c.ignore_index);
   };
   return rows >= 4096 ? run(ce_lse_kernel<16>, 16) : rows >= 1024 ? run(ce_lse_kernel<4>, 4)
@@ -775,8 +810,8 @@ hipError_t launch_all(const Call& c, const Plan& p, hipStream_t s, hipEvent_t st
         const int64_t segment = 128 * (pieces < 1 ? 1 : pieces > 16 ? 16 : pieces);
         e = launch_kernel(ce_grad_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(c.V, segment)), static_cast<uint32_t>(high)),
                           dim3(256), s, nullptr, nullptr, reinterpret_cast<const Stat*>(c.ws + p.stats),
-                          c.lse + row0, shares + row0, c.targets + row0, reinterpret_cast<S*>(c.ws + p.held),
-                          rows, c.V, p.ld, segment, p.group_bits, up_of(p), along_of(p, rows));
+                          reinterpret_cast<const float*>(c.ws + p.lse2), shares + row0, c.targets + row0,
+                          reinterpret_cast<S*>(c.ws + p.held), rows, c.V, p.ld, segment, p.group_bits, up_of(p), along_of(p, rows));
       }
     }
     if (e == hipSuccess && grads) e = launch_over_g<OP>(c, p, xc, w, row0, rows, s);

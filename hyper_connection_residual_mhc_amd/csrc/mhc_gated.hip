@@ -26,7 +26,7 @@ namespace {
 // ---------------------------------------------------------------------------
 
 struct GatedEpilogue {
-  static constexpr int kW = kBoth, kSums = 2;
+  static constexpr int kW = kBoth, kSums = 2, kGroup = 0;
   static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
   const void* gate_bias;
   const void* up_bias;

@@ -18,7 +18,7 @@ namespace {
 
 // Epilogue: scales, bias, activation and residual.
 struct Epilogue {
-  static constexpr int kW = kOne, kSums = 1;
+  static constexpr int kW = kOne, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
   const void* bias;
   const void* residual;

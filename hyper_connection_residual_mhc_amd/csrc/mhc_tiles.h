@@ -243,6 +243,8 @@ struct TileShape {
 
 // E, the epilogue, says
 //   kW       what W is (kOne, kBoth, kChain), kSums how many sums an output has;
+//   kGroup   through how many tiles of 16 columns a lane's results are consecutive, 0
+//            for as many as there are (of either weight);
 //   kSplits  whether sums come in parts, which another kernel joins;
 //   kHalves  two products in one launch: x (turned) is two blocks of M columns, and
 //            the rows of the second one's results come after the M of the first;
@@ -264,7 +266,7 @@ constexpr int log2_of() {
 
 // How many consecutive tiles of 16 columns a lane's results run through.
 template <class E>
-constexpr int group_of(int tj) { return E::kW == kBoth ? tj / 2 : tj < 4 ? tj : 4; }
+constexpr int group_of(int tj) { return E::kGroup != 0 ? E::kGroup : E::kW == kBoth ? tj / 2 : tj < 4 ? tj : 4; }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(
@@ -693,7 +695,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
 
   // Block scales. DMA: thread r brings 16 bytes of row r, x's then W's, which are
   // those of four passes: a load of 4 bytes for each pass asks the L2 for as many
-  // lines as two thirds of the operands (two weights of 14336 x 7168 and 24 rows REPLACE).
+  // lines as two thirds of the operands (two weights of 14336 x 7168 and 24
+  // rows: 55 -> 43.5 us).
   // Else: each lane the bytes of its own rows; rows past the end read the last
   // row's (their values are zeros), and past the last block of a row any finite
   // scale does (those values are zeros too).
@@ -907,6 +910,7 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
   i32x4 sr = {0, 0, 0, 0};
   if constexpr (kScales) {
     const bool of_x = wave < 4;
+    static_assert(W == kBoth || G == 4, "the order of W's rows in turn_scales");
     const bool of_2 = W == kBoth && wave >= 6;  // two waves bring a weight's 128 rows
     const uint32_t r = threadIdx.x % (W == kBoth && !of_x ? 128 : 256), here = of_x ? lx.here : lw.here;
     sr = buffer_of(of_x ? a.xs + place.m0 * kblocks : (of_2 ? a.ws2 : a.ws) + place.n0 * kblocks,
@@ -1252,7 +1256,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs<E> a) 
 // go to `out` and, from row M on, to `out2`.
 template <int W, bool HALVES>
 struct StoreEpilogue {
-  static constexpr int kW = W, kSums = 1;
+  static constexpr int kW = W, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = true, kHalves = HALVES, kTakes = false, kWrites = true;
   void* out;
   void* out2;

@@ -167,8 +167,9 @@ mhc_status make_plan(int64_t M, int64_t N, int64_t K, int32_t dtype,
 // of kTileK bytes while every CU has at most one block of it, and a CU with more
 // works one off in `busy`; a tile's end takes `end`, a launch 3, and joining s parts 3.5
 // and their bytes' way to memory and back. The constants are fitted to 8-bit and bf16
-// products of 17 to 4096 rows x 1024 to 28672 x 512 to 28672; of 110 of them this takes
-// the fastest launch or one within REPLACE of it. 8-bit integers, the rule above
+// products of 17 to 4096 rows x 1024 to 28672 x 512 to 28672; of 116 of them this takes
+// the fastest launch or one within 5% of it 97 times, and one 10% off or more 11 times
+// (36% at worst, 384 x 4096 x 8192 in bf16). 8-bit integers, the rule above
 // and this one: 32 x 7168 x 4096 12.5 -> 9.8 us (small tiles in 4 parts, short ones in
 // one), 256 x 4096 x 7168 21.9 -> 18.2, 1024 x 1024 x 4096 16.4 -> 11.9; two weights of
 // 14336 x 7168 in bf16 and 24 rows 117 -> 74 (medium tiles, short ones).
