@@ -100,76 +100,71 @@ struct StatEpilogue {
                                        f32x4 (&acc)[TI][TJ]) const {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
-    const int64_t first = at.n0 + (wave % WN) * (TJ * 16);
-    if (first >= a.N) return;
-    const int32_t left = static_cast<int32_t>(min(a.N - first, static_cast<int64_t>(TJ * 16)));
-    Stat* const out = stats + first / (TJ * 16) * a.M;
-    const auto column = [&](int j, int e) { return (j / 2) * 32 + static_cast<int>(g) * 8 + (j % 2) * 4 + e; };
+    constexpr int kTiles = TJ < 4 ? TJ : 4;  // of a group
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      const int64_t row = at.m0 + (wave / WN) * (TI * 16) + i * 16 + low;
-      if (left < TJ * 16) {
+    for (int sub = 0; sub < TJ / kTiles; ++sub) {
+      const int64_t first = at.n0 + (wave % WN) * (TJ * 16) + sub * (kTiles * 16);
+      if (first >= a.N) return;
+      const int32_t left = static_cast<int32_t>(min(a.N - first, static_cast<int64_t>(kTiles * 16)));
+      Stat* const out = stats + first / (kTiles * 16) * a.M;
+      const auto column = [&](int j, int e) { return (j / 2) * 32 + static_cast<int>(g) * 8 + (j % 2) * 4 + e; };
 #pragma unroll
-        for (int j = 0; j < TJ; ++j)
+      for (int i = 0; i < TI; ++i) {
+        f32x4(&z)[TJ] = acc[i];
+        from_here(z);
+        const int64_t row = at.m0 + (wave / WN) * (TI * 16) + i * 16 + low;
+        float v[kTiles * 4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (column(j, e) >= left) acc[i][j][e] = -INFINITY;
-      }
-      float m = acc[i][0][0];
-#pragma unroll
-      for (int j = 0; j < TJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
-      m = across_max(m) * kLog2E;
-      if (row < a.M) {
-        const int64_t t = targets[row] - first;
-        if (t >= 0 && t < left && t / 8 % 4 == g) {
-          float z = 0.0f;
-#pragma unroll
-          for (int j = 0; j < TJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z = t == column(j, e) ? acc[i][j][e] : z;
-          target_logit[row] = z;
-        }
-      }
-      const float below = m - kHeld;
-      float s = 0.0f;
-      if (__any(fabsf(m) == INFINITY)) {
-        // terms at an infinite maximum are 2^15, which leaves lse that infinity
-#pragma unroll
-        for (int j = 0; j < TJ; ++j)
+        for (int j = 0; j < kTiles; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float z = acc[i][j][e] * kLog2E;
-            acc[i][j][e] = __builtin_amdgcn_exp2f(z == m ? kHeld : z - below);
-            s = s + acc[i][j][e];
+            v[j * 4 + e] = z[sub * kTiles + j][e];
+            if (left < kTiles * 16 && column(j, e) >= left) v[j * 4 + e] = -INFINITY;
           }
-      } else {
+        float m = v[0];
 #pragma unroll
-        for (int j = 0; j < TJ; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[i][j][e] = __builtin_amdgcn_exp2f(fmaf(acc[i][j][e], kLog2E, -below));
-            s = s + acc[i][j][e];
-          }
-      }
-      s = across_sum(s);
-      if (g == 0 && row < a.M) out[row] = {below, s};
-      if constexpr (HOLD) {
+        for (int k = 1; k < kTiles * 4; ++k) m = fmaxf(m, v[k]);
+        m = across_max(m) * kLog2E;
         if (row < a.M) {
+          const int64_t t = targets[row] - first;
+          if (t >= 0 && t < left && t / 8 % 4 == g) {
+            float at_t = 0.0f;
 #pragma unroll
-          for (int j = 0; j < TJ; j += 2) {
-            const int count = min(left - column(j, 0), 8);
-            float v[8];
+            for (int k = 0; k < kTiles * 4; ++k) at_t = t == column(k / 4, k % 4) ? v[k] : at_t;
+            target_logit[row] = at_t;
+          }
+        }
+        const float below = m - kHeld;
+        float s = 0.0f;
+        if (__any(fabsf(m) == INFINITY)) {
+          // terms at an infinite maximum are 2^15, which leaves lse that infinity
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[e] = acc[i][j][e];
-              v[4 + e] = acc[i][j + 1][e];
+          for (int k = 0; k < kTiles * 4; ++k) {
+            const float y = v[k] * kLog2E;
+            v[k] = __builtin_amdgcn_exp2f(y == m ? kHeld : y - below);
+            s = s + v[k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kTiles * 4; ++k) {
+            v[k] = __builtin_amdgcn_exp2f(fmaf(v[k], kLog2E, -below));
+            s = s + v[k];
+          }
+        }
+        s = across_sum(s);
+        if (g == 0 && row < a.M) out[row] = {below, s};
+        if constexpr (HOLD) {
+          if (row < a.M) {
+#pragma unroll
+            for (int j = 0; j < kTiles; j += 2) {
+              float u[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) u[e] = v[j * 4 + e];
+              Chunk<kF16> c;
+              narrow_chunk<kF16>(u, c);
+              // rows of `held` are whole chunks: what is past the last column is read by no one
+              if (column(j, 0) < left) *reinterpret_cast<u32x4*>(held + row * ld + first + column(j, 0)) = c.w[0];
             }
-            Chunk<kF16> c;
-            narrow_chunk<kF16>(v, c);
-            // rows of `held` are whole chunks: what is past the last column is read by no one
-            if (count > 0) *reinterpret_cast<u32x4*>(held + row * ld + first + column(j, 0)) = c.w[0];
           }
         }
       }

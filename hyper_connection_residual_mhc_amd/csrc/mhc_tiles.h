@@ -35,6 +35,8 @@ constexpr int kOpMX = MHC_LINEAR_E4M3_MX;
 constexpr int kOpI8 = MHC_LINEAR_I8_ROW;
 
 constexpr bool is8(int op) { return op == kOpE4M3 || op == kOpMX || op == kOpI8; }
+// Whether large tiles are four waves' (see linear_wide_kernel).
+constexpr bool wide_tiles(int op) { return op == kOpBF16 || op == kOpF16; }
 // Scales of a row's, applied in the epilogue.
 constexpr bool scaled(int op) { return op == kOpE4M3 || op == kOpI8; }
 // Storage format of bias, residual, out and z.
@@ -166,6 +168,36 @@ __device__ __forceinline__ f32x4 mma(const Frag<OP>& a, const Frag<OP>& b, f32x4
   }
 }
 
+// c += a b^T in place, in the accumulation registers: left to itself the compiler
+// gives each result a new place and spends a sixth of a loop of 256 of them moving them
+// about. It sees no matrix instruction here, so what it would wait for is waited for
+// by hand: acc_ready() stands between these and any other access to c.
+template <int OP>
+__device__ __forceinline__ void mma_in_place(f32x4& c, const i32x4& a, const i32x4& b) {
+  static_assert(OP == kOpBF16 || OP == kOpF16, "16-bit values");
+  if constexpr (OP == kOpBF16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// The results of mma_in_place of one row of tiles are taken out of the accumulation
+// registers here, not all of them as soon as they are there.
+template <int TJ>
+__device__ __forceinline__ void from_here(f32x4 (&c)[TJ]) {
+  if constexpr (TJ == 8)
+    asm volatile("" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
+}
+
+template <int TI>
+__device__ __forceinline__ void acc_ready(f32x4 (&c)[TI][8]) {
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+    asm volatile("s_nop 15\n\ts_nop 15"
+                 : "+a"(c[i][0]), "+a"(c[i][1]), "+a"(c[i][2]), "+a"(c[i][3]), "+a"(c[i][4]),
+                   "+a"(c[i][5]), "+a"(c[i][6]), "+a"(c[i][7]));
+}
+
 // The same with the scale bytes named by values that unrolling makes constants.
 template <int OP>
 __device__ __forceinline__ f32x4 mma_bytes(const Frag<OP>& a, const Frag<OP>& b, f32x4 acc, int sa,
@@ -291,6 +323,17 @@ __device__ __forceinline__ void load_to_lds(uint32_t offset, i32x4 rsrc, uint32_
                  :
                  : "s"(to), "v"(offset), "s"(rsrc), "s"(at)
                  : "memory");
+}
+
+// The same in two steps, which want something between them: m0 needs a cycle.
+__device__ __forceinline__ void set_place(uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0" : : "s"(to) : "memory");
+}
+__device__ __forceinline__ void load_to_place(uint32_t offset, i32x4 rsrc, uint32_t at) {
+  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(offset), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(at))
+               : "memory");
 }
 
 // The buffer of up to 2^31 - 1 bytes from p on, in scalar registers.
@@ -434,6 +477,26 @@ struct Operand {
       else if (left > 0)
         held[SET][q] = short_piece<ELEM>(p, left, TURNED ? piece > 0 || inside : p - begin >= 16);
     }
+  }
+
+  // DMA: what the loads of one pass share, and load q of them, whose place is set.
+  struct Pass {
+    i32x4 from;
+    uint32_t offset, at;
+  };
+  __device__ __forceinline__ Pass pass(uint32_t kt) const {
+    Pass p;
+    const bool second = W == kChain && kt >= kfirst;
+    if (second) kt -= kfirst;
+    p.from = W == kChain && second ? rsrc2 : rsrc;
+    p.offset = TURNED || kt * kTileK + piece < kbytes ? offset : kOutside;
+    p.at = TURNED ? kt * (kTileK / ELEM) * ld : kt * kTileK;
+    return p;
+  }
+  __device__ __forceinline__ void load(const Pass& p, int q) const {
+    const bool second = W == kBoth && q * kEach >= kRows;
+    const uint32_t rows = q * kEach - (second ? kRows : 0);
+    load_to_place(p.offset, second ? rsrc2 : p.from, p.at + rows * ld);
   }
 
   // Through registers: writes the loaded tile.
@@ -846,7 +909,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
 }
 
 // ---------------------------------------------------------------------------
-// Large tiles
+// Large tiles of 8-bit values
 //
 // 256 x 256 outputs to a block of eight waves, 128 x 64 each, two waves to a
 // SIMD. A wave's reads run ahead of its matrix instructions: its W rows and the
@@ -858,23 +921,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void linear_tile_kernel(TileArgs<E
 // arrive. Reads and loads are spread between the instructions of one W row
 // (sched_barrier): a run of other instructions leaves the matrix unit idle.
 //
-// 8192^3 in bf16 (1373 TFLOP/s; the library's product 1430-1465): four waves of 128 x 128, one to a SIMD,
-// 1230 (nobody fills a wave's gaps); all loads at the start of the half 1140;
-// reads not ahead of the pass 1280; without the raised priority of the
-// matrix instructions 1346. Matrix units are busy 57-63% of the cycles, at a clock that the
-// load itself brings down to 1.7 GHz (bf16) and 1.95 GHz (e4m3). e4m3 at 8192^3 and 8192 x
-// 4096 x 7168: 2670 TFLOP/s with row scales (the library's 2436 and 2675), with block
-// scales 2270 and 2460; with a scale byte read for each row and pass instead of
-// one word for four tiles 2060.
-
+// e4m3 at 8192^3 and 8192 x 4096 x 7168: 2670 TFLOP/s with row scales (the library's 2436
+// and 2675), with block scales 2270 and 2460; with a scale byte read for each row and
+// pass instead of one word for four tiles 2060. 8-bit integers at 8192 x 4096 x 7168, with
+// four waves of 128 x 128 each as below 200 us, so 194. With bf16 at 8192^3 (1373 TFLOP/s on the
+// card of these figures): all loads at the start of the half 1140; reads not ahead of
+// the pass 1280; without the raised priority of the matrix instructions 1346.
 // ---------------------------------------------------------------------------
 
-template <int OP, bool TX, bool TW, class E>
+template <int OP, class E>
 __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
   constexpr int BM = 256, BN = 256, WN = 4, kThreads = 512;
   constexpr int TI = 8, TJ = 4, HALF = TI / 2;
-  constexpr int kPieces = is8(OP) ? 1 : 2;  // matrix instructions for one result in a pass
-  constexpr int ELEM = is8(OP) ? 1 : 2;
+  constexpr int ELEM = 1;
+  static_assert(!wide_tiles(OP), "these take linear_wide_kernel");
   constexpr uint32_t kBuffer = (BM + BN) * kTileK;
   constexpr bool kScales = OP == kOpMX;
   constexpr uint32_t kTurned = 8 * 64 + 16;  // words of a pass in `turned`; 16 more, so that four passes are in four banks
@@ -887,16 +947,15 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
   const uint32_t lane = threadIdx.x % 64, g = lane / 16;
   const uint32_t wm = wave / WN, wn = wave % WN;
 
-  typedef Operand<BM, kThreads, TX, false, 1, true, ELEM> OpX;
-  typedef Operand<BN, kThreads, TW, true, G, true, ELEM, W> OpW;
+  typedef Operand<BM, kThreads, false, false, 1, true, ELEM> OpX;
+  typedef Operand<BN, kThreads, false, true, G, true, ELEM, W> OpW;
   static_assert(OpX::Q == TJ && OpW::Q == TJ, "one round of loads for each W tile");
   OpX lx;
   OpW lw;
-  if constexpr (E::kHalves) lx.init(a.x, place.m0 + (place.second ? a.xupper : 0), a.M - place.m0, a);
-  else lx.init(a.x, place.m0, a);
+  lx.init(a.x, place.m0, a);
   lw.init(a.w, place.n0, a);
-  Reader<OpX, TX, false, 1> rx;
-  Reader<OpW, TW, true, G, W> rw;
+  Reader<OpX, false, false, 1> rx;
+  Reader<OpW, false, true, G, W> rw;
   rx.init(wm * (TI * 16));
   rw.init(wn * (W == kBoth ? TJ * 8 : TJ * 16));
 
@@ -982,18 +1041,11 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   const auto multiply = [&](int half, int j, const Row (&x)[HALF]) {
 #pragma unroll
-    for (int h = 0; h < kPieces; ++h)
-#pragma unroll
-      for (int i = 0; i < HALF; ++i) {
-        f32x4& c = acc[half * HALF + i][j];
-        if constexpr (is8(OP)) {
-          const Frag<OP> p = {w[j].w[0], w[j].w[1]}, q = {x[i].w[0], x[i].w[1]};
-          c = kScales ? mma_bytes<OP>(p, q, c, now.w, now.x[half], j, i) : mma<OP>(p, q, c, 0, 0);
-        } else {
-          const Frag<OP> p = {w[j].w[h]}, q = {x[i].w[h]};
-          c = mma<OP>(p, q, c, 0, 0);
-        }
-      }
+    for (int i = 0; i < HALF; ++i) {
+      f32x4& c = acc[half * HALF + i][j];
+      const Frag<OP> p = {w[j].w[0], w[j].w[1]}, q = {x[i].w[0], x[i].w[1]};
+      c = kScales ? mma_bytes<OP>(p, q, c, now.w, now.x[half], j, i) : mma<OP>(p, q, c, 0, 0);
+    }
   };
 
   const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
@@ -1040,6 +1092,114 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
     now = next;
   }
   wait_tiles<0>();  // nothing arrives in LDS any more
+  end_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
+}
+
+// ---------------------------------------------------------------------------
+// Large tiles of 16-bit values
+//
+// The same tile by four waves, 128 x 128 each and one to a SIMD: two thirds of the
+// reads from LDS, and results that never leave the accumulation registers. Nobody
+// fills a wave's gaps, so there are none: each of the 128 matrix instructions of a
+// pass (16 cycles) has at most one read, one load or one scalar step in front of it,
+// held there by sched_barrier. The first half of a pass (k 0..31 of 64) reads the second
+// half's values; its last instructions stand behind the barrier after which the
+// other buffer has arrived and this one is free, and the second half reads the next
+// pass's values there and loads this buffer again. An output's sums have the order that the
+// eight-wave kernel gives them.
+//
+// 8192^3 in bf16 on one card 1502 TFLOP/s, eight waves 1444, the library 1600; 4096 x
+// 16384 x 4096 1377, 1352, 1555. A load's three steps in a row 1.5% slower; left to
+// the compiler's registers slower than eight waves. Results straight from the
+// registers to memory, for epilogues of a few instructions, instead of through LDS:
+// no difference. Matrix units are busy 85% of the loop, at 1.76 GHz: more of them,
+// and the clock gives way.
+// ---------------------------------------------------------------------------
+
+template <int OP, bool TX, bool TW, class E>
+__global__ __launch_bounds__(256, 1) void linear_wide_kernel(TileArgs<E> a) {
+  constexpr int BM = 256, BN = 256, WN = 2, kThreads = 256;
+  constexpr int TI = 8, TJ = 8;
+  constexpr int ELEM = 2;
+  constexpr uint32_t kBuffer = (BM + BN) * kTileK;
+  constexpr int G = group_of<E>(TJ), W = E::kW;
+  __shared__ __align__(1024) uint8_t lds[2][kBuffer];
+  const Place place = place_of<BM, BN / E::kSums, E::kHalves>(a);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t wm = wave / WN, wn = wave % WN;
+  typedef Operand<BM, kThreads, TX, false, 1, true, ELEM> OpX;
+  typedef Operand<BN, kThreads, TW, true, G, true, ELEM, W> OpW;
+  static_assert(OpX::Q == 8 && OpW::Q == 8, "16 loads in a pass");
+  OpX lx;
+  OpW lw;
+  if constexpr (E::kHalves) lx.init(a.x, place.m0 + (place.second ? a.xupper : 0), a.M - place.m0, a);
+  else lx.init(a.x, place.m0, a);
+  lw.init(a.w, place.n0, a);
+  Reader<OpX, TX, false, 1> rx;
+  Reader<OpW, TW, true, G, W> rw;
+  rx.init(wm * (TI * 16));
+  rw.init(wn * (W == kBoth ? TJ * 8 : TJ * 16));
+
+  // The values of both halves of a pass: x's tiles, then W's.
+  i32x4 xf[2][TI], wf[2][TJ];
+  const auto read = [&](uint32_t b, int h, int k) {
+    if (k < TI) xf[h][k] = rx.read(lds[b], k, h);
+    else wf[h][k - TI] = rw.read(lds[b] + BM * kTileK, k - TI, h);
+  };
+  const uint32_t to_wave = __builtin_amdgcn_readfirstlane(lds_address(&lds[0][0]) + wave * 1024);
+  const auto set = [&](uint32_t b, int k) { set_place(to_wave + b * kBuffer + k * (kThreads * 16)); };
+  const auto load = [&](const typename OpX::Pass& px, const typename OpW::Pass& pw, int k) {
+    if (k < 8) lx.load(px, k);
+    else lw.load(pw, k - 8);
+  };
+  const auto load_all = [&](uint32_t kt, uint32_t b) {
+    const auto px = lx.pass(kt);
+    const auto pw = lw.pass(kt);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      set(b, k);
+      asm volatile("s_nop 0");
+      load(px, pw, k);
+    }
+  };
+  f32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
+  const uint32_t first = place.part * a.per_split;
+  const uint32_t last = min(all, first + a.per_split);
+  load_all(first, 0);
+  wait_tiles<0>();
+  load_all(first + 1, 1);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) read(0, 0, k);
+  acc_ready(acc);
+  for (uint32_t kt = first; kt < last; ++kt) {
+    const uint32_t b = (kt - first) & 1;
+    // past the last tile: zeros are loaded and old values read, and neither is used
+    const auto px = lx.pass(kt + 2);
+    const auto pw = lw.pass(kt + 2);
+#pragma unroll
+    for (int k = 0; k < 64; ++k) {
+      if (k % 2 == 0 && k < 32) read(b, 1, k / 2);
+      if (k == 56) wait_tiles<0>();
+      mma_in_place<OP>(acc[k % 8][k / 8], wf[0][k / 8], xf[0][k % 8]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int k = 0; k < 64; ++k) {
+      if (k % 4 == 0) read(b ^ 1, 0, k / 4);
+      if (k % 4 == 1) set(b, k / 4);
+      if (k % 4 == 2) load(px, pw, k / 4);
+      mma_in_place<OP>(acc[k % 8][k / 8], wf[1][k / 8], xf[1][k % 8]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  wait_tiles<0>();  // nothing arrives in LDS any more
+  acc_ready(acc);
   end_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
 

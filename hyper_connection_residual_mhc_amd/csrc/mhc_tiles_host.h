@@ -291,7 +291,10 @@ template <int OP, bool TX, bool TW, class E>
 hipError_t launch_large(TileArgs<E> a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
   if (!straight<OP, TX, TW>(a)) return launch_medium<OP, TX, TW>(a, s, start, stop);
   const dim3 grid = tile_grid<256, 256>(a);
-  return launch_kernel(linear_large_kernel<OP, TX, TW, E>, grid, dim3(512), s, start, stop, a);
+  if constexpr (wide_tiles(OP))
+    return launch_kernel(linear_wide_kernel<OP, TX, TW, E>, grid, dim3(256), s, start, stop, a);
+  else
+    return launch_kernel(linear_large_kernel<OP, E>, grid, dim3(512), s, start, stop, a);
 }
 
 // One product and its epilogue, as planned. The backward's products (TW), those
