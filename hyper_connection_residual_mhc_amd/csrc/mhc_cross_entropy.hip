@@ -101,71 +101,92 @@ struct StatEpilogue {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
     constexpr int kTiles = TJ < 4 ? TJ : 4;  // of a group
-#pragma unroll
+    // 128 x 128 of a wave would be 16 copies of 400 instructions
+    constexpr int kCopies = TJ == 8 ? 1 : TI;
+#pragma unroll 1
     for (int sub = 0; sub < TJ / kTiles; ++sub) {
       const int64_t first = at.n0 + (wave % WN) * (TJ * 16) + sub * (kTiles * 16);
       if (first >= a.N) return;
       const int32_t left = static_cast<int32_t>(min(a.N - first, static_cast<int64_t>(kTiles * 16)));
       Stat* const out = stats + first / (kTiles * 16) * a.M;
-      const auto column = [&](int j, int e) { return (j / 2) * 32 + static_cast<int>(g) * 8 + (j % 2) * 4 + e; };
-#pragma unroll
+      const int64_t row0 = at.m0 + (wave / WN) * (TI * 16) + low;
+#pragma unroll kCopies
       for (int i = 0; i < TI; ++i) {
-        f32x4(&z)[TJ] = acc[i];
-        from_here(z);
-        const int64_t row = at.m0 + (wave / WN) * (TI * 16) + i * 16 + low;
+        f32x4 z[kTiles];
+        if constexpr (kCopies == TI) {
+#pragma unroll
+          for (int j = 0; j < kTiles; ++j) z[j] = acc[i][j];
+        } else {
+          each_of<TI * 2>(sub * TI + i, [&](auto k) {
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) z[j] = acc[k % TI][k / TI * kTiles + j];
+          });
+        }
+        const int64_t row = row0 + i * 16;
         float v[kTiles * 4];
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            v[j * 4 + e] = z[sub * kTiles + j][e];
-            if (left < kTiles * 16 && column(j, e) >= left) v[j * 4 + e] = -INFINITY;
+            v[j * 4 + e] = z[j][e];
+            if (left < kTiles * 16 && column(j, e, g) >= left) v[j * 4 + e] = -INFINITY;
           }
-        float m = v[0];
+        one_row<kTiles>(a.M, row, first, left, g, v, out);
+      }
+    }
+  }
+
+  // The column of the group that is in v[4 j + e].
+  static __device__ __forceinline__ int column(int j, int e, uint32_t g) {
+    return (j / 2) * 32 + static_cast<int>(g) * 8 + (j % 2) * 4 + e;
+  }
+
+  template <int kTiles>
+  __device__ __forceinline__ void one_row(int64_t M, int64_t row, int64_t first, int32_t left, uint32_t g,
+                                          float (&v)[kTiles * 4], Stat* out) const {
+    float m = v[0];
 #pragma unroll
-        for (int k = 1; k < kTiles * 4; ++k) m = fmaxf(m, v[k]);
-        m = across_max(m) * kLog2E;
-        if (row < a.M) {
-          const int64_t t = targets[row] - first;
-          if (t >= 0 && t < left && t / 8 % 4 == g) {
-            float at_t = 0.0f;
+    for (int k = 1; k < kTiles * 4; ++k) m = fmaxf(m, v[k]);
+    m = across_max(m) * kLog2E;
+    if (row < M) {
+      const int64_t t = targets[row] - first;
+      if (t >= 0 && t < left && t / 8 % 4 == g) {
+        float at_t = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kTiles * 4; ++k) at_t = t == column(k / 4, k % 4) ? v[k] : at_t;
-            target_logit[row] = at_t;
-          }
-        }
-        const float below = m - kHeld;
-        float s = 0.0f;
-        if (__any(fabsf(m) == INFINITY)) {
-          // terms at an infinite maximum are 2^15, which leaves lse that infinity
+        for (int k = 0; k < kTiles * 4; ++k) at_t = t == column(k / 4, k % 4, g) ? v[k] : at_t;
+        target_logit[row] = at_t;
+      }
+    }
+    const float below = m - kHeld;
+    float s = 0.0f;
+    if (__any(fabsf(m) == INFINITY)) {
+      // terms at an infinite maximum are 2^15, which leaves lse that infinity
 #pragma unroll
-          for (int k = 0; k < kTiles * 4; ++k) {
-            const float y = v[k] * kLog2E;
-            v[k] = __builtin_amdgcn_exp2f(y == m ? kHeld : y - below);
-            s = s + v[k];
-          }
-        } else {
+      for (int k = 0; k < kTiles * 4; ++k) {
+        const float y = v[k] * kLog2E;
+        v[k] = __builtin_amdgcn_exp2f(y == m ? kHeld : y - below);
+        s = s + v[k];
+      }
+    } else {
 #pragma unroll
-          for (int k = 0; k < kTiles * 4; ++k) {
-            v[k] = __builtin_amdgcn_exp2f(fmaf(v[k], kLog2E, -below));
-            s = s + v[k];
-          }
-        }
-        s = across_sum(s);
-        if (g == 0 && row < a.M) out[row] = {below, s};
-        if constexpr (HOLD) {
-          if (row < a.M) {
+      for (int k = 0; k < kTiles * 4; ++k) {
+        v[k] = __builtin_amdgcn_exp2f(fmaf(v[k], kLog2E, -below));
+        s = s + v[k];
+      }
+    }
+    s = across_sum(s);
+    if (g == 0 && row < M) out[row] = {below, s};
+    if constexpr (HOLD) {
+      if (row < M) {
 #pragma unroll
-            for (int j = 0; j < kTiles; j += 2) {
-              float u[8];
+        for (int j = 0; j < kTiles; j += 2) {
+          float u[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) u[e] = v[j * 4 + e];
-              Chunk<kF16> c;
-              narrow_chunk<kF16>(u, c);
-              // rows of `held` are whole chunks: what is past the last column is read by no one
-              if (column(j, 0) < left) *reinterpret_cast<u32x4*>(held + row * ld + first + column(j, 0)) = c.w[0];
-            }
-          }
+          for (int e = 0; e < 8; ++e) u[e] = v[j * 4 + e];
+          Chunk<kF16> c;
+          narrow_chunk<kF16>(u, c);
+          // rows of `held` are whole chunks: what is past the last column is read by no one
+          if (column(j, 0, g) < left) *reinterpret_cast<u32x4*>(held + row * ld + first + column(j, 0, g)) = c.w[0];
         }
       }
     }
@@ -435,7 +456,11 @@ struct SumEpilogue {
   __device__ __forceinline__ void with(const Fn& fn) const {
     constexpr int F = out_format(OP);
     typedef typename Store<F>::type S;
-    const float scale = *inverse;
+    // to a scalar register, so that no load is on its way when the next tile begins: that one's loop
+    // would wait for it, and with it for its own, in every pass
+    float scale = 1.0f;
+    if (last != 0)
+      scale = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(*inverse)));
     fn([&](int64_t m, int64_t n, int count, float(&v)[8]) {
       if (first == 0) {
         float b[8];

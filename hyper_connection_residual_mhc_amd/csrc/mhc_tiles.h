@@ -181,12 +181,11 @@ __device__ __forceinline__ void mma_in_place(f32x4& c, const i32x4& a, const i32
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
-// The results of mma_in_place of one row of tiles are taken out of the accumulation
-// registers here, not all of them as soon as they are there.
-template <int TJ>
-__device__ __forceinline__ void from_here(f32x4 (&c)[TJ]) {
-  if constexpr (TJ == 8)
-    asm volatile("" : "+a"(c[0]), "+a"(c[1]), "+a"(c[2]), "+a"(c[3]), "+a"(c[4]), "+a"(c[5]), "+a"(c[6]), "+a"(c[7]));
+// Writes the results of mma_in_place of one row of tiles to LDS, out of the accumulation
+// registers (as inputs of the assembly, so that a row's place in a branch costs no copy).
+__device__ __forceinline__ void put_row(const f32x4 (&c)[8], const uint32_t (&to)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) asm volatile("ds_write_b128 %0, %1" : : "v"(to[j]), "a"(c[j]) : "memory");
 }
 
 template <int TI>
@@ -596,11 +595,10 @@ struct Place {
 };
 
 template <int BM, int BN, bool HALVES>
-__device__ __forceinline__ Place place_of(const TileShape& a) {
+__device__ __forceinline__ Place place_of(const TileShape& a, uint32_t id = blockIdx.x) {
   // Quotients are made in vector registers; what is the same in every lane is
   // taken back to scalar ones, or all that follows from it would stay there.
   const uint32_t tiles = a.tiles_m * a.tiles_n;
-  uint32_t id = blockIdx.x;
   const uint32_t part = __builtin_amdgcn_readfirstlane(id / tiles);
   id -= part * tiles;
   const uint32_t each = tiles / 8, more = tiles % 8, xcd = id % 8, k = id / 8;
@@ -615,10 +613,18 @@ __device__ __forceinline__ Place place_of(const TileShape& a) {
   return {static_cast<int64_t>(row) * BM, static_cast<int64_t>(column) * BN, part, second};
 }
 
+// f(constant) of the one of 0..N-1 that k is, the same in every lane.
+template <int N, class F>
+__device__ __forceinline__ void each_of(int k, const F& f) {
+  if constexpr (N == 1) f(std::integral_constant<int, 0>());
+  else if (k == N - 1) f(std::integral_constant<int, N - 1>());
+  else each_of<N - 1>(k, f);
+}
+
 // The tile's results, written. Lane l of wave (wm, wn) holds in acc[i][j] four
 // consecutive columns of row 16 i + l % 16 of the wave's part; over the G tiles
 // of a group they are 4 G consecutive ones. LDS: SIZE bytes.
-template <int OP, int BM, int BN, int WM, int WN, int SIZE, class E>
+template <int OP, int BM, int BN, int WM, int WN, int SIZE, bool OWN, class E>
 __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at, uint8_t* lds,
                                            f32x4 (&acc)[BM / WM / 16][BN / WN / 16]) {
   constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
@@ -631,24 +637,37 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
   // 8 consecutive columns each of whole rows: one loop for every activation
   // instead of TI * TJ / 2 copies (3% of a 256 x 256 tile's time at K = 4096).
   constexpr int kWide = TJ * 16;
-  constexpr int kHalves = BM * BN * 4 > SIZE ? 2 : 1;
-  constexpr int kRows = TI * 16 / kHalves;
+  constexpr int kSteps = BM * BN * 4 > SIZE ? BM * BN * 4 / SIZE : 1;
+  constexpr int kRows = TI * 16 / kSteps;
   constexpr int kCols = kWide / kSums;  // outputs: a row holds those of one sum, then of the other
-  static_assert(TI % kHalves == 0 && BM * BN * 4 / kHalves <= SIZE, "the results fit");
-  __syncthreads();  // every wave is done with the tiles
+  static_assert(TI % kSteps == 0 && BM * BN * 4 / kSteps <= SIZE, "the results fit");
+  if constexpr (!OWN) __syncthreads();  // every wave is done with the tiles
   float* mine = reinterpret_cast<float*>(lds) + wave * (kRows * kWide);
+  // four columns, at pieces exchanged by the row, or 16 rows would take turns at four pieces
+  const auto place = [](uint32_t row, uint32_t col) { return row * kWide + (col ^ (row % 8 * 4)); };
   const bool whole = at.m0 + BM <= a.M && at.n0 + BN / kSums <= a.N;
   const int64_t top = at.second ? a.M : 0;  // rows in front of this half's
+  constexpr bool kByName = TJ == 8;  // one copy of all that follows, and a step's results by name
+  constexpr int kCopies = kByName ? 1 : kSteps;
+  uint32_t to[TJ];
 #pragma unroll
-  for (int half = 0; half < kHalves; ++half) {
+  for (int j = 0; j < TJ; ++j)
+    to[j] = lds_address(mine) + place(low, (j / G) * (16 * G) + g * (4 * G) + (j % G) * 4) * 4;
+#pragma unroll kCopies
+  for (int step = 0; step < kSteps; ++step) {
+    if constexpr (kByName) {
+      static_assert(TI == kSteps, "a row of tiles in a step");
+      each_of<kSteps>(step, [&](auto i) { put_row(acc[i], to); });
+    } else {
 #pragma unroll
-    for (int i = 0; i < TI / kHalves; ++i)
+      for (int i = 0; i < TI / kSteps; ++i)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        *reinterpret_cast<f32x4*>(mine + (16 * i + low) * kWide + (j / G) * (16 * G) +
-                                  g * (4 * G) + (j % G) * 4) = acc[half * (TI / kHalves) + i][j];
+        for (int j = 0; j < TJ; ++j)
+          *reinterpret_cast<f32x4*>(mine + place(16 * i + low, (j / G) * (16 * G) + g * (4 * G) + (j % G) * 4)) =
+              acc[step * (TI / kSteps) + i][j];
+    }
     wave_sync();
-    const int64_t m0 = at.m0 + wm * (TI * 16) + half * kRows;
+    const int64_t m0 = at.m0 + wm * (TI * 16) + step * kRows;
     const int64_t n0 = at.n0 + wn * kCols;
     const auto each = [&](const auto& sink) {
 #pragma unroll 2
@@ -659,8 +678,8 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
           float v[8 * kSums];
 #pragma unroll
           for (int s = 0; s < kSums; ++s) {
-            const f32x4 p = *reinterpret_cast<const f32x4*>(mine + row * kWide + s * kCols + col);
-            const f32x4 q = *reinterpret_cast<const f32x4*>(mine + row * kWide + s * kCols + col + 4);
+            const f32x4 p = *reinterpret_cast<const f32x4*>(mine + place(row, s * kCols + col));
+            const f32x4 q = *reinterpret_cast<const f32x4*>(mine + place(row, s * kCols + col + 4));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               v[8 * s + e] = p[e];
@@ -692,13 +711,13 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
   }
 }
 
-// The end of a tile kernel.
-template <int OP, int BM, int BN, int WM, int WN, int SIZE, class E>
+// The end of a tile. OWN: its LDS is the results' alone.
+template <int OP, int BM, int BN, int WM, int WN, int SIZE, bool OWN = false, class E>
 __device__ __forceinline__ void end_tile(const TileArgs<E>& a, const Place& at, uint8_t* lds,
                                          f32x4 (&acc)[BM / WM / 16][BN / WN / 16]) {
   static_assert(!E::kTakes || !E::kSplits, "whole sums");
   if constexpr (E::kTakes) a.e.template take<OP, BM / WM / 16, BN / WN / 16, WN>(a, at, acc);
-  if constexpr (E::kWrites) write_tile<OP, BM, BN, WM, WN, SIZE>(a, at, lds, acc);
+  if constexpr (E::kWrites) write_tile<OP, BM, BN, WM, WN, SIZE, OWN>(a, at, lds, acc);
 }
 
 // ---------------------------------------------------------------------------
@@ -1105,14 +1124,19 @@ __global__ __launch_bounds__(512) void linear_large_kernel(TileArgs<E> a) {
 // held there by sched_barrier. The first half of a pass (k 0..31 of 64) reads the second
 // half's values; its last instructions stand behind the barrier after which the
 // other buffer has arrived and this one is free, and the second half reads the next
-// pass's values there and loads this buffer again. An output's sums have the order that the
-// eight-wave kernel gives them.
+// pass's values there and loads this buffer again.
 //
-// 8192^3 in bf16 on one card 1502 TFLOP/s, eight waves 1444, the library 1600; 4096 x
-// 16384 x 4096 1377, 1352, 1555. A load's three steps in a row 1.5% slower; left to
-// the compiler's registers slower than eight waves. Results straight from the
-// registers to memory, for epilogues of a few instructions, instead of through LDS:
-// no difference. Matrix units are busy 85% of the loop, at 1.76 GHz: more of them,
+// A block to each compute unit goes through its tiles, and its loads and reads run on
+// through their ends: a tile's results are worked on while the next one's first passes
+// arrive, and leave through 32 KiB of LDS of their own. Blocks of one tile each had 16 us of
+// it without a matrix instruction, as much as a sixth of K = 4096. An output's sums have
+// the order that the eight-wave kernel gives them.
+//
+// 8192^3 in bf16 on one card: 1582 TFLOP/s, blocks of one tile 1502, eight waves 1476, the
+// library 1616-1641; 4096 x 16384 x 4096 1465, 1400, 1377, 1605; 4096 x 4096 x 7168 1512, 1450,
+// 1437, 1428. What is scalar between two passes in one place (the next pass's addresses) 5% of
+// the loop; a load's three steps in a row 1.5%; left to the compiler's registers slower
+// than eight waves. Matrix units are busy 85% of the loop, at 1.76 GHz: more of them,
 // and the clock gives way.
 // ---------------------------------------------------------------------------
 
@@ -1123,38 +1147,66 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(TileArgs<E> a) {
   constexpr int ELEM = 2;
   constexpr uint32_t kBuffer = (BM + BN) * kTileK;
   constexpr int G = group_of<E>(TJ), W = E::kW;
-  __shared__ __align__(1024) uint8_t lds[2][kBuffer];
-  const Place place = place_of<BM, BN / E::kSums, E::kHalves>(a);
+  constexpr int kResults = E::kWrites ? 32768 : 0;  // a row of every wave's tiles
+  __shared__ __align__(1024) uint8_t lds[2 * kBuffer + kResults];
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const uint32_t wm = wave / WN, wn = wave % WN;
   typedef Operand<BM, kThreads, TX, false, 1, true, ELEM> OpX;
   typedef Operand<BN, kThreads, TW, true, G, true, ELEM, W> OpW;
   static_assert(OpX::Q == 8 && OpW::Q == 8, "16 loads in a pass");
-  OpX lx;
-  OpW lw;
-  if constexpr (E::kHalves) lx.init(a.x, place.m0 + (place.second ? a.xupper : 0), a.M - place.m0, a);
-  else lx.init(a.x, place.m0, a);
-  lw.init(a.w, place.n0, a);
   Reader<OpX, TX, false, 1> rx;
   Reader<OpW, TW, true, G, W> rw;
   rx.init(wm * (TI * 16));
   rw.init(wn * (W == kBoth ? TJ * 8 : TJ * 16));
+  const uint32_t tiles = a.tiles_m * a.tiles_n * a.splits;
+  const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
+  const auto last_of = [&](uint32_t first) { return min(all, first + a.per_split); };
+
+  // The loads run two passes ahead, through the ends of tiles: `coming` is the tile
+  // they are of, ahead its pass, end where its passes end. Behind the block's last tile zeros
+  // are loaded, and used by no one.
+  const uint32_t blocks = gridDim.x;
+  uint32_t coming = blockIdx.x, ahead = all, end = all;
+  OpX lx;
+  OpW lw;
+  const auto aim = [&] {
+    const Place p = place_of<BM, BN / E::kSums, E::kHalves>(a, coming);
+    if constexpr (E::kHalves) lx.init(a.x, p.m0 + (p.second ? a.xupper : 0), a.M - p.m0, a);
+    else lx.init(a.x, p.m0, a);
+    lw.init(a.w, p.n0, a);
+    ahead = p.part * a.per_split;
+    end = last_of(ahead);
+  };
+  // from the end of a tile's passes to the next tile's first; a part may have none
+  const auto next = [&] {
+    do {
+      coming += blocks;
+      if (coming < tiles) {
+        aim();
+      } else {
+        ahead = all;
+        end = 0xFFFFFFFFu;  // stays there
+      }
+    } while (ahead >= end);
+  };
+  aim();
+  if (ahead >= end) next();
 
   // The values of both halves of a pass: x's tiles, then W's.
   i32x4 xf[2][TI], wf[2][TJ];
   const auto read = [&](uint32_t b, int h, int k) {
-    if (k < TI) xf[h][k] = rx.read(lds[b], k, h);
-    else wf[h][k - TI] = rw.read(lds[b] + BM * kTileK, k - TI, h);
+    if (k < TI) xf[h][k] = rx.read(lds + b * kBuffer, k, h);
+    else wf[h][k - TI] = rw.read(lds + b * kBuffer + BM * kTileK, k - TI, h);
   };
-  const uint32_t to_wave = __builtin_amdgcn_readfirstlane(lds_address(&lds[0][0]) + wave * 1024);
+  const uint32_t to_wave = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * 1024);
   const auto set = [&](uint32_t b, int k) { set_place(to_wave + b * kBuffer + k * (kThreads * 16)); };
   const auto load = [&](const typename OpX::Pass& px, const typename OpW::Pass& pw, int k) {
     if (k < 8) lx.load(px, k);
     else lw.load(pw, k - 8);
   };
-  const auto load_all = [&](uint32_t kt, uint32_t b) {
-    const auto px = lx.pass(kt);
-    const auto pw = lw.pass(kt);
+  const auto load_all = [&](uint32_t b) {
+    const auto px = lx.pass(ahead);
+    const auto pw = lw.pass(ahead);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       set(b, k);
@@ -1162,45 +1214,52 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(TileArgs<E> a) {
       load(px, pw, k);
     }
   };
-  f32x4 acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-  const uint32_t all = (a.kbytes + kTileK - 1) / kTileK;
-  const uint32_t first = place.part * a.per_split;
-  const uint32_t last = min(all, first + a.per_split);
-  load_all(first, 0);
+  load_all(0);
+  if (++ahead >= end) next();
   wait_tiles<0>();
-  load_all(first + 1, 1);
+  load_all(1);
 #pragma unroll
   for (int k = 0; k < 16; ++k) read(0, 0, k);
-  acc_ready(acc);
-  for (uint32_t kt = first; kt < last; ++kt) {
-    const uint32_t b = (kt - first) & 1;
-    // past the last tile: zeros are loaded and old values read, and neither is used
-    const auto px = lx.pass(kt + 2);
-    const auto pw = lw.pass(kt + 2);
+  uint32_t b = 0;
+  for (uint32_t id = blockIdx.x; id < tiles; id += blocks) {
+    const Place place = place_of<BM, BN / E::kSums, E::kHalves>(a, id);
+    f32x4 acc[TI][TJ];
 #pragma unroll
-    for (int k = 0; k < 64; ++k) {
-      if (k % 2 == 0 && k < 32) read(b, 1, k / 2);
-      if (k == 56) wait_tiles<0>();
-      mma_in_place<OP>(acc[k % 8][k / 8], wf[0][k / 8], xf[0][k % 8]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int k = 0; k < 64; ++k) {
-      if (k % 4 == 0) read(b ^ 1, 0, k / 4);
-      if (k % 4 == 1) set(b, k / 4);
-      if (k % 4 == 2) load(px, pw, k / 4);
-      mma_in_place<OP>(acc[k % 8][k / 8], wf[1][k / 8], xf[1][k % 8]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    acc_ready(acc);
+    const uint32_t first = place.part * a.per_split, last = last_of(first);
+    for (uint32_t kt = first; kt < last; ++kt, b ^= 1) {
+      const auto multiply = [&](int h, int k) {
+        mma_in_place<OP>(acc[k % 8][k / 8], wf[h][k / 8], xf[h][k % 8]);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+#pragma unroll
+      for (int k = 0; k < 36; ++k) {
+        if (k % 2 == 0 && k < 32) read(b, 1, k / 2);
+        multiply(0, k);
+      }
+      if (++ahead >= end) next();
+      const auto px = lx.pass(ahead);
+      const auto pw = lw.pass(ahead);
+#pragma unroll
+      for (int k = 36; k < 64; ++k) {
+        if (k == 56) wait_tiles<0>();
+        multiply(0, k);
+      }
+#pragma unroll
+      for (int k = 0; k < 64; ++k) {
+        if (k % 4 == 0) read(b ^ 1, 0, k / 4);
+        if (k % 4 == 1) set(b, k / 4);
+        if (k % 4 == 2) load(px, pw, k / 4);
+        multiply(1, k);
+      }
     }
+    acc_ready(acc);
+    end_tile<OP, BM, BN, 2, WN, kResults, true>(a, place, lds + 2 * kBuffer, acc);
   }
   wait_tiles<0>();  // nothing arrives in LDS any more
-  acc_ready(acc);
-  end_tile<OP, BM, BN, 2, WN, 2 * static_cast<int>(kBuffer)>(a, place, &lds[0][0], acc);
 }
 
 // The parts of a split sum, added in ascending order, and the epilogue. One wave

@@ -285,6 +285,8 @@ hipError_t launch_medium(const TileArgs<E>& a, hipStream_t s, hipEvent_t start, 
   return launch_tile<OP, 128, 128, 2, 2, kMediumStages, TX, TW>(a, s, start, stop);
 }
 
+constexpr uint32_t kUnits = 256;  // compute units: blocks of the wide kernel at once
+
 // The large tiles are loaded straight into LDS only; other operands go through
 // the medium tiles, whose sums have the same order.
 template <int OP, bool TX, bool TW, class E>
@@ -292,7 +294,8 @@ hipError_t launch_large(TileArgs<E> a, hipStream_t s, hipEvent_t start, hipEvent
   if (!straight<OP, TX, TW>(a)) return launch_medium<OP, TX, TW>(a, s, start, stop);
   const dim3 grid = tile_grid<256, 256>(a);
   if constexpr (wide_tiles(OP))
-    return launch_kernel(linear_wide_kernel<OP, TX, TW, E>, grid, dim3(256), s, start, stop, a);
+    return launch_kernel(linear_wide_kernel<OP, TX, TW, E>, dim3(grid.x < kUnits ? grid.x : kUnits),
+                         dim3(256), s, start, stop, a);
   else
     return launch_kernel(linear_large_kernel<OP, E>, grid, dim3(512), s, start, stop, a);
 }

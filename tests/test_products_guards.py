@@ -64,14 +64,7 @@ def test_no_immediate_overwrite_of_wide_store_data(asm):
 
 def lines_of(body: str):
     """(instruction, whether it is inline assembly's) of a kernel."""
-    inside = False
-    for line in body.splitlines():
-        if ";;#ASMSTART" in line or ";;#ASMEND" in line:
-            inside = ";;#ASMSTART" in line
-            continue
-        code = line.split(";", 1)[0].strip()
-        if code and not code.startswith(".") and not code.endswith(":"):
-            yield code, inside
+    return [line for code, _ in blocks_of(body).values() for line in code]
 
 
 def test_only_the_inline_assembly_uses_m0(asm):
@@ -101,35 +94,83 @@ def registers(text: str, file: str) -> set[int]:
     return got
 
 
+WAIT = 32      # cycles from a matrix instruction in inline assembly to another access to its result
+DISTANCE = 3   # instructions from a vector instruction to a matrix instruction that reads what it wrote
+
+
+def blocks_of(body: str):
+    """The kernel's basic blocks: {name: ([(instruction, in inline assembly)], [names of those that follow])}."""
+    blocks, name, inside, count = {}, "", False, 0
+    blocks[name] = ([], [])
+    for line in body.splitlines():
+        if ";;#ASMSTART" in line or ";;#ASMEND" in line:
+            inside = ";;#ASMSTART" in line
+            continue
+        code = line.split(";", 1)[0].strip()
+        label = re.match(r"(\.L\w+):", code)
+        if label:
+            blocks[name][1].append(label[1])
+            name = label[1]
+            blocks[name] = ([], [])
+        elif code and not code.startswith(".") and not code.endswith(":"):
+            blocks[name][0].append((code, inside))
+            jump = re.match(r"s_(c?)branch\S*\s+(\S+)", code)
+            if jump or code.startswith("s_endpgm"):
+                if jump:
+                    blocks[name][1].append(jump[2])
+                count += 1
+                after = f"after jump {count}"
+                if jump and jump[1]:
+                    blocks[name][1].append(after)
+                name = after
+                blocks[name] = ([], [])
+    return blocks
+
+
 def mfma_hazards(body: str) -> tuple[int, list[str]]:
-    """How many matrix instructions are inline assembly's, and what reaches one of them, or its result, too soon:
-    the compiler does not see them, so it keeps none of the distances that it would keep from its own. A vector
-    instruction that writes an operand stands at least three instructions ahead; an instruction that reads a result
-    or writes it otherwise stands behind a wait of 32 cycles, as does a jump back to code that would."""
-    code = list(lines_of(body))
-    ours = [k for k, (c, inside) in enumerate(code) if inside and c.startswith("v_mfma")]
-    bad = []
-    for k in ours:
-        dest, *sources = [o.strip() for o in code[k][0].split(" ", 1)[1].split(", ")]
-        for c, _ in code[max(0, k - 3):k]:
-            if c.startswith("v_") and not c.startswith("v_mfma"):
-                to = c.split(" ", 1)[1].split(",")[0]
-                if any(registers(to, f) & registers(" ".join(sources), f) for f in "va"):
-                    bad.append(f"{c} before {code[k][0]}")
-    if ours:
-        results = set().union(*(registers(code[k][0].split(",")[0], "a") for k in ours))
-        waited = 0
-        for c, inside in code[ours[-1] + 1:]:
-            if c.startswith("s_nop"):
-                waited += int(c.split()[1]) + 1
-            elif waited < 32 and registers(c, "a") & results:
-                bad.append(f"{c} after {waited} cycles")
-                break
-        # between the first and the last of them nothing else touches a result
-        for c, inside in code[ours[0]:ours[-1]]:
-            if not (inside and c.startswith("v_mfma")) and registers(c, "a") & results:
-                bad.append(f"{c} among them")
-    return len(ours), bad
+    """How many matrix instructions are inline assembly's, and what reaches one of them, or its result, too soon on
+    some way through the kernel: the compiler does not see them, so it keeps none of the distances that it would keep
+    from its own. A vector instruction that writes an operand stands DISTANCE instructions ahead; an instruction that
+    reads a result or writes it otherwise stands WAIT cycles behind, an instruction other than s_nop counted as one."""
+    blocks = blocks_of(body)
+    ours = {c for code, _ in blocks.values() for c, inside in code if inside and c.startswith("v_mfma")}
+    parts = {c: [o.strip() for o in c.split(" ", 1)[1].split(", ")] for c in ours}
+    results = set().union(set(), *(registers(p[0], "a") for p in parts.values()))
+    reads = {c: {(f, r) for f in "va" for r in registers(" ".join(p[1:]), f)} for c, p in parts.items()}
+    bad = set()
+
+    def through(code, left, written):
+        """State behind a block: cycles that a result still takes, and {register: instructions that it still takes}."""
+        for c, inside in code:
+            if inside and c.startswith("v_mfma"):
+                if reads[c] & set(written):
+                    bad.add(f"an operand of {c} is written just before it")
+                left = WAIT
+            elif left and registers(c, "a") & results:
+                bad.add(f"{c} with {left} cycles to go")
+            passed = int(c.split()[1]) + 1 if c.startswith("s_nop") else 1
+            left = max(0, left - passed)
+            written = {r: n - passed for r, n in written.items() if n > passed}
+            if c.startswith("v_") and not (inside and c.startswith("v_mfma")):
+                to = c.split(" ", 1)[1].split(",")[0] if " " in c else ""
+                written |= {(f, r): DISTANCE for f in "va" for r in registers(to, f)}
+        return left, written
+
+    states = {name: None for name in blocks}
+    states[""] = (0, {})
+    todo = [""]
+    while todo:
+        name = todo.pop()
+        code, follow = blocks[name]
+        left, written = through(code, *states[name])
+        for f in follow:
+            old = states[f]
+            merged = (left, written) if old is None else (
+                max(left, old[0]), {r: max(written.get(r, 0), old[1].get(r, 0)) for r in set(written) | set(old[1])})
+            if merged != old:
+                states[f] = merged
+                todo.append(f)
+    return sum(1 for code, _ in blocks.values() for c, inside in code if inside and c.startswith("v_mfma")), sorted(bad)
 
 
 def test_matrix_instructions_in_assembly_are_waited_for(asm):
@@ -142,16 +183,33 @@ def test_matrix_instructions_in_assembly_are_waited_for(asm):
     assert found > 0
 
 
+def test_only_the_tiles_are_waited_for_in_a_pass(asm):
+    """A load that an epilogue leaves on its way is waited for in every pass of the next tile, and the tile's own with it."""
+    for name, body in kernel_blocks(asm).items():
+        if "linear_wide_kernel" in name:
+            for code, _ in blocks_of(body).values():
+                if any(c.startswith("v_mfma") for c, _ in code):
+                    assert not [c for c, inside in code if "vmcnt" in c and not inside], name
+
+
 def test_hazard_scan_detects_the_pattern():
     mfma = ";;#ASMSTART\n\tv_mfma_f32_16x16x32_bf16 a[0:3], v[4:7], v[8:11], a[0:3]\n;;#ASMEND\n"
     wait = ";;#ASMSTART\n\ts_nop 15\n\ts_nop 15\n;;#ASMEND\n"
     read = "\tv_accvgpr_read_b32 v1, a2\n"
-    assert mfma_hazards(mfma + wait + read) == (1, [])
+    nops = "\ts_nop 0\n\ts_nop 0\n\ts_nop 0\n"
+    end = "\ts_endpgm\n"
+    assert mfma_hazards(mfma + wait + read + end) == (1, [])
     assert mfma_hazards(mfma + read)[1] and mfma_hazards(mfma + "\ts_nop 15\n" + read)[1]
     assert mfma_hazards("\tv_mov_b32_e32 v9, v1\n" + mfma + wait)[1]
     assert mfma_hazards("\tv_accvgpr_write_b32 a1, v1\n\ts_nop 0\n" + mfma + wait)[1]
-    assert not mfma_hazards("\tv_mov_b32_e32 v9, v1\n\ts_nop 0\n\ts_nop 0\n\ts_nop 0\n" + mfma + wait)[1]
+    assert not mfma_hazards("\tv_mov_b32_e32 v9, v1\n" + nops + mfma + wait)[1]
     assert mfma_hazards(mfma + read + mfma + wait)[1]
+    # through jumps: out of a loop past its wait, and back into it
+    loop = ".LBB0_1:\n" + mfma + "\ts_cbranch_scc1 .LBB0_1\n"
+    assert not mfma_hazards(loop + wait + read + end)[1]
+    assert mfma_hazards(loop + "\ts_branch .LBB0_3\n.LBB0_2:\n" + wait + end + ".LBB0_3:\n" + read + end)[1]
+    assert not mfma_hazards(loop + "\ts_branch .LBB0_3\n.LBB0_2:\n" + read + end + ".LBB0_3:\n" + wait + end)[1]
+    assert mfma_hazards(nops + ".LBB0_1:\n" + mfma + nops + "\tv_mov_b32_e32 v5, v1\n\ts_cbranch_scc1 .LBB0_1\n" + wait + end)[1]
 
 
 @pytest.mark.parametrize("name", sorted(LIBRARIES))
