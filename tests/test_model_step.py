@@ -166,3 +166,22 @@ def test_large_tiles_give_the_medium_tiles_bytes(device, kind, M, N, K):
             make(*args, out, launch={"kernel": kernel, "splits": 1}, **scales)
             outs.append(out)
         assert R.same_bytes(*outs)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K,splits", [(4100, 4104, 40, 1), (4100, 4104, 104, 1), (1024, 1031, 4480, 33), (300, 520, 640, 7),
+                                          (1024, 2050, 64, 1)])
+def test_large_tiles_one_after_another(device, M, N, K, splits):
+    """More tiles than blocks, of one and of two passes, and parts of the sum without any: the loads run ahead through all of them."""
+    from hyper_connection_residual_mhc_amd import linear
+    from hyper_connection_residual_mhc_amd._lib import MHC_LINEAR_LARGE, MHC_LINEAR_MEDIUM
+    say(f"tiles in turn {M} x {N} x {K} in {splits}")
+    gen = torch.Generator().manual_seed(M + K)
+    x, w, b = (R.normal(gen, *s).to(device) for s in ((M, K), (N, K), (N,)))
+    outs = []
+    for kernel in (MHC_LINEAR_LARGE, MHC_LINEAR_MEDIUM):
+        out = torch.full((M, N), 7.0, dtype=BF16, device=device)
+        linear.mhc_linear_fwd(x, w, out, bias=b, launch={"kernel": kernel, "splits": splits})
+        outs.append(out)
+    assert R.same_bytes(*outs)
+    near(outs[0][::37], x[::37].cpu().double() @ w.cpu().double().t() + b.cpu().double(), H16, "product")
