@@ -670,7 +670,8 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
     const int64_t m0 = at.m0 + wm * (TI * 16) + step * kRows;
     const int64_t n0 = at.n0 + wn * kCols;
     const auto each = [&](const auto& sink) {
-#pragma unroll 2
+      constexpr int kAhead = TJ == 8 ? 4 : 2;  // chunks whose other inputs are loaded together: four waves have no others to wait under
+#pragma unroll kAhead
       for (uint32_t id = lane; id < kRows * kCols / 8; id += 64) {
         const uint32_t row = id / (kCols / 8), col = id % (kCols / 8) * 8;
         const int64_t m = m0 + row, n = n0 + col;
