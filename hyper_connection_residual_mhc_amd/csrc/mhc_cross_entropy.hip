@@ -18,15 +18,14 @@ namespace {
 
 constexpr float kLog2E = 1.44269504f, kLn2 = 0.69314718f;
 
-// exp(a - b), 1 where they are the same infinity. The difference comes before
+// exp(a - b), NaN where they are the same infinity. The difference comes before
 // the product with log2(e): rounding a log2(e) and b log2(e) apart would put an
 // error that grows with |a| into every term of a row.
 __device__ __forceinline__ float exp_of(float a, float b) {
-  const float d = a == b ? 0.0f : a - b;
-  return __builtin_amdgcn_exp2f(d * kLog2E);
+  return __builtin_amdgcn_exp2f((a - b) * kLog2E);
 }
 
-// 2^(a - b), 1 where they are the same infinity.
+// 2^(a - b), 1 where they are the same infinity: of sums that are joined.
 __device__ __forceinline__ float exp2_of(float a, float b) {
   return __builtin_amdgcn_exp2f(a == b ? 0.0f : a - b);
 }
@@ -160,12 +159,14 @@ struct StatEpilogue {
     const float below = m - kHeld;
     float s = 0.0f;
     if (__any(fabsf(m) == INFINITY)) {
-      // terms at an infinite maximum are 2^15, which leaves lse that infinity
+      // terms at an infinite maximum count as 2^15, which leaves lse that infinity; exp(inf - inf)
+      // has no value, and where it stands NaN is held (ce_grad_kernel sees a row of -inf alone)
 #pragma unroll
       for (int k = 0; k < kTiles * 4; ++k) {
         const float y = v[k] * kLog2E;
         v[k] = __builtin_amdgcn_exp2f(y == m ? kHeld : y - below);
         s = s + v[k];
+        v[k] = y == INFINITY ? NAN : v[k];
       }
     } else {
 #pragma unroll
@@ -243,6 +244,7 @@ struct RowStatEpilogue {
         const float z = v[e] * kLog2E;
         v[e] = __builtin_amdgcn_exp2f(z == top ? kHeld : fmaf(v[e], kLog2E, -below));
         s = s + v[e];
+        v[e] = z == INFINITY ? NAN : v[e];  // see StatEpilogue
       }
       stats[m * groups + n / 8] = {below, s};
       if constexpr (HOLD) {
@@ -423,7 +425,9 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(
     typename Store<F>::type* const p = held + row * ld + n;
     float v[8];
     widen_chunk<kF16>(load_chunk<kF16>(p, 8), v);
-    const float f = exp2_of(stats[(n >> group_bits) * along + row * up].m, l) * w.a;
+    // 1 at an infinite lse, whose terms are 0 or NaN; NaN where all logits are -inf
+    const float m = stats[(n >> group_bits) * along + row * up].m;
+    const float f = __builtin_amdgcn_exp2f(m == l && m == INFINITY ? 0.0f : m - l) * w.a;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = v[e] * f;

@@ -10,7 +10,8 @@
  *            = sum of l / C                MHC_REDUCTION_MEAN                   (fp32 [1])
  * with C the number of rows whose target is not ignore_index (the mean over none
  * is NaN). x and W are MHC_LINEAR_BF16 or MHC_LINEAR_F16. Sums, exponentials
- * and logarithms are fp32; an infinite logit follows the formulas.
+ * and logarithms are fp32; an infinite logit follows the formulas (lse is +inf where one
+ * is +inf and -inf where all are -inf, and G is NaN where z and lse are the same infinity).
  *
  * Gradients, from grad_loss (fp32, [M] or [1] as loss is; NULL stands for 1):
  *     s[m]        = grad_loss[m] (NONE), grad_loss (SUM), grad_loss / C (MEAN); 0 where the target is ignored

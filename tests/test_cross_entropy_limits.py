@@ -1,0 +1,144 @@
+"""The cross entropy (include/mhc_cross_entropy.h) where logits or gradients leave the
+ordinary: infinite logits, finite ones so large that fp32 holds them in steps of 2 or
+more, shares whose sum is what has to fit 16 bits.
+
+Inputs are made so that every logit is exact in fp32 (products and their partial sums
+are), so a probability is off by what its exponentials, sums and roundings cost alone:
+`REL` for the chain of the forward's sums (see test_cross_entropy.py: fewer than 64 steps
+of 8 u), half a step of fp16 where it was held there, then half a step of G's type and
+of the gradient's. Where the formula gives NaN or an infinity, so does the kernel.
+"""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import sublayer_ref as R
+from gpu_util import say
+from hyper_connection_residual_mhc_amd import _lib
+from test_linear import LARGE, MEDIUM, ROWS, SMALL, STEP, additions
+
+BF16, F16 = torch.bfloat16, torch.float16
+SHORT = _lib.MHC_LINEAR_SHORT
+TYPES = {"bf16": BF16, "f16": F16}
+REL = 64 * 8 * R.U32
+IGNORE = -100
+
+
+def product(a, b):
+    """a @ b by single products, so that 0 times an infinity is there as NaN."""
+    return (a[:, :, None] * b[None]).sum(1)
+
+
+def formula(x, w, targets, s, e=None):
+    """(lse, each row's loss, G, a p), fp64, of logits as fp32 has them."""
+    z = product(x.double(), w.double().t())
+    z = torch.where(z.abs() > 3.4028235e38, torch.sign(z) * math.inf, z)
+    lse = torch.logsumexp(z, 1)
+    rows = torch.arange(len(x))
+    each = torch.where(targets != IGNORE, lse - z[rows, targets.clamp(0)], torch.zeros_like(lse))
+    a = s if e is None else s + e
+    ap = a[:, None] * torch.exp(z - lse[:, None])
+    g = ap.clone()
+    g[rows, targets.clamp(0)] -= s
+    g[(a == 0) & (s == 0)] = 0
+    return lse, each, g, ap
+
+
+def check(got, x, w, g, ap, t, held, a_most):
+    """(grad_x, grad_weight) against G's products."""
+    xv, wv = x.double(), w.double()
+    rel = REL + (R.HALF_STEP[F16] if held else 0)
+    # fp16 shares are scaled to 2^13 at least, so that next to zero G is off by half of its smallest number over that
+    dg = ap.abs() * rel + (g.abs() + ap.abs() * rel) * R.HALF_STEP[t] + R.HALF_TINY[t] * (a_most * 2.0 ** -13 if t == F16 else 1)
+    dg = torch.nan_to_num(dg)
+    if held:
+        dg = dg + ap.nan_to_num().abs().amax(1, keepdim=True) * 2.0 ** -40
+    clean = lambda v: torch.nan_to_num(v, posinf=0.0, neginf=0.0)  # noqa: E731
+    for name, out, want, left, right, dl in (
+            ("grad_x", got[0], product(g, wv), g, wv, dg), ("grad_weight", got[1], product(g.t(), xv), g.t(), xv, dg.t())):
+        size = clean(left).abs() @ clean(right).abs()
+        tol = dl @ clean(right).abs() + size * additions(left.shape[1], 32) * STEP
+        # half a step past the type's largest number (3.39e38 in bf16) a value is an infinity
+        past = want.abs() >= torch.finfo(t).max * (1 + torch.finfo(t).eps / 4)
+        want = torch.where(past, torch.sign(want) * math.inf, want)
+        # terms that together pass fp32's largest number have partial sums that may, whatever they come to: 1.33 p 3e38 over
+        # all other columns is 3.9e38, which the target's column takes back
+        any_value = (size > torch.finfo(torch.float32).max) & torch.isfinite(want)
+        out = torch.where(any_value, want, out.double().cpu())
+        R.assert_within(out, want, tol + R.rounding(clean(want).abs() + tol, t), name)
+
+
+def calls(device, x, w, targets, s, kernel, lse=None):
+    """The loss and its gradients in one call, and the gradients from lse (the forward's unless given)."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    x, w, targets, s = x.to(device), w.to(device), targets.to(device), s.float().to(device)
+    value, made = torch.empty(len(x), device=device), torch.empty(len(x), device=device)
+    gx, gw, bx, bw = torch.empty_like(x), torch.empty_like(w), torch.empty_like(x), torch.empty_like(w)
+    launch = {"kernel": kernel} if kernel else None
+    C.mhc_cross_entropy_grads(x, w, targets, value, made, s, grad_x=gx, grad_weight=gw, reduction="none", launch=launch)
+    C.mhc_cross_entropy_bwd(x, w, targets, made if lse is None else lse.to(device), s, grad_x=bx, grad_weight=bw, reduction="none",
+                            launch=None if kernel == ROWS else launch)
+    torch.cuda.synchronize()
+    return value, made, (gx, gw), (bx, bw)
+
+
+KERNELS = [ROWS, SHORT, SMALL, MEDIUM, LARGE]
+
+
+# ---------------------------------------------------------------------------
+# Infinite logits
+# ---------------------------------------------------------------------------
+
+def infinite(kind, case, M, V):
+    """x, W, targets, s. `above`: two logits of row 0 are inf, its target one of them; of row 1 the target alone; of row 2
+    one that is not its target; a row that counts for nothing has some as well. `below`: all of row 0 is -inf, of row 1
+    its target alone. `nan`: row 0; one logit of row 1 is inf, all others are NaN."""
+    x, w = torch.zeros(M, 8, dtype=TYPES[kind]), torch.zeros(V, 8, dtype=TYPES[kind])
+    x[:, 3] = torch.arange(M) % 3 - 1.0
+    w[:, 3] = torch.arange(V) % 5 * 0.5
+    targets = torch.arange(M) % V
+    s = torch.linspace(0.5, 1.5, M, dtype=torch.float64)
+    s[::2] *= -1
+    # bf16 overflows in the product; fp16 has infinities in x, times values that are not 0
+    high = 3e38 if kind == "bf16" else 1.0
+    if case == "above" and kind == "bf16":
+        w[[1, V - 1], 0], x[0, 0] = high, high
+        w[4, 1], x[1, 1], x[2, 1], x[M - 1, 1] = high, high, high, high
+        targets[0], targets[1], targets[2], targets[M - 1] = V - 1, 4, 3, IGNORE
+    elif case == "above":
+        # an infinity in W meets every row: +inf in rows 0, 1 and the last, -inf in the others
+        w[4, 0] = math.inf
+        x[:, 0] = -1
+        x[[0, 1, M - 1], 0] = 1
+        targets[0], targets[1], targets[M - 1] = 4, 2, IGNORE
+    elif case == "below":
+        w[:, 2], x[0, 2] = (-high, high) if kind == "bf16" else (1.0, -math.inf)
+        if kind == "bf16":
+            w[5, 1], x[1, 1] = -high, high
+            targets[1] = 5
+    else:
+        x[0, 5], x[1, 5], w[3, 5] = math.nan, math.inf, 1.0
+    return x, w, targets, s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("case", ["above", "below", "nan"])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_infinite_logits_have_the_formula_s_gradients(device, kind, case, kernel):
+    """NaN where z - lse has no value, in G's own places and in both calls alike; a row that counts for nothing stays 0."""
+    for M, V in ((7, 12), (7, 150)) if kernel == ROWS else ((70, 150), (40, 300)):
+        say(f"infinite logits {kind} {case} kernel={kernel} M={M} V={V}")
+        x, w, targets, s = infinite(kind, case, M, V)
+        s = torch.where(targets == IGNORE, torch.zeros_like(s), s)
+        lse, each, g, ap = formula(x, w, targets, s)
+        value, made, one, two = calls(device, x, w, targets, s, kernel)
+        R.assert_within(made, lse, lse.abs().nan_to_num(posinf=0) * 4 * R.U32 + REL, "lse")
+        R.assert_within(value, each, each.abs().nan_to_num(posinf=0) * 4 * R.U32 + REL, "loss")
+        assert torch.isnan(g).any()
+        check(one, x, w, g, ap, w.dtype, True, 1.5)
+        check(two, x, w, g, ap, w.dtype, False, 1.5)
