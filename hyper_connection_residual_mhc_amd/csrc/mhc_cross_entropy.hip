@@ -20,30 +20,35 @@ constexpr float kLog2E = 1.44269504f, kLn2 = 0.69314718f;
 
 // exp(a - b), NaN where they are the same infinity. The difference comes before
 // the product with log2(e): rounding a log2(e) and b log2(e) apart would put an
-// error that grows with |a| into every term of a row.
+// error that grows with |a| into every term of a row (half a step of 1e7 is e^(1/2)),
+// and would overflow from 2.36e38 on.
 __device__ __forceinline__ float exp_of(float a, float b) {
   return __builtin_amdgcn_exp2f((a - b) * kLog2E);
 }
 
-// 2^(a - b), 1 where they are the same infinity: of sums that are joined.
-__device__ __forceinline__ float exp2_of(float a, float b) {
-  return __builtin_amdgcn_exp2f(a == b ? 0.0f : a - b);
+// The same, 1 where they are the same infinity: of sums that are joined.
+__device__ __forceinline__ float ratio_of(float a, float b) {
+  return __builtin_amdgcn_exp2f((a == b ? 0.0f : a - b) * kLog2E);
 }
 
-// A group of columns: s is the sum of 2^(z log2(e) - m), with m 15 below the
-// largest z log2(e). Everything up to lse stays in powers of two, where a term is one
-// fused multiply-add and one exponential whatever m was rounded to; log2(e)'s own
-// rounding scales all logits alike and moves lse by 2^-25 of the row's entropy.
+// A group of columns: its largest logit, and the sum of exp(z - m) 2^15. Of a row:
+// the same of all its columns, of which lse is m + log(s / 2^15).
 struct Stat {
   float m, s;
 };
 
 // The exponentials that the workspace holds between the logits and G are those
-// terms, at most 2^15, in fp16, of either type of x: fp16's rounding is an eighth of
+// terms, at most 2^15 (the largest logit's is just that, whatever fp32 makes of
+// m - 15), in fp16, of either type of x: fp16's rounding is an eighth of
 // bf16's, which G then adds (held in bf16 the gradients at 4096 x 131072 x 4096 were
 // 0.0027 off by the norm, so 0.0024; the output's own rounding is 0.0017). What is 2^-29
 // of a group's largest is a normal number, and what is below 2^-40 of it counts as 0.
 constexpr float kHeld = 15.0f;
+
+// The term of z in a group whose largest logit is m, neither of them infinite.
+__device__ __forceinline__ float term_of(float z, float m) {
+  return __builtin_amdgcn_exp2f(fmaf(z - m, kLog2E, kHeld));
+}
 
 // Several groups at once: one exponential each, and one for what was there.
 template <int K>
@@ -51,15 +56,15 @@ __device__ __forceinline__ Stat join_all(const Stat& a, const Stat (&b)[K]) {
   float m = a.m;
 #pragma unroll
   for (int k = 0; k < K; ++k) m = fmaxf(m, b[k].m);
-  float s = a.s * exp2_of(a.m, m);
+  float s = a.s * ratio_of(a.m, m);
 #pragma unroll
-  for (int k = 0; k < K; ++k) s = s + b[k].s * exp2_of(b[k].m, m);
+  for (int k = 0; k < K; ++k) s = s + b[k].s * ratio_of(b[k].m, m);
   return {m, s};
 }
 
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   const float m = fmaxf(a.m, b.m);
-  return {m, a.s * exp2_of(a.m, m) + b.s * exp2_of(b.m, m)};
+  return {m, a.s * ratio_of(a.m, m) + b.s * ratio_of(b.m, m)};
 }
 
 // What of its row's gradient a probability (a) and the target's place (b) get.
@@ -73,8 +78,8 @@ struct Share {
 // The product's kernels with an epilogue that never writes a logit: each wave
 // takes the largest of its 64 (or 32) columns of a row and the sum of exponentials
 // under it from its registers, and the target's logit where it is among them. For
-// the gradients the exponentials themselves, at most 1 by that maximum, are
-// written in 16 bits: a later pass only has to scale them.
+// the gradients the exponentials themselves (see kHeld) are written in 16 bits: a
+// later pass only has to scale them.
 // ---------------------------------------------------------------------------
 
 // Epilogue of the tile kernels. Groups of columns are a wave's; their statistics
@@ -146,7 +151,7 @@ struct StatEpilogue {
     float m = v[0];
 #pragma unroll
     for (int k = 1; k < kTiles * 4; ++k) m = fmaxf(m, v[k]);
-    m = across_max(m) * kLog2E;
+    m = across_max(m);
     if (row < M) {
       const int64_t t = targets[row] - first;
       if (t >= 0 && t < left && t / 8 % 4 == g) {
@@ -156,27 +161,25 @@ struct StatEpilogue {
         target_logit[row] = at_t;
       }
     }
-    const float below = m - kHeld;
     float s = 0.0f;
     if (__any(fabsf(m) == INFINITY)) {
       // terms at an infinite maximum count as 2^15, which leaves lse that infinity; exp(inf - inf)
       // has no value, and where it stands NaN is held (ce_grad_kernel sees a row of -inf alone)
 #pragma unroll
       for (int k = 0; k < kTiles * 4; ++k) {
-        const float y = v[k] * kLog2E;
-        v[k] = __builtin_amdgcn_exp2f(y == m ? kHeld : y - below);
-        s = s + v[k];
-        v[k] = y == INFINITY ? NAN : v[k];
+        const float t = v[k] == m ? 0x1p15f : term_of(v[k], m);
+        s = s + t;
+        v[k] = v[k] == INFINITY ? NAN : t;
       }
     } else {
 #pragma unroll
       for (int k = 0; k < kTiles * 4; ++k) {
-        v[k] = __builtin_amdgcn_exp2f(fmaf(v[k], kLog2E, -below));
+        v[k] = term_of(v[k], m);
         s = s + v[k];
       }
     }
     s = across_sum(s);
-    if (g == 0 && row < M) out[row] = {below, s};
+    if (g == 0 && row < M) out[row] = {m, s};
     if constexpr (HOLD) {
       if (row < M) {
 #pragma unroll
@@ -236,17 +239,14 @@ struct RowStatEpilogue {
         if (e >= count) v[e] = -INFINITY;
         top = fmaxf(top, v[e]);
       }
-      top = top * kLog2E;
-      const float below = top - kHeld;
       float s = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = v[e] * kLog2E;
-        v[e] = __builtin_amdgcn_exp2f(z == top ? kHeld : fmaf(v[e], kLog2E, -below));
-        s = s + v[e];
-        v[e] = z == INFINITY ? NAN : v[e];  // see StatEpilogue
+        const float t = v[e] == top ? 0x1p15f : term_of(v[e], top);
+        s = s + t;
+        v[e] = v[e] == INFINITY ? NAN : t;  // see StatEpilogue
       }
-      stats[m * groups + n / 8] = {below, s};
+      stats[m * groups + n / 8] = {top, s};
       if constexpr (HOLD) {
         Chunk<kF16> c;
         narrow_chunk<kF16>(v, c);
@@ -302,7 +302,7 @@ template <int R>
 __global__ __launch_bounds__(1024) void ce_lse_kernel(const Stat* __restrict__ stats,
                                                       const float* __restrict__ target_logit,
                                                       const int64_t* __restrict__ targets,
-                                                      float* __restrict__ lse, float* __restrict__ lse2,
+                                                      float* __restrict__ lse, Stat* __restrict__ whole,
                                                       float* __restrict__ loss, int64_t M, int64_t V, int64_t groups, int64_t up,
                                                       int64_t along, int64_t ignore_index) {
   constexpr int kEach = 1024 / R;
@@ -330,12 +330,13 @@ __global__ __launch_bounds__(1024) void ce_lse_kernel(const Stat* __restrict__ s
   }
   if (k == 0 && row < M) {
     all = part[threadIdx.x];
-    // with the largest term at 1 the logarithm is small, and rounded as finely
-    const float l2 = (all.m + kHeld) + __log2f(all.s * 0x1p-15f), l = l2 * kLn2;
-    lse[row] = l;
-    lse2[row] = l2;
+    // with the largest term at 1 the logarithm is small, and rounded as finely; the loss takes
+    // it after the logits' difference, which does not see how large they are
+    const float log = __log2f(all.s * 0x1p-15f) * kLn2;
+    lse[row] = all.m + log;
+    whole[row] = all;
     const int64_t t = targets[row];
-    loss[row] = t == ignore_index ? 0.0f : t >= 0 && t < V ? l - target_logit[row] : NAN;
+    loss[row] = t == ignore_index ? 0.0f : t >= 0 && t < V ? (all.m - target_logit[row]) + log : NAN;
   }
 }
 
@@ -409,13 +410,14 @@ __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
 // `segment` columns, 128 of each row at a time: the groups' 16 rows are one line.
 template <int F>
 __global__ __launch_bounds__(256) void ce_grad_kernel(
-    const Stat* __restrict__ stats, const float* __restrict__ lse2, const Share* __restrict__ shares,
+    const Stat* __restrict__ stats, const Stat* __restrict__ whole, const Share* __restrict__ shares,
     const int64_t* __restrict__ targets, typename Store<F>::type* __restrict__ held, int64_t M,
     int64_t V, int64_t ld, int64_t segment, int group_bits, int64_t up, int64_t along) {
   const int64_t row = static_cast<int64_t>(blockIdx.y) * 16 + threadIdx.x / 16;
   if (row >= M) return;
   const Share w = shares[row];
-  const float l = lse2[row];
+  const Stat all = whole[row];
+  const float share = w.a / all.s;
   const int64_t t = targets[row];
   const bool none = w.a == 0.0f && w.b == 0.0f;
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * segment + threadIdx.x % 16 * 8;
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(
     widen_chunk<kF16>(load_chunk<kF16>(p, 8), v);
     // 1 at an infinite lse, whose terms are 0 or NaN; NaN where all logits are -inf
     const float m = stats[(n >> group_bits) * along + row * up].m;
-    const float f = __builtin_amdgcn_exp2f(m == l && m == INFINITY ? 0.0f : m - l) * w.a;
+    const float f = (m == all.m && m == INFINITY ? 1.0f : exp_of(m, all.m)) * share;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       v[e] = v[e] * f;
@@ -516,7 +518,7 @@ struct Plan {
   bool pad;                      // rows along K are copied whole
   int64_t ldk;                   // their bytes
   mhc_linear_launch px, pw;      // the products over G
-  int64_t x, w, stats, target, lse2, rows, shares, inverse, held, part, sum_x, sum_w, total;  // places
+  int64_t x, w, stats, target, whole, rows, shares, inverse, held, part, sum_x, sum_w, total;  // places
 };
 
 // Rows of a chunk: as many as the held values' bytes allow, evenly, in whole tiles.
@@ -565,7 +567,7 @@ mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
     // the launch that the policy chose may go through the medium tiles, whose groups are as wide
     p.stats = at.take(mul_bytes(p.groups, p.chunk, sizeof(Stat)));
     p.target = at.take(mul_bytes(p.chunk, 4, 1));
-    p.lse2 = at.take(mul_bytes(p.chunk, 4, 1));
+    p.whole = at.take(mul_bytes(p.chunk, sizeof(Stat), 1));
     p.rows = at.take(mul_bytes(M, 4, 1));
   }
   if (mode != kFwd) {
@@ -726,7 +728,7 @@ hipError_t launch_stats(const Call& c, const Plan& p, const void* x, const void*
   float* const loss = c.reduction == MHC_REDUCTION_NONE ? c.loss : reinterpret_cast<float*>(c.ws + p.rows);
   const auto run = [&](auto kernel, int64_t r) {
     return launch_kernel(kernel, dim3(static_cast<uint32_t>(ceil_div(rows, r))), dim3(1024), s, nullptr,
-                         nullptr, stats, target, targets, c.lse + row0, reinterpret_cast<float*>(c.ws + p.lse2),
+                         nullptr, stats, target, targets, c.lse + row0, reinterpret_cast<Stat*>(c.ws + p.whole),
                          loss + row0, rows, c.V,
                          p.groups, up_of(p), along_of(p, rows), c.ignore_index);
   };
@@ -834,7 +836,7 @@ hipError_t launch_all(const Call& c, const Plan& p, hipStream_t s, hipEvent_t st
         const int64_t segment = 128 * (pieces < 1 ? 1 : pieces > 16 ? 16 : pieces);
         e = launch_kernel(ce_grad_kernel<F>, dim3(static_cast<uint32_t>(ceil_div(c.V, segment)), static_cast<uint32_t>(high)),
                           dim3(256), s, nullptr, nullptr, reinterpret_cast<const Stat*>(c.ws + p.stats),
-                          reinterpret_cast<const float*>(c.ws + p.lse2), shares + row0, c.targets + row0,
+                          reinterpret_cast<const Stat*>(c.ws + p.whole), shares + row0, c.targets + row0,
                           reinterpret_cast<S*>(c.ws + p.held), rows, c.V, p.ld, segment, p.group_bits, up_of(p), along_of(p, rows));
       }
     }

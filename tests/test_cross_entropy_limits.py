@@ -33,15 +33,25 @@ def product(a, b):
     return (a[:, :, None] * b[None]).sum(1)
 
 
+def fp32(v):
+    """fp64 values whose overflows are fp32's."""
+    return torch.where(v.abs() > torch.finfo(torch.float32).max, torch.sign(v) * math.inf, v)
+
+
 def formula(x, w, targets, s, e=None):
     """(lse, each row's loss, G, a p), fp64, of logits as fp32 has them."""
     z = product(x.double(), w.double().t())
-    z = torch.where(z.abs() > 3.4028235e38, torch.sign(z) * math.inf, z)
-    lse = torch.logsumexp(z, 1)
+    z = fp32(z)
+    # from the largest on, since 64 bits hold 2.55e38 in steps of 2^75
+    top = z.amax(1, keepdim=True)
+    d = torch.where((z == top) & torch.isfinite(z), torch.zeros_like(z), z - top)
+    some = torch.where(torch.isinf(top), torch.zeros_like(top), torch.log(torch.exp(d).sum(1, keepdim=True)))
+    lse = (top + some)[:, 0]
     rows = torch.arange(len(x))
-    each = torch.where(targets != IGNORE, lse - z[rows, targets.clamp(0)], torch.zeros_like(lse))
+    each = torch.where(targets != IGNORE, some[:, 0] - (z - top)[rows, targets.clamp(0)], torch.zeros_like(lse))
+    each = fp32(torch.where(torch.isinf(lse) & (targets != IGNORE), lse - z[rows, targets.clamp(0)], each))
     a = s if e is None else s + e
-    ap = a[:, None] * torch.exp(z - lse[:, None])
+    ap = a[:, None] * torch.exp(d - some)
     g = ap.clone()
     g[rows, targets.clamp(0)] -= s
     g[(a == 0) & (s == 0)] = 0
@@ -142,3 +152,53 @@ def test_infinite_logits_have_the_formula_s_gradients(device, kind, case, kernel
         assert torch.isnan(g).any()
         check(one, x, w, g, ap, w.dtype, True, 1.5)
         check(two, x, w, g, ap, w.dtype, False, 1.5)
+
+
+# ---------------------------------------------------------------------------
+# Finite logits of any size
+# ---------------------------------------------------------------------------
+
+def large(kind, k, sign, M, V):
+    """Logits of 2^(24 + k) to 2^(25 + k), another in each row, and within a row apart by multiples of their own step."""
+    x, w = torch.zeros(M, 8, dtype=TYPES[kind]), torch.zeros(V, 8, dtype=TYPES[kind])
+    x[:, 0], w[:, 0] = (128.0 + torch.arange(M) * 37 % 128) * 32, sign * 2.0 ** (12 + k)
+    x[:, 3], w[:, 3] = 2.0 ** (1 + k), -(torch.arange(V) * 7 % 13).float()
+    targets = torch.arange(M) * 11 % V
+    s = torch.linspace(0.5, 1.5, M, dtype=torch.float64)
+    s[::2] *= -1
+    return x, w, targets, s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_large_logits(device, kind, kernel):
+    """A row's probabilities are those of its differences, which are exact however large the logits are."""
+    M, V = (16, 150) if kernel == ROWS else (100, 300)
+    for k in range(4):
+        for sign in (1, -1):
+            say(f"large logits {kind} kernel={kernel} k={k} sign={sign}")
+            x, w, targets, s = large(kind, k, sign, M, V)
+            assert float(product(x.double(), w.double().t()).abs().max()) < 2.0 ** (26 + k)
+            lse, each, g, ap = formula(x, w, targets, s)
+            value, made, one, _ = calls(device, x, w, targets, s, kernel)
+            R.assert_within(made, lse, lse.abs() * 2 * R.U32 + REL, "lse")
+            R.assert_within(value, each, each.abs() * 4 * R.U32 + REL, "loss")
+            check(one, x, w, g, ap, w.dtype, True, 1.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_logits_whose_product_with_log2_e_has_no_place_in_fp32(device, kernel):
+    M, V = (7, 150) if kernel == ROWS else (70, 150)
+    say(f"logits of 2.55e38 kernel={kernel}")
+    x, w = torch.zeros(M, 8, dtype=BF16), torch.zeros(V, 8, dtype=BF16)
+    x[::2, 0], x[1::2, 0] = 2.0 ** 64, -2.0 ** 64
+    w[::3, 0], w[1::5, 0] = 1.5 * 2.0 ** 63, -1.5 * 2.0 ** 63
+    targets, s = torch.arange(M) * 3 % V, torch.linspace(0.5, 1.5, M, dtype=torch.float64)
+    lse, each, g, ap = formula(x, w, targets, s)
+    assert torch.isfinite(lse).all() and float(lse.max()) > 2.5e38
+    value, made, one, two = calls(device, x, w, targets, s, kernel)
+    R.assert_within(made, lse, lse.abs() * 2 * R.U32 + REL, "lse")
+    R.assert_within(value, each, each.abs() * 4 * R.U32 + REL, "loss")
+    check(one, x, w, g, ap, BF16, True, 1.5)
