@@ -364,7 +364,9 @@ __global__ __launch_bounds__(kOneBlock) void ce_total_kernel(const float* __rest
 }
 
 // The rows' shares and, for fp16 (`narrow`), the power of two that brings the
-// largest to [2^14, 2^15), by which they are scaled, and its inverse.
+// largest G that they allow to [2^14, 2^15), by which they are scaled, and its inverse.
+// G is a p or, at the target, a p - b, with p from 0 to 1: at most |a|, |b| or |a - b|,
+// which is twice either where grad_lse is twice -s.
 __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
     const int64_t* __restrict__ targets, const float* __restrict__ grad_loss,
     const float* __restrict__ grad_lse, Share* __restrict__ shares, float* __restrict__ inverse,
@@ -390,7 +392,7 @@ __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
 #pragma unroll 4
     for (int64_t m = threadIdx.x; m < M; m += kOneBlock) {
       const Share w = share(m);
-      most = fmaxf(most, fmaxf(fabsf(w.a), fabsf(w.b)));
+      most = fmaxf(most, fmaxf(fmaxf(fabsf(w.a), fabsf(w.b)), fabsf(w.a - w.b)));
     }
     most = block_max<kOneBlock>(most, part[2]);
   }

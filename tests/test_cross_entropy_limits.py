@@ -202,3 +202,31 @@ def test_logits_whose_product_with_log2_e_has_no_place_in_fp32(device, kernel):
     R.assert_within(made, lse, lse.abs() * 2 * R.U32 + REL, "lse")
     R.assert_within(value, each, each.abs() * 4 * R.U32 + REL, "loss")
     check(one, x, w, g, ap, BF16, True, 1.5)
+
+
+# ---------------------------------------------------------------------------
+# Shares
+# ---------------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("factor", [1.0, 2.0 ** -13, 512.0])
+def test_a_target_s_two_shares_of_opposite_signs(device, kind, factor):
+    """At its target a row's G is a p - s with a = s + grad_lse: as large as both together where they differ in sign."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    M, V, t = 40, 150, TYPES[kind]
+    x, w = torch.zeros(M, M + 1, dtype=t), torch.zeros(V, M + 1, dtype=t)
+    targets = torch.arange(M) * 11 % V
+    rows = torch.arange(M)
+    x[rows, rows], w[targets, rows] = 8.0, 8.0             # each target's probability is nearly 1
+    x[:, M], w[:, M] = rows % 3 - 1.0, torch.arange(V) % 5 * 0.25
+    for s0, e0 in ((-1.9999, 3.9998), (1.9999, -3.9998), (1.0, -1.0), (0.0, 1.9999)):
+        say(f"shares {kind} s={s0 * factor} grad_lse={e0 * factor}")
+        s = (torch.linspace(0.25, 1.0, M) * s0 * factor).float()
+        e = (torch.linspace(0.25, 1.0, M) * e0 * factor).float()
+        lse, _, g, ap = formula(x, w, targets, s.double(), e.double())
+        gx, gw = torch.empty_like(x, device=device), torch.empty_like(w, device=device)
+        C.mhc_cross_entropy_bwd(x.to(device), w.to(device), targets.to(device), lse.float().to(device), s.to(device),
+                                grad_lse=e.to(device), grad_x=gx, grad_weight=gw, reduction="none")
+        torch.cuda.synchronize()
+        check((gx, gw), x, w, g, ap, t, False, 4 * factor)
