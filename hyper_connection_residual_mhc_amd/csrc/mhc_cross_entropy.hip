@@ -257,7 +257,9 @@ struct RowStatEpilogue {
 };
 
 // Epilogue of the logits made again: G itself, from the rows' lse and shares.
-// Columns V.. of the last piece of a row are zeros (W has no such rows).
+// Columns V.. of the last piece of a row are zeros (W has no such rows). z - lse is
+// at most 0: a rounding of either to the other side (half a step of 1e8 is 4) would
+// make a probability of e^4, past all that the shares' scale leaves room for.
 struct GradEpilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true;
@@ -278,7 +280,8 @@ struct GradEpilogue {
       const bool none = w.a == 0.0f && w.b == 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float p = exp_of(v[e], l) * w.a;
+        const float d = v[e] - l;
+        const float p = __builtin_amdgcn_exp2f((d > 0.0f ? 0.0f : d) * kLog2E) * w.a;
         v[e] = none || n + e >= V ? 0.0f : t == e ? p - w.b : p;
       }
       Chunk<F> c;

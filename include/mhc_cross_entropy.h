@@ -29,7 +29,8 @@
  * is read for it.
  *
  * mhc_cross_entropy_fwd gives loss and lse. mhc_cross_entropy_bwd gives the
- * gradients from lse and makes the logits again; it also takes grad_lse (fp32
+ * gradients from lse and makes the logits again (where lse was rounded below one of them, z - lse
+ * counts as 0: no probability passes 1); it also takes grad_lse (fp32
  * [M], may be NULL), the gradient that reaches lse from its other uses:
  * G += grad_lse[m] exp(z - lse), for ignored rows too. mhc_cross_entropy_grads gives loss, lse and
  * gradients in one call, for callers that know grad_loss beforehand, and makes

@@ -230,3 +230,23 @@ def test_a_target_s_two_shares_of_opposite_signs(device, kind, factor):
                                 grad_lse=e.to(device), grad_x=gx, grad_weight=gw, reduction="none")
         torch.cuda.synchronize()
         check((gx, gw), x, w, g, ap, t, False, 4 * factor)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS[1:])
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_no_probability_passes_1(device, kind, kernel):
+    """From lse, which is rounded: below the largest logit by up to half its step, where exp(z - lse) would be e^(1/2) and
+    more, which in fp16's scale is an infinity."""
+    M, V = 100, 300
+    for k in range(4):
+        say(f"large logits from lse {kind} kernel={kernel} k={k}")
+        x, w, targets, s = large(kind, k, 1, M, V)
+        w[1:, 3] -= 13.0                                   # one logit is ahead of all others
+        z = product(x.double(), w.double().t())
+        for lse in (torch.logsumexp(z, 1).float(), z.amax(1).float() - 2.0 ** (1 + k)):
+            ap = s[:, None] * torch.exp((z - lse.double()[:, None]).clamp(max=0.0))
+            g = ap.clone()
+            g[torch.arange(M), targets] -= s
+            *_, two = calls(device, x, w, targets, s, kernel, lse)
+            check(two, x, w, g, ap, w.dtype, False, 1.5)
