@@ -561,7 +561,13 @@ mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
                  : p.logits.kernel == MHC_LINEAR_SMALL || p.logits.kernel == MHC_LINEAR_SHORT ? 5
                                                                                               : 6;
   p.groups = ceil_div(V, 1 << p.group_bits);
-  p.pad = K % 8 != 0 && (M > INT64_MAX / V / K || M * V * K >= kPadBackward);
+  // The loss alone has one product, as the forward of mhc_linear.h, and its rule: at few rows a
+  // copy of W is three times W's bytes (65536 x 7167 in bf16, 8 rows 619 us and 897 MiB of
+  // workspace, so 532 and 0.5; 17 rows 612, 211; 129 rows 638, 404; 16 rows 648, 690). With gradients W is
+  // read turned as well, which through registers costs more than the copy.
+  const bool few = mode == kFwd && (p.logits.kernel == MHC_LINEAR_ROWS || M < kPadRows || V < kPadRows);
+  p.pad = K % 8 != 0 && !few &&
+          (M > INT64_MAX / V / K || M * V * K >= (mode == kFwd ? kPadForward : kPadBackward));
   p.ldk = p.pad ? round_up(K * 2, 16) : K * 2;
   Places at;
   if (p.pad) {
@@ -699,12 +705,13 @@ TileArgs<E> logits_of(const Call& c, const Plan& p, const void* x, const void* w
   return t;
 }
 
-// The row kernel with groups of 8 columns: 16 or 8 rows of W to a block.
+// The row kernel with groups of 8 columns: 16 or 8 rows of W to a block. bytes: of a row that count.
 template <int OP, class E>
-hipError_t launch_row_logits(const TileArgs<E>& t, hipStream_t s, hipEvent_t start) {
+hipError_t launch_row_logits(const TileArgs<E>& t, uint32_t bytes, hipStream_t s, hipEvent_t start) {
   const int64_t wide = t.N > 256 * 8 ? 16 : 8;
+  // padded or not, a row's sum is that of its K values: the loss alone and the loss with gradients agree
   const RowsArgs<E> a = {static_cast<const uint8_t*>(t.x.p), static_cast<const uint8_t*>(t.w.p), nullptr,
-                         nullptr, nullptr, nullptr, t.M, t.N, t.kbytes, static_cast<uint32_t>(wide), t.e};
+                         nullptr, nullptr, nullptr, t.M, t.N, bytes, t.kbytes, static_cast<uint32_t>(wide), t.e};
   return launch_kernel(linear_rows_kernel<OP, 8, E>, dim3(static_cast<uint32_t>(ceil_div(t.N, wide))),
                        dim3(512), s, start, nullptr, a);
 }
@@ -724,7 +731,7 @@ hipError_t launch_stats(const Call& c, const Plan& p, const void* x, const void*
   hipError_t e;
   if (p.logits.kernel == MHC_LINEAR_ROWS) {
     const RowStatEpilogue<HOLD> ep = {stats, target, targets, held, p.ld, p.groups};
-    e = launch_row_logits<OP>(logits_of(c, p, x, w, rows, ep), s, marks->first());
+    e = launch_row_logits<OP>(logits_of(c, p, x, w, rows, ep), static_cast<uint32_t>(c.K * 2), s, marks->first());
   } else {
     const StatEpilogue<HOLD> ep = {stats, target, targets, held, p.ld};
     e = launch_product<OP, false, false>(logits_of(c, p, x, w, rows, ep), p.logits, s, marks->first(), nullptr);

@@ -1351,7 +1351,8 @@ struct RowsArgs {
   const uint8_t* ws;   // kMX
   const uint8_t* ws2;  // kMX of kBoth
   int64_t M, N;
-  uint32_t kbytes;
+  uint32_t kbytes;  // of a row that count, which alone set the order of its sum
+  uint32_t ld;      // from row to row, the same in x and W
   uint32_t wide;  // rows of a weight for each block: at most 16, of kBoth 8
   E e;
 };
@@ -1388,8 +1389,8 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs<E> a) 
   const int64_t wrow = min(n0 + (in_w ? low % kOf : 0), a.N - 1);
   const uint32_t xrow = in_x ? low : 0;
   const uint32_t kblocks = (a.kbytes + 31) / 32;
-  const uint8_t* w = (of_2 ? a.w2 : a.w) + wrow * a.kbytes;
-  const uint8_t* x = a.x + static_cast<int64_t>(xrow) * a.kbytes;
+  const uint8_t* w = (of_2 ? a.w2 : a.w) + wrow * a.ld;
+  const uint8_t* x = a.x + static_cast<int64_t>(xrow) * a.ld;
   const uint8_t* ws = OP == kOpMX ? (of_2 ? a.ws2 : a.ws) + wrow * kblocks : nullptr;
   const uint8_t* xs = OP == kOpMX ? a.xs + static_cast<int64_t>(xrow) * kblocks : nullptr;
   f32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};

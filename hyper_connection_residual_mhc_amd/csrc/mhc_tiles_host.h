@@ -347,7 +347,7 @@ hipError_t launch_rows(const TileArgs<E>& t, hipStream_t s, hipEvent_t start, hi
   const int64_t wide = ceil_div(t.N, 256 * ceil_div(t.N, 256 * most));
   const RowsArgs<E> a = {static_cast<const uint8_t*>(t.x.p), static_cast<const uint8_t*>(t.w.p),
                          static_cast<const uint8_t*>(t.w2.p), t.xs, t.ws, t.ws2, t.M, t.N, t.kbytes,
-                         static_cast<uint32_t>(wide), t.e};
+                         t.kbytes, static_cast<uint32_t>(wide), t.e};
   const dim3 grid(static_cast<uint32_t>(ceil_div(t.N, wide)));
   return launch_kernel(linear_rows_kernel<OP, 8, E>, grid, dim3(512), s, start, stop, a);
 }

@@ -250,3 +250,35 @@ def test_no_probability_passes_1(device, kind, kernel):
             g[torch.arange(M), targets] -= s
             *_, two = calls(device, x, w, targets, s, kernel, lse)
             check(two, x, w, g, ap, w.dtype, False, 1.5)
+
+
+# ---------------------------------------------------------------------------
+# Rows that are no whole pieces
+# ---------------------------------------------------------------------------
+
+def test_the_loss_of_few_rows_copies_no_weight(built_library):
+    """The loss alone, a few rows, K no multiple of 8: its workspace is that of a K that is one."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    for M, V, K in ((1, 131072, 8191), (2, 131072, 8191), (8, 65536, 7161), (16, 65536, 7167), (17, 65536, 7167), (300, 131072, 4095)):
+        odd = C.mhc_cross_entropy_workspace_bytes("fwd", M, V, K, 1)
+        assert odd == C.mhc_cross_entropy_workspace_bytes("fwd", M, V, -(-K // 8) * 8, 1), (M, V, K)
+        assert odd < V * K * 2 // 32
+    # with gradients, and of many rows, the copies pay
+    assert C.mhc_cross_entropy_workspace_bytes("grads", 16, 65536, 7167, 1) > 65536 * 7168 * 2
+    assert C.mhc_cross_entropy_workspace_bytes("fwd", 1024, 65536, 7167, 1) > 65536 * 7168 * 2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,V,K", [(8, 100000, 2047), (16, 50000, 2047), (130, 20000, 1023), (600, 12000, 1023)])
+def test_the_loss_alone_and_with_gradients_agree(device, M, V, K):
+    """Bit for bit, also where W is copied for the gradients and not for the loss alone."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    from test_cross_entropy import check_loss
+    assert C.mhc_cross_entropy_workspace_bytes("grads", M, V, K, 1) > V * (K + 1) * 2
+    say(f"cross entropy of rows that are no whole pieces M={M} V={V} K={K}")
+    gen = torch.Generator(device=device).manual_seed(M)
+    x, w = (torch.randn(r, K, device=device, generator=gen) for r in (M, V))
+    x, w, targets = x.to(BF16), (w * 2 * K ** -0.5).to(BF16), torch.randint(V, (M,), device=device, generator=gen)
+    f, o = C.linear_cross_entropy(x, w, targets), C.linear_cross_entropy_grads(x, w, targets)
+    assert R.same_bytes(f.loss, o.loss) and R.same_bytes(f.lse, o.lse)
+    check_loss(f.loss, f.lse, x.double(), w.double(), targets, "mean", IGNORE)
