@@ -23,6 +23,10 @@
  * only together). act' of an infinite gate is its limit, 0 or 1; the products
  * with it follow fp32's rules (infinity times 0 is NaN).
  *
+ * Where dg and du together pass 2^31 - 1 bytes (4 M times N rounded up to 64: 32768 rows x 16384)
+ * the weights' gradients take about two thirds longer: 32768 x 4096 with 16320
+ * columns 7.4 ms, with 16384 12.4.
+ *
  * The order of a sum depends on M, N, K, the type and the launch shape, on
  * nothing else: a call repeated gives the same bytes. With a launch that names
  * a tile kernel and splits = 1 a row's bytes do not depend on M either.
