@@ -598,6 +598,7 @@ mhc_status make_all(int64_t M, int64_t V, int64_t K, int32_t dtype, int mode,
     const int64_t a = parts(p.chunk, K, p.px), b = parts(V, K, p.pw);
     p.part = at.take(a < 0 || b < 0 ? -1 : a > b ? a : b);
     if (p.piece < V) p.sum_x = at.take(mul_bytes(p.chunk, K, 4));
+    // (more than all logits in 16 bits where K > M / 2; the next chunk's part joins it in fp32)
     if (p.chunk < M) p.sum_w = at.take(mul_bytes(V, K, 4));
   }
   p.total = at.total;

@@ -35,9 +35,17 @@
  * G += grad_lse[m] exp(z - lse), for ignored rows too. mhc_cross_entropy_grads gives loss, lse and
  * gradients in one call, for callers that know grad_loss beforehand, and makes
  * the logits once: of a chunk of rows at a time it keeps exp(z - the largest of
- * 64 neighbours), rounded to fp16, in the workspace (what is below 2^-40 of that
- * largest counts as 0). Chunks of rows hold at
- * most MHC_CROSS_ENTROPY_CHUNK_BYTES of such values (256 rows at least).
+ * its 64 neighbours; of 32 or 8 in the smaller kernels), rounded to fp16, in the workspace
+ * (what is below 2^-40 of that largest counts as 0).
+ *
+ * Workspace. Both calls with gradients hold a chunk of rows of G at a time: at most
+ * MHC_CROSS_ENTROPY_CHUNK_BYTES in 16 bits (or 256 rows). Where M makes several chunks and
+ * grad_weight is a sum over them, its V K fp32 values are held too, which may be more than the
+ * logits in 16 bits: with V = 131072 and K = 4096 1.06 GiB at 4096 rows (one chunk),
+ * 2.74 at 4097, and up to 3.1 however large M is. A weight past 2^31 bytes
+ * adds a chunk's M K fp32 values of grad_x, and rows along K that are no multiple of 16
+ * bytes copies of x and W where they pay. The loss alone needs 8 bytes for each row
+ * and 64 columns (32, 8) of a chunk, and such copies for many rows.
  *
  * The order of a sum depends on M, V, K, the type and the launch shape, on
  * nothing else: a call repeated gives the same bytes.

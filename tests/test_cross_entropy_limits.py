@@ -268,6 +268,18 @@ def test_the_loss_of_few_rows_copies_no_weight(built_library):
     assert C.mhc_cross_entropy_workspace_bytes("fwd", 1024, 65536, 7167, 1) > 65536 * 7168 * 2
 
 
+def test_workspaces_are_what_the_header_says(built_library):
+    """One chunk of G, and from the second on the weight's gradient in fp32 as well, however many rows."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    V, K, gib = 131072, 4096, 2.0 ** 30
+    of = {M: [C.mhc_cross_entropy_workspace_bytes(call, M, V, K, 1) / gib for call in ("fwd", "bwd", "grads")]
+          for M in (4096, 4097, 8192, 65536, 1 << 20)}
+    assert of[4096] == pytest.approx([0.0625, 1.0, 1.0625], abs=0.001)
+    assert of[4097][2] == pytest.approx(2.74, abs=0.01)
+    for M in (8192, 65536, 1 << 20):
+        assert of[M][0] < 0.07 and 3.0 <= of[M][1] < 3.1 and 3.0 < of[M][2] < 3.1
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,V,K", [(8, 100000, 2047), (16, 50000, 2047), (130, 20000, 1023), (600, 12000, 1023)])
 def test_the_loss_alone_and_with_gradients_agree(device, M, V, K):
