@@ -309,7 +309,11 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // brings zeros (the check counts `at` too). No vector register is written; the
 // loads are waited for by wait_tiles(). m0 is a reserved register, which a list
 // of clobbers cannot name: nothing else in this library may use it (a test
-// reads the machine code for that).
+// reads the machine code for that). A vector instruction that writes a scalar
+// register (a readfirstlane, or the compiler's own readlane of a spilled one) has
+// to stand five wait states ahead of a load that reads it. The compiler keeps that
+// distance for its own loads and not for these: where it might not be there, safe_load
+// waits, and a test reads the machine code of all of them.
 template <int BYTES>
 __device__ __forceinline__ void load_to_lds(uint32_t offset, i32x4 rsrc, uint32_t at, uint32_t to) {
   if constexpr (BYTES == 16)
@@ -330,6 +334,14 @@ __device__ __forceinline__ void set_place(uint32_t to) {
 }
 __device__ __forceinline__ void load_to_place(uint32_t offset, i32x4 rsrc, uint32_t at) {
   asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds"
+               :
+               : "v"(offset), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(at))
+               : "memory");
+}
+
+// The same, after the wait states that the buffer and `at` may need, and m0.
+__device__ __forceinline__ void safe_load(uint32_t offset, i32x4 rsrc, uint32_t at) {
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :
                : "v"(offset), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(at))
                : "memory");
@@ -492,10 +504,12 @@ struct Operand {
     p.at = TURNED ? kt * (kTileK / ELEM) * ld : kt * kTileK;
     return p;
   }
+  template <bool SAFE = false>
   __device__ __forceinline__ void load(const Pass& p, int q) const {
     const bool second = W == kBoth && q * kEach >= kRows;
     const uint32_t rows = q * kEach - (second ? kRows : 0);
-    load_to_place(p.offset, second ? rsrc2 : p.from, p.at + rows * ld);
+    if constexpr (SAFE) safe_load(p.offset, second ? rsrc2 : p.from, p.at + rows * ld);
+    else load_to_place(p.offset, second ? rsrc2 : p.from, p.at + rows * ld);
   }
 
   // Through registers: writes the loaded tile.
@@ -1205,14 +1219,15 @@ __global__ __launch_bounds__(256, 1) void linear_wide_kernel(TileArgs<E> a) {
     if (k < 8) lx.load(px, k);
     else lw.load(pw, k - 8);
   };
+  // the block's first loads, whose addresses are only just made
   const auto load_all = [&](uint32_t b) {
     const auto px = lx.pass(ahead);
     const auto pw = lw.pass(ahead);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       set(b, k);
-      asm volatile("s_nop 0");
-      load(px, pw, k);
+      if (k < 8) lx.template load<true>(px, k);
+      else lw.template load<true>(pw, k - 8);
     }
   };
   load_all(0);
