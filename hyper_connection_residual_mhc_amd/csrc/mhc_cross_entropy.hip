@@ -90,7 +90,7 @@ struct Share {
 template <bool HOLD>
 struct StatEpilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 2;
-  static constexpr bool kSplits = false, kHalves = false, kTakes = true, kWrites = false;
+  static constexpr bool kSplits = false, kHalves = false, kTakes = true, kWrites = false, kEarly = false;
   Stat* stats;
   float* target_logit;     // [rows]: written where a target is among the columns
   const int64_t* targets;  // [rows]
@@ -219,7 +219,7 @@ struct StatEpilogue {
 template <bool HOLD>
 struct RowStatEpilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 0;
-  static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true, kEarly = false;
   Stat* stats;
   float* target_logit;
   const int64_t* targets;
@@ -262,7 +262,7 @@ struct RowStatEpilogue {
 // make a probability of e^4, past all that the shares' scale leaves room for.
 struct GradEpilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 0;
-  static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = false, kHalves = false, kTakes = false, kWrites = true, kEarly = false;
   const float* lse;        // [rows]
   const Share* shares;     // [rows]
   const int64_t* targets;  // [rows]
@@ -456,7 +456,7 @@ __global__ void ce_fill_kernel(float* p, float v) { *p = v; }
 // fp32, in ascending order, and rounded once, with the shares' scale taken back.
 struct SumEpilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 0;
-  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true, kEarly = false;
   void* out;
   float* sum;            // where there are several
   const float* inverse;  // of the scale

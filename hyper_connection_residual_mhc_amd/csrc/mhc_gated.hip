@@ -27,7 +27,7 @@ namespace {
 
 struct GatedEpilogue {
   static constexpr int kW = kBoth, kSums = 2, kGroup = 0;
-  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true, kEarly = false;
   const void* gate_bias;
   const void* up_bias;
   void* out;

@@ -19,7 +19,7 @@ namespace {
 // Epilogue: scales, bias, activation and residual.
 struct Epilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 0;
-  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true, kEarly = true;
   const void* bias;
   const void* residual;
   void* out;
@@ -33,10 +33,23 @@ struct Epilogue {
   __device__ __forceinline__ void with(const Fn& fn) const;
 };
 
-// Columns [n, n + count) of row m, count <= 8, from the sums over k.
-template <int OP, int ACT>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int64_t n, int count,
-                                       float (&v)[8]) {
+// The values as they are, in fp32: an instruction that multiplies and rounds to fp16 at
+// once, which the compiler takes at the end of a wide tile and nowhere else, rounds once
+// where a product in fp32 and its conversion round twice, and a row is to be the same
+// from every kernel, bit for bit (elsewhere this would keep loops from being unrolled).
+template <int F>
+__device__ __forceinline__ void in_fp32(float (&v)[8]) {
+  if constexpr (F == kF16) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("" : "+v"(v[i]));
+  }
+}
+
+// Columns [n, n + count) of row m, count <= 8, from the sums over k; bias_of() and
+// residual_of() bring those chunks, where there are any. FENCE: see in_fp32.
+template <int OP, int ACT, bool FENCE, class B, class R>
+__device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int64_t n, int count, float (&v)[8],
+                                       const B& bias_of, const R& residual_of) {
   constexpr int F = out_format(OP);
   typedef typename Store<F>::type S;
   float b[8];
@@ -47,33 +60,46 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int64_t n, 
     for (int i = 0; i < 8; ++i) v[i] = sum_value<OP>(v[i]) * (xs * b[i]);
   }
   if (e.bias != nullptr) {
-    widen_chunk<F>(load_chunk<F>(static_cast<const S*>(e.bias) + n, count), b);
+    widen_chunk<F>(bias_of(), b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
   }
   Chunk<F> c;
   if (e.z != nullptr) {
+    if constexpr (FENCE) in_fp32<F>(v);
     narrow_chunk<F>(v, c);
     store_chunk<F>(static_cast<S*>(e.z) + m * e.N + n, count, c);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
   if (e.residual != nullptr) {
-    widen_chunk<F>(load_chunk<F>(static_cast<const S*>(e.residual) + m * e.N + n, count), b);
+    widen_chunk<F>(residual_of(), b);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = v[i] + b[i];
   }
+  if constexpr (FENCE) in_fp32<F>(v);
   narrow_chunk<F>(v, c);
   store_chunk<F>(static_cast<S*>(e.out) + m * e.N + n, count, c);
 }
 
+template <int OP, int ACT>
+struct Finish {
+  static constexpr int F = out_format(OP);
+  typedef typename Store<F>::type S;
+  const Epilogue& e;
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, int count, float (&v)[8]) const {
+    finish<OP, ACT, false>(e, m, n, count, v, [&] { return load_chunk<F>(static_cast<const S*>(e.bias) + n, count); },
+                           [&] { return load_chunk<F>(static_cast<const S*>(e.residual) + m * e.N + n, count); });
+  }
+  __device__ __forceinline__ void operator()(int64_t m, int64_t n, int count, float (&v)[8], const u32x4& bias,
+                                             const u32x4& residual) const {
+    finish<OP, ACT, true>(e, m, n, count, v, [&] { return Chunk<F>{{bias}}; }, [&] { return Chunk<F>{{residual}}; });
+  }
+};
+
 template <int OP, class Fn>
 __device__ __forceinline__ void Epilogue::with(const Fn& fn) const {
-  with_act(act, [&](auto a) {
-    fn([&](int64_t m, int64_t n, int count, float(&v)[8]) {
-      finish<OP, decltype(a)::value>(*this, m, n, count, v);
-    });
-  });
+  with_act(act, [&](auto a) { fn(Finish<OP, decltype(a)::value>{*this}); });
 }
 
 typedef TileArgs<Epilogue> Args;

@@ -281,7 +281,9 @@ struct TileShape {
 //            the rows of the second one's results come after the M of the first;
 //   kTakes   e.take() has the sums in their registers first;
 //   kWrites  e.with<OP>(f) calls f(finish), and finish(m, n, count, v) gets up to 8
-//            consecutive columns of a row, v[8 s ...] those of sum s.
+//            consecutive columns of a row, v[8 s ...] those of sum s;
+//   kEarly   finish reads e.bias, of the columns, and e.residual, both of 16 bits and each
+//            absent where it is null, and also takes them loaded (see write_early).
 template <class E>
 struct TileArgs : TileShape {
   E e;
@@ -635,6 +637,87 @@ __device__ __forceinline__ void each_of(int k, const F& f) {
   else each_of<N - 1>(k, f);
 }
 
+// The 8 values of 16 bits behind the first `back` (0 to 7) of v.
+__device__ __forceinline__ u32x4 values_behind(u32x4 v, int back) {
+  v = (back & 4) != 0 ? u32x4{v[2], v[3], 0, 0} : v;
+  v = (back & 2) != 0 ? u32x4{v[1], v[2], v[3], 0} : v;
+  const u32x4 half = {__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+                      __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
+  return (back & 1) != 0 ? half : v;
+}
+
+// The results of a wide tile, with what the epilogue reads on its way before it is
+// needed: one wave to a SIMD has no other to wait under. A lane's columns are the
+// same in every row, so their bias is loaded once; a row's residual (ROWS) is loaded as
+// soon as the one of the step before is used, a step ahead, without a branch, since one
+// around a load in a loop is a wait for it: past the last row from there, and a row's
+// short last chunk from the 8 values that end there. The last step starts no load, and
+// all are used by name: one on its way there would be waited for in the next tile's passes.
+// Waited for chunk by chunk they took 5 us of a tile's end (a bias) and 11 (a residual):
+// 8192 x 8192 x 512 with both 148 us, so 96 (eight waves of 128 x 64: 130).
+template <int OP, bool ROWS, int TI, int TJ, int WN, class E>
+__device__ __forceinline__ void write_early(const TileArgs<E>& a, const Place& at, uint8_t* lds,
+                                            f32x4 (&acc)[TI][TJ]) {
+  static_assert(TJ == 8 && E::kSums == 1 && E::kSplits && !E::kHalves && out_format(OP) != kF32,
+                "a row of 128 columns in 16 lanes");
+  constexpr int G = group_of<E>(TJ), kCols = TJ * 16, kChunks = 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = threadIdx.x % 64, low = lane % 16, g = lane / 16;
+  const int64_t m0 = at.m0 + (wave / WN) * (TI * 16), n = at.n0 + (wave % WN) * kCols + low * 8;
+  float* const mine = reinterpret_cast<float*>(lds) + wave * (16 * kCols);
+  const auto place = [](uint32_t row, uint32_t col) { return row * kCols + (col ^ (row % 8 * 4)); };
+  uint32_t to[TJ];
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+    to[j] = lds_address(mine) + place(low, (j / G) * (16 * G) + g * (4 * G) + (j % G) * 4) * 4;
+  // lane (g, low) has columns n.. of rows g, g + 4, g + 8 and g + 12 of a step
+  const bool whole = at.m0 + 256 <= a.M && at.n0 + 256 <= a.N;
+  const int count = whole || n + 8 <= a.N ? 8 : n < a.N ? static_cast<int>(a.N - n) : 0;
+  const int back = count > 0 ? 8 - count : 0;
+  const int64_t from = count > 0 ? n - back : 0;
+  // (a wave whose rows are all past the last reads the last one)
+  const int64_t m_first = min(m0, a.M - 1);
+  const uint8_t* const base = static_cast<const uint8_t*>(a.e.residual) + m_first * a.N * 2;
+  const uint32_t ld = static_cast<uint32_t>(a.N * 2), column_at = static_cast<uint32_t>(from * 2);
+  const uint32_t last = static_cast<uint32_t>(min(a.M - 1 - m_first, static_cast<int64_t>(TI * 16 - 1))) * ld;
+  u32x4 rows[kChunks] = {};
+  const auto load = [&](int step, int k) {
+    const uint32_t row = min((g + step * 16 + k * 4) * ld, last);
+    rows[k] = *reinterpret_cast<const u32x4_at2*>(base + (row + column_at));
+  };
+  u32x4 bias = {0, 0, 0, 0};
+  if (a.e.bias != nullptr) bias = *reinterpret_cast<const u32x4_at2*>(static_cast<const uint8_t*>(a.e.bias) + from * 2);
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) load(0, k);
+    asm volatile("" : : "v"(rows[0]), "v"(rows[1]), "v"(rows[2]), "v"(rows[3]));
+  }
+  asm volatile("" : : "v"(bias));
+  if (!whole) bias = values_behind(bias, back);
+  a.e.template with<OP>([&](const auto& finish) {
+    const auto one = [&](int step, auto more) {
+      each_of<TI>(step, [&](auto i) { put_row(acc[i], to); });
+      wave_sync();
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const uint32_t row = g + 4 * k;
+        const f32x4 p = *reinterpret_cast<const f32x4*>(mine + place(row, low * 8));
+        const f32x4 q = *reinterpret_cast<const f32x4*>(mine + place(row, low * 8 + 4));
+        float v[8] = {p[0], p[1], p[2], p[3], q[0], q[1], q[2], q[3]};
+        if constexpr (ROWS) asm volatile("" : : "v"(rows[k]));
+        const int64_t m = m0 + step * 16 + row;
+        if (whole) finish(m, n, 8, v, bias, rows[k]);
+        else if (count > 0 && m < a.M) finish(m, n, count, v, bias, values_behind(rows[k], back));
+        if constexpr (decltype(more)::value) load(step + 1, k);
+      }
+      wave_sync();
+    };
+#pragma unroll 1
+    for (int step = 0; step < (ROWS ? TI - 1 : TI); ++step) one(step, std::bool_constant<ROWS>());
+    if constexpr (ROWS) one(TI - 1, std::false_type());
+  });
+}
+
 // The tile's results, written. Lane l of wave (wm, wn) holds in acc[i][j] four
 // consecutive columns of row 16 i + l % 16 of the wave's part; over the G tiles
 // of a group they are 4 G consecutive ones. LDS: SIZE bytes.
@@ -661,6 +744,12 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
   const auto place = [](uint32_t row, uint32_t col) { return row * kWide + (col ^ (row % 8 * 4)); };
   const bool whole = at.m0 + BM <= a.M && at.n0 + BN / kSums <= a.N;
   const int64_t top = at.second ? a.M : 0;  // rows in front of this half's
+  if constexpr (TJ == 8 && E::kEarly) {
+    if (a.splits == 1) {
+      if (a.e.residual != nullptr) return write_early<OP, true, TI, TJ, WN>(a, at, lds, acc);
+      return write_early<OP, false, TI, TJ, WN>(a, at, lds, acc);
+    }
+  }
   constexpr bool kByName = TJ == 8;  // one copy of all that follows, and a step's results by name
   constexpr int kCopies = kByName ? 1 : kSteps;
   uint32_t to[TJ];
@@ -719,7 +808,7 @@ __device__ __forceinline__ void write_tile(const TileArgs<E>& a, const Place& at
           store_chunk<kF32>(partial + (s * rows + m) * a.N + n, count, c);
         }
       });
-    } else {
+    } else if constexpr (!(kByName && E::kEarly)) {
       a.e.template with<OP>([&](const auto& finish) { each(finish); });
     }
     wave_sync();
@@ -1493,7 +1582,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(RowsArgs<E> a) 
 template <int W, bool HALVES>
 struct StoreEpilogue {
   static constexpr int kW = W, kSums = 1, kGroup = 0;
-  static constexpr bool kSplits = true, kHalves = HALVES, kTakes = false, kWrites = true;
+  static constexpr bool kSplits = true, kHalves = HALVES, kTakes = false, kWrites = true, kEarly = false;
   void* out;
   void* out2;
   int64_t M, N;

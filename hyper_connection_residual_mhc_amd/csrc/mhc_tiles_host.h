@@ -287,11 +287,15 @@ hipError_t launch_medium(const TileArgs<E>& a, hipStream_t s, hipEvent_t start, 
 
 constexpr uint32_t kUnits = 256;  // compute units: blocks of the wide kernel at once
 
-// The large tiles are loaded straight into LDS only; other operands go through
-// the medium tiles, whose sums have the same order.
+// The large tiles are loaded straight into LDS only; other operands, and results of
+// hardly any or of very many columns, go through the medium tiles, whose sums have
+// the same order.
 template <int OP, bool TX, bool TW, class E>
 hipError_t launch_large(TileArgs<E> a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
   if (!straight<OP, TX, TW>(a)) return launch_medium<OP, TX, TW>(a, s, start, stop);
+  // write_early reads 8 values of a row at a time, and 128 rows within 2^30 bytes
+  if (wide_tiles(OP) && E::kEarly && (a.N < 8 || a.N > (1 << 22)))
+    return launch_medium<OP, TX, TW>(a, s, start, stop);
   const dim3 grid = tile_grid<256, 256>(a);
   if constexpr (wide_tiles(OP))
     return launch_kernel(linear_wide_kernel<OP, TX, TW, E>, dim3(grid.x < kUnits ? grid.x : kUnits),
