@@ -41,7 +41,7 @@ struct Stat {
 // terms, at most 2^15 (the largest logit's is just that, whatever fp32 makes of
 // m - 15), in fp16, of either type of x: fp16's rounding is an eighth of
 // bf16's, which G then adds (held in bf16 the gradients at 4096 x 131072 x 4096 were
-// 0.0027 off by the norm, so 0.0024; the output's own rounding is 0.0017). What is 2^-29
+// 0.0027 off by the norm, so 0.0024, with a mean's factor still in G). What is 2^-29
 // of a group's largest is a normal number, and what is below 2^-40 of it counts as 0.
 constexpr float kHeld = 15.0f;
 
@@ -366,10 +366,15 @@ __global__ __launch_bounds__(kOneBlock) void ce_total_kernel(const float* __rest
   if (threadIdx.x == 0) loss[0] = mean ? sum / (high * 4096.0f + low) : sum;
 }
 
-// The rows' shares and, for fp16 (`narrow`), the power of two that brings the
-// largest G that they allow to [2^14, 2^15), by which they are scaled, and its inverse.
-// G is a p or, at the target, a p - b, with p from 0 to 1: at most |a|, |b| or |a - b|,
-// which is twice either where grad_lse is twice -s.
+// The rows' shares, and what they were divided by, which the products' sums take back.
+// For a sum or a mean that is |s|, which all rows have alike: left in, its rounding would
+// be in every target's G, and not a random part of it (bf16 has 1 / 3870 off by 0.0035, and
+// the gradients at 4096 x 131072 x 4096 were 0.0024 to 0.0042 off by the norm with C,
+// 0.0028 at 3890, so 0.0019; the output's own rounding is 0.0017). It stays in where
+// grad_lse would be more than 2^10 of it. For fp16 (`narrow`) then the power of two that
+// brings the largest G that the shares allow to [2^14, 2^15): G is a p or, at the target,
+// a p - b, with p from 0 to 1, so at most |a|, |b| or |a - b|, which is twice either where
+// grad_lse is twice -s.
 __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
     const int64_t* __restrict__ targets, const float* __restrict__ grad_loss,
     const float* __restrict__ grad_lse, Share* __restrict__ shares, float* __restrict__ inverse,
@@ -390,24 +395,31 @@ __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
     const float s = t == ignore_index ? 0.0f : t >= 0 && t < V ? g / over : NAN;
     return Share{grad_lse == nullptr ? s : s + grad_lse[m], s};
   };
+  float unit = 1.0f;
+  if (reduction != MHC_REDUCTION_NONE) {
+    const float s = fabsf((grad_loss == nullptr ? 1.0f : grad_loss[0]) / over);
+    if (s >= 0x1p-100f && s < INFINITY) unit = s;
+  }
   float most = 0.0f;
-  if (narrow) {
+  if (narrow || grad_lse != nullptr) {
 #pragma unroll 4
     for (int64_t m = threadIdx.x; m < M; m += kOneBlock) {
       const Share w = share(m);
       most = fmaxf(most, fmaxf(fmaxf(fabsf(w.a), fabsf(w.b)), fabsf(w.a - w.b)));
     }
     most = block_max<kOneBlock>(most, part[2]);
+    if (most > 0x1p10f * unit) unit = 1.0f;
   }
   int power = 0;
-  if (most > 0.0f && most < INFINITY) power = 14 - ilogbf(most);
+  most = most / unit;
+  if (narrow && most > 0.0f && most < INFINITY) power = 14 - ilogbf(most);
   power = power > 126 ? 126 : power;
   const float scale = ldexpf(1.0f, power);
   for (int64_t m = threadIdx.x; m < M; m += kOneBlock) {
     const Share w = share(m);
-    shares[m] = {w.a * scale, w.b * scale};
+    shares[m] = {w.a / unit * scale, w.b / unit * scale};
   }
-  if (threadIdx.x == 0) *inverse = ldexpf(1.0f, -power);
+  if (threadIdx.x == 0) *inverse = unit * ldexpf(1.0f, -power);
 }
 
 // held -> G in place: the exponentials under their groups' maxima become the
@@ -453,13 +465,13 @@ __global__ void ce_fill_kernel(float* p, float v) { *p = v; }
 // ---------------------------------------------------------------------------
 
 // Sums over pieces of V (grad_x) or chunks of rows (grad_weight) are added up in
-// fp32, in ascending order, and rounded once, with the shares' scale taken back.
+// fp32, in ascending order, and rounded once, with what the shares were divided by taken back.
 struct SumEpilogue {
   static constexpr int kW = kOne, kSums = 1, kGroup = 0;
   static constexpr bool kSplits = true, kHalves = false, kTakes = false, kWrites = true, kEarly = false;
   void* out;
   float* sum;            // where there are several
-  const float* inverse;  // of the scale
+  const float* inverse;  // what the shares were divided by
   int64_t N;
   int32_t first, last;
 

@@ -21,8 +21,10 @@
  * in the type of x; each output may be NULL (not wanted). A row with s = 0 has
  * G = 0, whatever its logits are (in grad_weight these zeros still meet its row of
  * x: an infinity or a NaN there makes NaN). G is rounded to the 16 bits that the next
- * products read, in fp16 after scaling by a power of two that the products take
- * back, so that neither a mean over many rows nor a small probability underflows.
+ * products read: of a sum or a mean without the factor |grad_loss| or |grad_loss| / C
+ * that all rows share (unless grad_lse passes 2^10 of it), in fp16 after scaling by a power
+ * of two as well; the products' sums take both back, so that neither a mean over many
+ * rows nor a small probability underflows.
  *
  * A target outside [0, V) that is not ignore_index makes its row's loss and
  * gradients NaN (and with them a sum, a mean and grad_weight); nothing outside W

@@ -294,3 +294,33 @@ def test_the_loss_alone_and_with_gradients_agree(device, M, V, K):
     f, o = C.linear_cross_entropy(x, w, targets), C.linear_cross_entropy_grads(x, w, targets)
     assert R.same_bytes(f.loss, o.loss) and R.same_bytes(f.lse, o.lse)
     check_loss(f.loss, f.lse, x.double(), w.double(), targets, "mean", IGNORE)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_the_factor_of_all_rows_is_not_in_g_s_rounding(device, kind, reduction):
+    """256 equal logits: p = 2^-8 and p - 1 = -255/256 are numbers of 8 bits, so that G without its rows' factor is exact,
+    and the gradients are off by their sums and their own rounding alone, whatever 1 / C or grad_loss are."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    t, M, V, K = TYPES[kind], 130, 256, 72
+    gen = torch.Generator().manual_seed(7)
+    targets = torch.arange(M) * 11 % V
+    targets[M - 10:] = IGNORE                              # C = 120: 1 / C is 0.0034 off in bf16
+    rows = torch.arange(M)
+    on = (targets != IGNORE).double()
+    for factor in (None, 1.0 / 3.0, -120.0 / 3870.0):
+        for x, w in ((torch.zeros(M, K, dtype=t), R.normal(gen, V, K, dtype=t)), (R.normal(gen, M, K, dtype=t), torch.zeros(V, K, dtype=t))):
+            say(f"common factor {kind} {reduction} {factor}")
+            g = None if factor is None else torch.tensor(factor, device=device)
+            s = on * (1.0 if factor is None else float(g.cpu().double()))
+            s = s / on.sum() if reduction == "mean" else s
+            G = s[:, None].repeat(1, V) / V
+            G[rows, targets.clamp(0)] -= s
+            o = C.linear_cross_entropy_grads(x.to(device), w.to(device), targets.to(device), g, reduction=reduction)
+            two = C.linear_cross_entropy_backward(x.to(device), w.to(device), targets.to(device), o.lse, g, reduction=reduction)
+            xv, wv = x.double(), w.double()
+            for got in ((o.grad_x, o.grad_weight), two):
+                for p, want, size, long in ((got[0], G @ wv, G.abs() @ wv.abs(), V), (got[1], G.t() @ xv, G.t().abs() @ xv.abs(), M)):
+                    tol = size * (additions(long, 32) + 4) * STEP
+                    R.assert_within(p, want, tol + R.rounding(want.abs() + tol, t), "gradient")
