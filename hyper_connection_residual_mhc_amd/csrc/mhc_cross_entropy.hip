@@ -370,8 +370,9 @@ __global__ __launch_bounds__(kOneBlock) void ce_total_kernel(const float* __rest
 // For a sum or a mean that is |s|, which all rows have alike: left in, its rounding would
 // be in every target's G, and not a random part of it (bf16 has 1 / 3870 off by 0.0035, and
 // the gradients at 4096 x 131072 x 4096 were 0.0024 to 0.0042 off by the norm with C,
-// 0.0028 at 3890, so 0.0019; the output's own rounding is 0.0017). It stays in where
-// grad_lse would be more than 2^10 of it. For fp16 (`narrow`) then the power of two that
+// 0.0028 at 3890, so 0.0019; the output's own rounding is 0.0017). Its power of two
+// stays in, so that sums keep their size, and all of it where grad_lse would be more
+// than 2^10 of it. For fp16 (`narrow`) then the power of two that
 // brings the largest G that the shares allow to [2^14, 2^15): G is a p or, at the target,
 // a p - b, with p from 0 to 1, so at most |a|, |b| or |a - b|, which is twice either where
 // grad_lse is twice -s.
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(kOneBlock) void ce_shares_kernel(
     most = block_max<kOneBlock>(most, part[2]);
     if (most > 0x1p10f * unit) unit = 1.0f;
   }
-  int power = 0;
+  int power = narrow ? 0 : ilogbf(unit);
   most = most / unit;
   if (narrow && most > 0.0f && most < INFINITY) power = 14 - ilogbf(most);
   power = power > 126 ? 126 : power;

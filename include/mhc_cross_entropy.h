@@ -22,9 +22,9 @@
  * G = 0, whatever its logits are (in grad_weight these zeros still meet its row of
  * x: an infinity or a NaN there makes NaN). G is rounded to the 16 bits that the next
  * products read: of a sum or a mean without the factor |grad_loss| or |grad_loss| / C
- * that all rows share (unless grad_lse passes 2^10 of it), in fp16 after scaling by a power
- * of two as well; the products' sums take both back, so that neither a mean over many
- * rows nor a small probability underflows.
+ * that all rows share, but for its power of two (unless grad_lse passes 2^10 of it), in fp16
+ * after scaling by another power of two; the products' sums take both back, so that
+ * neither a mean over many rows nor a small probability underflows.
  *
  * A target outside [0, V) that is not ignore_index makes its row's loss and
  * gradients NaN (and with them a sum, a mean and grad_weight); nothing outside W
@@ -57,7 +57,8 @@
  * nothing allocated, calls only enqueue on `stream`. M == 0 is a successful
  * call: a sum is +0.0, a mean NaN, grad_weight +0.0. M < 0 or over 2^31 - 1, V < 1 or over
  * MHC_CROSS_ENTROPY_MAX_V, K < 1 or over MHC_LINEAR_MAX_K, another dtype, an unknown
- * reduction, a launch of MHC_LINEAR_NARROW or with more than one part, a NULL or
+ * reduction, a launch of MHC_LINEAR_NARROW (in the backward of MHC_LINEAR_ROWS too) or with
+ * more than one part, a NULL or
  * misaligned pointer, a workspace that is too small or a size past 64 bits give
  * MHC_ERROR_INVALID_VALUE; any overlap of an output (the workspace is one) with
  * an input or another output MHC_ERROR_ALIASING; with either nothing is

@@ -324,3 +324,23 @@ def test_the_factor_of_all_rows_is_not_in_g_s_rounding(device, kind, reduction):
                 for p, want, size, long in ((got[0], G @ wv, G.abs() @ wv.abs(), V), (got[1], G.t() @ xv, G.t().abs() @ xv.abs(), M)):
                     tol = size * (additions(long, 32) + 4) * STEP
                     R.assert_within(p, want, tol + R.rounding(want.abs() + tol, t), "gradient")
+
+
+@pytest.mark.gpu
+def test_a_mean_of_large_rows_has_sums_of_its_own_size(device):
+    """Rows of 2^126 with one target: their mean is finite where their sum is not, and the products sum it as a mean."""
+    from hyper_connection_residual_mhc_amd import loss as C
+    M, V, K = 70, 40, 16
+    x, w = torch.zeros(M, K, dtype=BF16), torch.zeros(V, K, dtype=BF16)
+    x[:, 3] = 2.0 ** 126
+    targets = torch.full((M,), 5)
+    o = C.linear_cross_entropy_grads(x.to(device), w.to(device), targets.to(device))
+    gx, gw = C.linear_cross_entropy_backward(x.to(device), w.to(device), targets.to(device), o.lse)
+    want = torch.zeros(V, K, dtype=torch.float64)
+    want[:, 3] = 2.0 ** 126 / V
+    want[5, 3] -= 2.0 ** 126
+    # p and p - 1 are rounded to bf16 each, then the mean itself
+    tol = want.abs() * (2 * R.HALF_STEP[BF16] + REL)
+    for got in (o.grad_weight, gw):
+        R.assert_within(got, want, tol, "grad_weight")
+    assert not o.grad_x.any() and not gx.any()
